@@ -11,12 +11,18 @@ Entry points (same names as the C ABI):
   hlq_compress_activation(x, rank)            -> (xbar int8 [Cin, T'], s_x)
   hlq_linear_backward_gx(g_y, w, ...)         -> g_x fp32 [T, Cin]
   hlq_linear_backward_gw(g_y, xbar, s_x, ...) -> g_w fp32 [Cout, Cin]
+  hlq_layer_norm(x, w, b, ...)                -> y, mean, rstd (, x + residual)
+  hlq_layer_norm_backward(g_y, x, ...)        -> g_x, g_weight, g_bias
+  hlq_token_logprobs(logits, targets)         -> logp, lse fp32 [T]
+  hlq_policy_loss(logits, actions, ...)       -> stats, logp, gradient of logits
+  hlq_clip_grad_norm(grads, max_norm, ...)    -> norm and coefficient, grads clipped
   hlq_debug_gx_parts / hlq_debug_gw_parts     -> intermediates for checks
   hlq_workspace_bytes, hlq_read_device_status, hlq_status_string
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -51,6 +57,9 @@ EXPORTS = [
     "hlq_debug_gemm_plan",
     "hlq_debug_wait_timeout",
     "hlq_set_gw_operands", "hlq_get_gw_operands", "hlq_debug_serialize_branches",
+    "hlq_layer_norm", "hlq_layer_norm_backward", "hlq_layer_norm_backward_workspace_bytes",
+    "hlq_token_logprobs", "hlq_policy_loss", "hlq_policy_loss_workspace_bytes",
+    "hlq_clip_grad_norm", "hlq_clip_grad_norm_workspace_bytes",
 ]
 
 _lock = threading.Lock()
@@ -82,6 +91,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, i64, i32, u64, sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                 ctypes.c_uint64, ctypes.c_size_t)
+        f32 = ctypes.c_float
         sig = {
             "hlq_workspace_bytes": (sz, [i32, i64, i64, i64, i32, i32]),
             "hlq_compress_activation": (i32, [P, i32, i64, i64, i32, i32, i32, P,
@@ -129,6 +139,17 @@ def lib() -> ctypes.CDLL:
             "hlq_set_gw_operands": (i32, [i32]),
             "hlq_get_gw_operands": (i32, []),
             "hlq_debug_serialize_branches": (i32, [i32]),
+            "hlq_layer_norm": (i32, [P, i64, P, i64, i32, P, P, i32, i64, i64, f32, P, i64,
+                                     i32, P, i64, P, P, P]),
+            "hlq_layer_norm_backward": (i32, [P, i64, i32, P, i64, i32, P, P, P, i32, P, i64,
+                                              i64, i64, P, i64, i32, P, P, P, sz, P]),
+            "hlq_layer_norm_backward_workspace_bytes": (sz, [i64, i64]),
+            "hlq_token_logprobs": (i32, [P, i64, i32, P, i64, i64, f32, P, P, P]),
+            "hlq_policy_loss": (i32, [P, i64, i32, P, P, P, P, P, i64, i64, f32, f32, f32,
+                                      f32, f32, P, P, P, i64, P, sz, P]),
+            "hlq_policy_loss_workspace_bytes": (sz, [i64, i64]),
+            "hlq_clip_grad_norm": (i32, [i64, P, P, P, P, P, f32, P, P, sz, P]),
+            "hlq_clip_grad_norm_workspace_bytes": (sz, [i64]),
             "hlq_status_string": (ctypes.c_char_p, [i32]),
             "hlq_version": (i32, []),
         }
@@ -573,6 +594,277 @@ def hlq_ablation_gx_hla(g_y, w, rank: int = 8, block: int = 16, with_acc: bool =
         _ptr(acc), _ptr(ws), _ws_bytes(ws, dev.index), _stream(stream)),
         "hlq_ablation_gx_hla")
     return (gx, acc) if with_acc else gx
+
+
+# ----------------------------------------------------------------------------
+# Around the layer in a training step
+# ----------------------------------------------------------------------------
+
+def _on_stream(f):
+    """`stream`: run the call with that stream current, so that what it
+    allocates (outputs, workspace) belongs to the stream that uses it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+def _rows(t, what, shape=None, index=None, dtype=None):
+    """Row stride, dtype code and address of a [rows, columns] CUDA tensor
+    whose rows are contiguous (any row stride, 0 for a repeated row), of
+    `shape`, on device `index` and of `dtype` where these are given."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must have shape "
+                         f"{'[rows, columns]' if shape is None else tuple(shape)}, "
+                         f"not {tuple(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and t.shape[1] > 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the inputs on cuda:{index}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be of dtype {dtype}, not {t.dtype}")
+    return ld, _dtype_code(t), t.data_ptr()
+
+
+def _vector(t, what, n, index, dtype=None):
+    """Address of a contiguous CUDA tensor [n] (None: a null pointer)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the inputs on cuda:{index}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what} must have shape ({n},), not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be of dtype {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _need_current(index):
+    cur = _torch().cuda.current_device()
+    if index != cur:
+        raise ValueError(f"tensors are on cuda:{index} but cuda:{cur} is current; "
+                         "make their device current first")
+
+
+def _affine(weight, bias, C, index):
+    """dtype code and addresses of a layer norm's weight and bias."""
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    some = weight if weight is not None else bias
+    return (F32 if some is None else _dtype_code(some),
+            _vector(weight, "weight", C, index), _vector(bias, "bias", C, index))
+
+
+@_on_stream
+def hlq_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None,
+                   out_dtype=None, out=None, h=None, mean=None, rstd=None,
+                   with_stats: bool = True):
+    """Layer norm of x [T, C] (of h = x + residual where one is given): returns
+    (y, mean, rstd), or (y, mean, rstd, h) with a residual.  y has `out_dtype`
+    (default: x's); mean and rstd are fp32 [T], for the backward pass, and None
+    with with_stats=False.  x, residual, out and h may have any row stride."""
+    torch = _torch()
+    ldx, dt, px = _rows(x, "x")
+    shape, index = x.shape, x.get_device()
+    _need_current(index)
+    T, C = shape
+    w_dt, pw, pb = _affine(weight, bias, C, index)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    ldy, y_dt, py = _rows(out, "out", shape, index, out_dtype)
+    ldr = ldh = 0
+    pr = ph = None
+    if residual is not None:
+        ldr, _, pr = _rows(residual, "residual", shape, index, x.dtype)
+        if h is None:
+            h = torch.empty(shape, dtype=x.dtype, device=x.device)
+        ldh, _, ph = _rows(h, "h", shape, index, x.dtype)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    if with_stats:
+        if mean is None:
+            mean = torch.empty(T, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    elif mean is not None or rstd is not None:
+        raise ValueError("mean and rstd are written only with with_stats")
+    args = (
+        px, ldx, pr, ldr, dt, pw, pb, w_dt, T, C, eps, py, ldy, y_dt, ph, ldh,
+        _vector(mean, "mean", T, index, torch.float32),
+        _vector(rstd, "rstd", T, index, torch.float32), _stream(None))
+    _check(lib().hlq_layer_norm(*args), "hlq_layer_norm")
+    return (out, mean, rstd) if residual is None else (out, mean, rstd, h)
+
+
+@_on_stream
+def hlq_layer_norm_backward(g_y, x, mean, rstd, weight=None, g_residual=None, out_dtype=None,
+                            out=None, g_weight=None, g_bias=None,
+                            with_weight_grads: bool = True, ws=None):
+    """Backward pass of hlq_layer_norm: g_y [T, C] (bf16 or fp32, whatever x's
+    type), x the normalised input (h where there was a residual) and its mean
+    and rstd.  Returns (g_x, g_weight, g_bias): g_x of `out_dtype` (default:
+    x's), with g_residual (of that type) added; g_weight and g_bias fp32 [C],
+    None with with_weight_grads=False."""
+    torch = _torch()
+    ldx, x_dt, px = _rows(x, "x")
+    shape, index = x.shape, x.get_device()
+    _need_current(index)
+    T, C = shape
+    ldgy, gy_dt, pgy = _rows(g_y, "g_y", shape, index)
+    w_dt, pw, _ = _affine(weight, None, C, index)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    ldgx, gx_dt, pgx = _rows(out, "out", shape, index, out_dtype)
+    ldgr, pgr = 0, None
+    if g_residual is not None:
+        ldgr, _, pgr = _rows(g_residual, "g_residual", shape, index, out.dtype)
+    pws, n_ws = None, 0
+    if with_weight_grads:
+        if g_weight is None:
+            g_weight = torch.empty(C, dtype=torch.float32, device=x.device)
+        if g_bias is None:
+            g_bias = torch.empty(C, dtype=torch.float32, device=x.device)
+        if ws is None:
+            ws = torch.empty(lib().hlq_layer_norm_backward_workspace_bytes(T, C),
+                             dtype=torch.uint8, device=x.device)
+        pws, n_ws = ws.data_ptr(), _ws_bytes(ws, index)
+    elif g_weight is not None or g_bias is not None:
+        raise ValueError("g_weight and g_bias are written only with with_weight_grads")
+    f32 = torch.float32
+    args = (
+        pgy, ldgy, gy_dt, px, ldx, x_dt, _vector(mean, "mean", T, index, f32),
+        _vector(rstd, "rstd", T, index, f32), pw, w_dt, pgr, ldgr, T, C, pgx, ldgx, gx_dt,
+        _vector(g_weight, "g_weight", C, index, f32), _vector(g_bias, "g_bias", C, index, f32),
+        pws, n_ws, _stream(None))
+    _check(lib().hlq_layer_norm_backward(*args), "hlq_layer_norm_backward")
+    return out, g_weight, g_bias
+
+
+@_on_stream
+def hlq_token_logprobs(logits, targets, scale: float = 1.0, logp=None, lse=None):
+    """log softmax(scale * logits) [T, V] at targets (int64 [T]) and the rows'
+    log-sum-exp: (logp, lse), fp32 [T]."""
+    torch = _torch()
+    ld, dt, pl = _rows(logits, "logits")
+    T, V = logits.shape
+    index = logits.get_device()
+    _need_current(index)
+    if logp is None:
+        logp = torch.empty(T, dtype=torch.float32, device=logits.device)
+    if lse is None:
+        lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    args = (
+        pl, ld, dt, _vector(targets, "targets", T, index, torch.int64), T, V, scale,
+        _vector(logp, "logp", T, index, torch.float32),
+        _vector(lse, "lse", T, index, torch.float32), _stream(None))
+    _check(lib().hlq_token_logprobs(*args), "hlq_token_logprobs")
+    return logp, lse
+
+
+@_on_stream
+def hlq_policy_loss(logits, actions, old_logp, advantages, weights, ref_logp=None,
+                    clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                    scale: float = 1.0, grad_scale: float = 1.0, with_grad: bool = True,
+                    stats=None, logp=None, out=None, ws=None):
+    """Clipped policy loss with a KL term to a reference (see include/hlq.h for
+    the formulas) over logits [T, V], and its gradient: (stats, logp, g).
+    stats fp32 [4]: loss, policy term, KL term, clipped share of the weights;
+    logp fp32 [T]; g [T, V] in the logits' dtype, grad_scale times the gradient
+    of the loss (None with with_grad=False; out=logits overwrites them).
+    actions int64 [T]; old_logp, advantages, weights, ref_logp fp32 [T]; a row
+    of weight 0 takes no part and is not read."""
+    torch = _torch()
+    f32 = torch.float32
+    ld, dt, pl = _rows(logits, "logits")
+    shape, index = logits.shape, logits.get_device()
+    _need_current(index)
+    T, V = shape
+    dev = logits.device
+    if stats is None:
+        stats = torch.empty(4, dtype=f32, device=dev)
+    if logp is None:
+        logp = torch.empty(T, dtype=f32, device=dev)
+    ldg, pg = 0, None
+    if with_grad:
+        if out is None:
+            out = torch.empty(shape, dtype=logits.dtype, device=dev)
+        ldg, _, pg = _rows(out, "out", shape, index, logits.dtype)
+    elif out is not None:
+        raise ValueError("out is written only with with_grad")
+    if ws is None:
+        ws = torch.empty(lib().hlq_policy_loss_workspace_bytes(T, V), dtype=torch.uint8,
+                         device=dev)
+    args = (
+        pl, ld, dt, _vector(actions, "actions", T, index, torch.int64),
+        _vector(old_logp, "old_logp", T, index, f32),
+        _vector(ref_logp, "ref_logp", T, index, f32),
+        _vector(advantages, "advantages", T, index, f32),
+        _vector(weights, "weights", T, index, f32), T, V, scale, clip_low, clip_high, kl_coef,
+        grad_scale, _vector(stats, "stats", 4, index, f32),
+        _vector(logp, "logp", T, index, f32), pg, ldg, ws.data_ptr(), _ws_bytes(ws, index),
+        _stream(None))
+    _check(lib().hlq_policy_loss(*args), "hlq_policy_loss")
+    return stats, logp, out
+
+
+@_on_stream
+def hlq_clip_grad_norm(grads, max_norm: float, outs=None, norm_only: bool = False,
+                       norm_coef=None, ws=None):
+    """Global norm of `grads` (contiguous bf16 / fp32 CUDA tensors of any
+    shapes) and their clipping to max_norm: writes coef * g to `outs` (tensors
+    of as many elements, bf16 or fp32), or over the gradients themselves by
+    default, or nowhere with norm_only.  Returns fp32 [2]: norm, coef."""
+    torch = _torch()
+    grads = list(grads)
+    n = len(grads)
+    if norm_only and outs is not None:
+        raise ValueError("norm_only writes no outs")
+    dsts = None if norm_only else grads if outs is None else list(outs)
+    if dsts is not None and len(dsts) != n:
+        raise ValueError(f"{len(dsts)} outs for {n} gradients")
+    index = grads[0].get_device() if n else torch.cuda.current_device()
+    _need_current(index)
+    dts = {torch.float32: F32, torch.bfloat16: BF16}
+
+    def table(ts, what):
+        for t in ts:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous CUDA tensors")
+            if t.get_device() != index:
+                raise ValueError(f"{what} must be on one device")
+            if t.dtype not in dts:
+                raise TypeError(f"unsupported dtype {t.dtype}: use bfloat16 or float32")
+        return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
+                (ctypes.c_int32 * n)(*[dts[t.dtype] for t in ts]))
+
+    numels = [t.numel() for t in grads]
+    g_ptr, g_dt = table(grads, "grads")
+    o_ptr = o_dt = None
+    if dsts is grads:
+        o_ptr, o_dt = g_ptr, g_dt
+    elif dsts is not None:
+        if [t.numel() for t in dsts] != numels:
+            raise ValueError("outs must have as many elements as the gradients")
+        o_ptr, o_dt = table(dsts, "outs")
+    if norm_coef is None:
+        norm_coef = torch.empty(2, dtype=torch.float32, device=f"cuda:{index}")
+    if ws is None:
+        ws = torch.empty(lib().hlq_clip_grad_norm_workspace_bytes(n), dtype=torch.uint8,
+                         device=norm_coef.device)
+    args = (
+        n, g_ptr, g_dt, o_ptr, o_dt, (ctypes.c_int64 * n)(*numels), max_norm,
+        _vector(norm_coef, "norm_coef", 2, index, torch.float32), ws.data_ptr(),
+        _ws_bytes(ws, index), _stream(None))
+    _check(lib().hlq_clip_grad_norm(*args), "hlq_clip_grad_norm")
+    return norm_coef
 
 
 def hlq_debug_gx_parts(g_y, w, gran_gy=PER_TOKEN, gran_w=PER_TENSOR, rnd=SR,

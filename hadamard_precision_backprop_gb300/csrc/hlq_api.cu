@@ -7,16 +7,15 @@
 #include <cuda_runtime.h>
 
 #include "hlq.h"
+#include "hlq_host.h"
 #include "hlq_kernels.h"
 
 namespace hlq {
 
 namespace {
-
-constexpr int kMaxDevices = 64;
 unsigned int* g_status_ptr[kMaxDevices] = {};
+}  // namespace
 
-// Address of the status word on the current device (looked up once).
 unsigned int* device_status_ptr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
@@ -29,6 +28,7 @@ unsigned int* device_status_ptr() {
   return g_status_ptr[dev];
 }
 
+namespace {
 // ---------------------------------------------------------------------------
 // Launch tracing (hlq_trace_*): while enabled, every kernel launch of this
 // library is bracketed by two events recorded on its stream, so per-kernel
@@ -61,16 +61,33 @@ inline void trace_record(cudaEvent_t ev, cudaStream_t s) {
   else
     cudaEventRecord(ev, s);
 }
-inline void trace_before(cudaStream_t s) {
+}  // namespace
+
+void trace_before(cudaStream_t s) {
   if (g_trace.on && g_trace.n < g_trace.cap) trace_record(g_trace.ev[2 * g_trace.n], s);
 }
-inline void trace_after(const char* what, cudaStream_t s) {
+void trace_after(const char* what, cudaStream_t s) {
   if (g_trace.on && g_trace.n < g_trace.cap) {
     trace_record(g_trace.ev[2 * g_trace.n + 1], s);
     g_trace.name[g_trace.n] = what;
     ++g_trace.n;
   }
 }
+
+int device_sm_count() {
+  static int count[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if (!count[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 0;
+    count[dev] = n;
+  }
+  return count[dev];
+}
+
+namespace {
 
 // Auxiliary streams per device: 0 runs the g_w branch, 1 the HQ of w, 2 the
 // host-to-device and 3 the device-to-host copies of hlq_layer_step_host.
@@ -103,12 +120,6 @@ std::atomic<bool> g_serial_branches{false};
 cudaStream_t branch_stream(int which, cudaStream_t caller, bool serial) {
   return serial ? caller : aux_stream(which);
 }
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 // Workspace layouts (offsets in bytes from ws).
 struct GxLayout {
@@ -167,19 +178,6 @@ GxHlaLayout gx_hla_layout(int64_t T, int64_t Cin, int64_t Cout, int rank) {
   return L;
 }
 
-int device_sm_count() {
-  static int count[kMaxDevices] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if (!count[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return 0;
-    count[dev] = n;
-  }
-  return count[dev];
-}
-
 // amax slot(s): one for the tensor, or one per channel
 size_t compress_ws(int64_t, int64_t Cin) {
   return kAlign + align_up((size_t)(Cin > 0 ? Cin : 0) * 4);
@@ -215,21 +213,6 @@ hlq_status check_common(int dt, int64_t T, int64_t Cin, int64_t Cout,
   return HLQ_OK;
 }
 
-
-#define HLQ_TRY(expr)                                  \
-  do {                                                 \
-    cudaError_t _e = (expr);                           \
-    if (_e != cudaSuccess) return HLQ_ERR_CUDA;        \
-  } while (0)
-
-// A kernel launch: traced when tracing is on.
-#define HLQ_LAUNCH(name, s, expr)                      \
-  do {                                                 \
-    trace_before(s);                                   \
-    cudaError_t _e = (expr);                           \
-    if (_e != cudaSuccess) return HLQ_ERR_CUDA;        \
-    trace_after(name, s);                              \
-  } while (0)
 
 // HQ of w (amax pass, then quantization to transposed E4M3 codes).
 hlq_status hq_w_launches(const void* w, bool bf16, int64_t Cout, int64_t Cin,

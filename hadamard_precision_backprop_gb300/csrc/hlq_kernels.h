@@ -160,4 +160,80 @@ hlq_status backward_gx_with_ws(const void* gy, const void* w, int dt, int64_t T,
                                int gran_w, int rnd, uint64_t seed, float* gx,
                                void* ws, size_t ws_bytes, void* stream);
 
+// ---------------------------------------------------------------------------
+// Operators around the layer in a training step.  Each struct holds one
+// call's arguments (row strides in elements) and is a kernel's parameter.
+// ---------------------------------------------------------------------------
+struct NormFwd {
+  const void *x, *residual, *weight, *bias;  // residual, weight, bias may be null
+  void *y, *h;                               // h null without residual
+  float *mean, *rstd;                        // both or neither
+  int64_t ldx, ldr, ldy, ldh, T, C;
+  float eps;
+  bool x_bf16, w_bf16, y_bf16;  // residual and h have the type of x, bias that of weight
+  unsigned int* status;
+};
+cudaError_t launch_norm_fwd(const NormFwd& p, cudaStream_t st);
+
+struct NormBwd {
+  const void *gy, *x, *weight, *gres;  // weight, gres may be null
+  const float *mean, *rstd;
+  void* gx;
+  float *gweight, *gbias;  // either may be null
+  float* part;             // [slabs][2][C] partial column sums
+  int64_t ldgy, ldx, ldgr, ldgx, T, C;
+  bool gy_bf16, x_bf16, w_bf16, gx_bf16;  // gres has the type of gx
+  unsigned int* status;
+};
+int norm_bwd_slabs(int64_t T);
+cudaError_t launch_norm_bwd_x(const NormBwd& p, cudaStream_t st);
+cudaError_t launch_norm_bwd_cols(const NormBwd& p, cudaStream_t st);
+cudaError_t launch_norm_bwd_join(const NormBwd& p, cudaStream_t st);
+
+struct TokenLogprobs {
+  const void* logits;
+  const int64_t* targets;
+  float *logp, *lse;  // lse may be null
+  int64_t ld, T, V;
+  float scale;
+  bool bf16;
+  unsigned int* status;
+};
+cudaError_t launch_token_logprobs(const TokenLogprobs& p, cudaStream_t st);
+
+struct PolicyLoss {
+  const void* logits;
+  const int64_t* actions;
+  const float *old_logp, *ref_logp, *advantage, *weight;  // ref_logp may be null
+  float *stats, *logp;                                    // logp may be null
+  void* g;                                                // may be null
+  float* part;                                            // [3][T] per-row terms of the sums
+  int64_t ld, ldg, T, V;
+  float scale, clip_low, clip_high, kl_coef, grad_scale;
+  bool bf16;
+  unsigned int* status;
+};
+cudaError_t launch_policy_rows(const PolicyLoss& p, cudaStream_t st);
+cudaError_t launch_policy_stats(const PolicyLoss& p, cudaStream_t st);
+
+// Up to kClipTensors tensors of a clipping call, cut into chunks of
+// kClipChunk elements; chunk first[i] is the first one of tensor i.
+constexpr int kClipTensors = 512;
+constexpr int kClipChunk = 8192;
+constexpr unsigned char kClipInBf16 = 1, kClipOutBf16 = 2;
+struct ClipTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  int64_t numel[kClipTensors], first[kClipTensors];
+  unsigned char flags[kClipTensors];
+  int n;
+  int64_t chunks;
+};
+int clip_norm_grid(int64_t chunks, int sms);
+cudaError_t launch_clip_norm(const ClipTable& tab, double* part, int grid, cudaStream_t st);
+cudaError_t launch_clip_coef(const double* part, int n_part, float max_norm, float* norm_coef,
+                             unsigned int* status, cudaStream_t st);
+cudaError_t launch_clip_scale(const ClipTable& tab, const float* norm_coef, int grid,
+                              cudaStream_t st);
+
 }  // namespace hlq

@@ -526,6 +526,119 @@ hlq_status hlq_linear_backward_gx_noalloc(const void *d_gy, const void *d_w, int
                                           void *stream);
 size_t hlq_noalloc_scratch_bytes(void);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the layer in a training step: the layer norm whose output the layer
+ * reads and whose backward pass takes the layer's g_x, the loss of a policy
+ * whose logits' gradient is the g_y of the vocabulary projection, and the
+ * clipping of all gradients.  The conventions above hold, with these changes:
+ *  - any sizes: rows T >= 0, columns C, V >= 1 (both below 2^31);
+ *  - matrices are rows of contiguous elements, a row stride (in elements) of
+ *    its own for each: >= the row's length, or for an input 0 (one row,
+ *    repeated); strides are not read where T <= 1;
+ *  - pointers need only the alignment of their element type (ws: 256 bytes);
+ *    rows that all begin on 16-byte boundaries are moved fastest;
+ *  - an output may be exactly one of the call's inputs of the same type and
+ *    stride (in place); other overlaps are not allowed;
+ *  - all sums are taken in fp32 (the norm's in fp64 across threads) in an
+ *    order fixed by the sizes and the GPU: equal calls give equal bits;
+ *  - device flags: HLQ_DEV_NONFINITE where a row's statistics, its loss
+ *    coefficient or the norm is infinite or NaN (outputs follow the formulas),
+ *    HLQ_DEV_BADCODE where a token is outside [0, V).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Layer norm: per row of h = x (+ residual, the sum kept in fp32),
+ *   mean = sum_c h / C,  rstd = 1 / sqrt(sum_c (h - mean)^2 / C + eps),
+ *   y = (h - mean) rstd weight + bias.
+ * x, residual, h [T, C] have dtype x_dt; y [T, C] dtype y_dt; weight, bias
+ * [C] dtype w_dt, either may be NULL (1, 0).  d_residual and d_h go together:
+ * both NULL, or h (rounded to x_dt) is written to d_h.  d_mean, d_rstd fp32
+ * [T]: both NULL, or both written.
+ */
+hlq_status hlq_layer_norm(const void *d_x, int64_t ldx, const void *d_residual, int64_t ldr,
+                          int x_dt, const void *d_weight, const void *d_bias, int w_dt,
+                          int64_t T, int64_t C, float eps, void *d_y, int64_t ldy, int y_dt,
+                          void *d_h, int64_t ldh, float *d_mean, float *d_rstd, void *stream);
+
+/*
+ * Its backward pass.  x is what was normalised (h where there was a
+ * residual), mean and rstd fp32 [T] its statistics:
+ *   xhat = (x - mean) rstd,  a = g_y weight,
+ *   g_x = rstd (a - sum_c a / C - xhat sum_c(a xhat) / C) (+ g_residual),
+ *   g_weight = sum_t g_y xhat,  g_bias = sum_t g_y   (fp32 [C]).
+ * g_y may have another type than x (hlq_linear_backward gives fp32 g_x);
+ * g_residual, the gradient that reached h by the residual path, has the type
+ * of g_x.  d_weight, d_gres, d_gweight, d_gbias may be NULL; the workspace
+ * (hlq_layer_norm_backward_workspace_bytes) is needed for g_weight or g_bias.
+ */
+hlq_status hlq_layer_norm_backward(const void *d_gy, int64_t ldgy, int gy_dt, const void *d_x,
+                                   int64_t ldx, int x_dt, const float *d_mean,
+                                   const float *d_rstd, const void *d_weight, int w_dt,
+                                   const void *d_gres, int64_t ldgr, int64_t T, int64_t C,
+                                   void *d_gx, int64_t ldgx, int gx_dt, float *d_gweight,
+                                   float *d_gbias, void *d_ws, size_t ws_bytes, void *stream);
+size_t hlq_layer_norm_backward_workspace_bytes(int64_t T, int64_t C);
+
+/*
+ * Log-probabilities of given tokens: z = scale logits (scale > 0, the inverse
+ * temperature), lse = log sum_v exp(z_v), logp = z[target] - lse, per row of
+ * logits [T, V] (dtype dt).  targets int64 [T]; a target outside [0, V) gives
+ * a NaN and HLQ_DEV_BADCODE.  Logits of -inf are tokens of probability 0; a
+ * row of nothing else has no distribution (NaN).  logp, lse fp32 [T]; d_lse
+ * may be NULL.  Serves for the old and the reference log-probabilities of
+ * hlq_policy_loss.
+ */
+hlq_status hlq_token_logprobs(const void *d_logits, int64_t ld, int dt,
+                              const int64_t *d_targets, int64_t T, int64_t V, float scale,
+                              float *d_logp, float *d_lse, void *stream);
+
+/*
+ * Clipped policy loss with a KL term, and the gradient of the logits.  Per
+ * row t with lp as above (actions as targets), A = advantage:
+ *   r  = exp(lp - old_logp),
+ *   pg = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A),
+ *   kl = exp(d) - d - 1,  d = ref_logp - lp      (0 where d_ref_logp is NULL),
+ *   loss = sum_t weight_t (pg + kl_coef kl),
+ *   c  = (pg unclipped ? -r A : 0) + kl_coef (1 - exp(d)),
+ *   g[t, v] = grad_scale weight_t c scale ([v == action] - softmax(z)_v).
+ * weight fp32 [T] holds the normalisation of the user's choice (mask / number
+ * of tokens, per sequence, ...).  A row of weight 0 is not read at all: it adds
+ * nothing, its logp is 0 and its gradient row is zeros, whatever its logits,
+ * action and log-probabilities hold.
+ * d_stats fp32 [4]: loss, sum weight pg, sum weight kl, sum of the weights of
+ * the clipped rows.  d_logp fp32 [T] may be NULL; d_g [T, V] (dtype dt) may be
+ * NULL (the loss alone) or d_logits itself with the same stride.
+ * Workspace: hlq_policy_loss_workspace_bytes.
+ */
+hlq_status hlq_policy_loss(const void *d_logits, int64_t ld, int dt, const int64_t *d_actions,
+                           const float *d_old_logp, const float *d_ref_logp,
+                           const float *d_advantage, const float *d_weight, int64_t T,
+                           int64_t V, float scale, float clip_low, float clip_high,
+                           float kl_coef, float grad_scale, float *d_stats, float *d_logp,
+                           void *d_g, int64_t ldg, void *d_ws, size_t ws_bytes, void *stream);
+size_t hlq_policy_loss_workspace_bytes(int64_t T, int64_t V);
+
+/*
+ * Global norm of n gradients and their clipping:
+ *   norm = sqrt(sum over all elements of all tensors of g^2),
+ *   coef = min(1, max_norm / (norm + 1e-6)),  out_i = coef g_i.
+ * The tables are host arrays of n entries: device pointers, dtypes (hlq_dtype),
+ * element counts (0 allowed; each tensor contiguous).  h_outs may be h_grads
+ * (in place), other buffers of either dtype (h_out_dts), or NULL: the norm and
+ * the coefficient alone.  d_norm_coef fp32 [2]: norm, coef.  The squares
+ * neither overflow nor vanish: the norm is right to fp32 rounding wherever it
+ * is a finite fp32 number.  An infinite norm gives coef 0, a NaN coef NaN, and
+ * HLQ_DEV_NONFINITE; max_norm +inf clips nothing.
+ * Workspace: hlq_clip_grad_norm_workspace_bytes(n).
+ */
+hlq_status hlq_clip_grad_norm(int64_t n, const void *const *h_grads, const int32_t *h_grad_dts,
+                              void *const *h_outs, const int32_t *h_out_dts,
+                              const int64_t *h_numels, float max_norm, float *d_norm_coef,
+                              void *d_ws, size_t ws_bytes, void *stream);
+size_t hlq_clip_grad_norm_workspace_bytes(int64_t n);
+
 /* Static text for a status code. */
 const char *hlq_status_string(int status);
 
