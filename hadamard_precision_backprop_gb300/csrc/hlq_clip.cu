@@ -4,14 +4,18 @@
 //
 // The tensors' table travels as a kernel parameter: nothing is copied to the
 // device beforehand, and a captured call replays with the addresses it was
-// captured with.
+// captured with.  The tensors are cut into chunks of 8192 elements; a CTA
+// takes a run of consecutive chunks, and each of its threads 32 elements of a
+// chunk, all loaded before the first is used.
 #include "hlq_device.cuh"
 #include "hlq_kernels.h"
+#include "hlq_rows.cuh"
 
 namespace hlq {
 namespace {
 
-constexpr int kClipThreads = 256;
+constexpr int kThreads = 256;
+constexpr int kQuads = kClipChunk / kThreads / 4;  // groups of four a thread
 
 __device__ __forceinline__ double cta_sum_f64(double v, double* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -20,12 +24,12 @@ __device__ __forceinline__ double cta_sum_f64(double v, double* red) {
   if (lane == 0) red[warp] = v;
   __syncthreads();
   double s = 0.0;
-  for (int i = 0; i < kClipThreads / 32; ++i) s += red[i];
+  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
   return s;
 }
 
 // The tensor that holds chunk `k` of the concatenation: the last one whose
-// first chunk is <= k (tensors without elements have no chunk).
+// first chunk is <= k (tensors without elements are not in the table).
 __device__ __forceinline__ int tensor_of(const ClipTable& tab, int64_t k) {
   int lo = 0, hi = tab.n - 1;
   while (lo < hi) {
@@ -38,31 +42,96 @@ __device__ __forceinline__ int tensor_of(const ClipTable& tab, int64_t k) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
+// This thread's elements of a chunk of n elements that begins at `e0` of the
+// tensor, zeros past its end: groups of four where the tensor is aligned to
+// them, else single elements a CTA width apart.  Element (i, k) is number
+// (i * kThreads + threadIdx.x) * 4 + k of the chunk, or
+// (i * 4 + k) * kThreads + threadIdx.x.
+__device__ __forceinline__ int64_t place(bool four, int i, int k) {
+  return four ? ((int64_t)i * kThreads + threadIdx.x) * 4 + k
+              : ((int64_t)i * 4 + k) * kThreads + threadIdx.x;
+}
+__device__ __forceinline__ void load_chunk(const void* in, bool bf16, bool four, int64_t e0,
+                                           int64_t n, float (&v)[kQuads * 4]) {
+  if (four && n == kClipChunk) {
+    if (bf16) {
+      uint2 r[kQuads];
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i)
+        r[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(in) + e0 +
+                                               place(true, i, 0));
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        v[i * 4] = bf16_lo(r[i].x), v[i * 4 + 1] = bf16_hi(r[i].x);
+        v[i * 4 + 2] = bf16_lo(r[i].y), v[i * 4 + 3] = bf16_hi(r[i].y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const float4 f =
+            *reinterpret_cast<const float4*>(static_cast<const float*>(in) + e0 + place(true, i, 0));
+        v[i * 4] = f.x, v[i * 4 + 1] = f.y, v[i * 4 + 2] = f.z, v[i * 4 + 3] = f.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t e = place(four, i, k);
+        v[i * 4 + k] = e < n ? load_elem(in, bf16, e0 + e) : 0.f;
+      }
+  }
+}
+
+// Sum of the squares of a thread's 32 elements: in fp32 where that neither
+// overflows nor loses small terms (the sum is between 2^-95 and 2^120: any
+// square that went below 2^-126 is then beneath its last bit), else in fp64.
+__device__ __forceinline__ double sum_of_squares(const float (&v)[kQuads * 4]) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kQuads * 4; ++i) s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
+  const float f = (s[0] + s[1]) + (s[2] + s[3]);
+  if (f >= 0x1p-95f && f <= 0x1p120f) return f;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < kQuads * 4; ++i) any |= __float_as_uint(v[i]) << 1;
+  if (any == 0) return 0.0;
+  double d = 0.0;
+#pragma unroll
+  for (int i = 0; i < kQuads * 4; ++i) d += (double)v[i] * v[i];
+  return d;
+}
+
+__global__ void __launch_bounds__(kThreads)
     clip_norm_kernel(const __grid_constant__ ClipTable tab, double* part) {
   __shared__ double red[32];
+  pdl_wait();
+  const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
+  const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
+  int i = tensor_of(tab, k0);
   double acc = 0.0;
-  for (int64_t k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
-    const int i = tensor_of(tab, k);
+  for (int64_t k = k0; k < k1; ++k) {
+    if (i + 1 < tab.n && tab.first[i + 1] <= k) ++i;  // every tensor has a chunk
     const int64_t e0 = (k - tab.first[i]) * kClipChunk;
-    const int64_t n = min((int64_t)kClipChunk, tab.numel[i] - e0);
-    for (int64_t e = threadIdx.x; e < n; e += kClipThreads) {
-      const double g = (tab.flags[i] & kClipInBf16)
-                           ? __bfloat162float(static_cast<const __nv_bfloat16*>(tab.in[i])[e0 + e])
-                           : static_cast<const float*>(tab.in[i])[e0 + e];
-      acc += g * g;
-    }
+    float v[kQuads * 4];
+    load_chunk(tab.in[i], tab.flags[i] & kClipInBf16, tab.flags[i] & kClipInFour, e0,
+               min((int64_t)kClipChunk, tab.numel[i] - e0), v);
+    acc += sum_of_squares(v);
   }
+  pdl_trigger();
   acc = cta_sum_f64(acc, red);
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kThreads)
     clip_coef_kernel(const double* part, int n_part, float max_norm, float* norm_coef,
                      unsigned int* status) {
   __shared__ double red[32];
+  pdl_wait();
+  pdl_trigger();
   double s = 0.0;
-  for (int i = threadIdx.x; i < n_part; i += kClipThreads) s += part[i];
+  for (int i = threadIdx.x; i < n_part; i += kThreads) s += ld_dep_f64(part + i);
   s = cta_sum_f64(s, red);
   if (threadIdx.x == 0) {
     const float norm = (float)sqrt(s);
@@ -73,47 +142,74 @@ __global__ void __launch_bounds__(kClipThreads)
   }
 }
 
-__global__ void __launch_bounds__(kClipThreads)
+// The runs and their chunks in the opposite order of the norm's pass: what
+// that pass read last is still in L2.
+__global__ void __launch_bounds__(kThreads)
     clip_scale_kernel(const __grid_constant__ ClipTable tab, const float* norm_coef) {
-  const float coef = norm_coef[1];
-  for (int64_t k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
-    const int i = tensor_of(tab, k);
+  pdl_wait();
+  const float coef = ld_dep_f32(norm_coef + 1);
+  const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
+  const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
+  if (k1 == k0) return;
+  int i = tensor_of(tab, k1 - 1);
+  for (int64_t k = k1 - 1; k >= k0; --k) {
+    if (tab.first[i] > k) --i;
+    const unsigned char fl = tab.flags[i];
+    const bool in_bf16 = fl & kClipInBf16, out_bf16 = fl & kClipOutBf16;
+    // in place, by a coefficient of 1: already there
+    if (coef == 1.f && tab.in[i] == tab.out[i] && in_bf16 == out_bf16) continue;
+    const bool four = (fl & kClipInFour) && (fl & kClipOutFour);
     const int64_t e0 = (k - tab.first[i]) * kClipChunk;
     const int64_t n = min((int64_t)kClipChunk, tab.numel[i] - e0);
-    for (int64_t e = threadIdx.x; e < n; e += kClipThreads) {
-      const float g = (tab.flags[i] & kClipInBf16)
-                          ? __bfloat162float(static_cast<const __nv_bfloat16*>(tab.in[i])[e0 + e])
-                          : static_cast<const float*>(tab.in[i])[e0 + e];
-      if (tab.flags[i] & kClipOutBf16)
-        static_cast<__nv_bfloat16*>(tab.out[i])[e0 + e] = __float2bfloat16_rn(coef * g);
-      else
-        static_cast<float*>(tab.out[i])[e0 + e] = coef * g;
+    float v[kQuads * 4];
+    load_chunk(tab.in[i], in_bf16, four, e0, n, v);
+#pragma unroll
+    for (int q = 0; q < kQuads * 4; ++q) v[q] *= coef;
+    void* out = tab.out[i];
+    if (four && n == kClipChunk) {
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int64_t e = e0 + place(true, q, 0);
+        if (out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + e) = make_uint2(
+              pack_bf16(v[q * 4], v[q * 4 + 1]), pack_bf16(v[q * 4 + 2], v[q * 4 + 3]));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(out) + e) =
+              make_float4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t e = place(four, q, j);
+          if (e < n) store_elem(out, out_bf16, e0 + e, v[q * 4 + j]);
+        }
     }
   }
 }
 
 }  // namespace
 
-int clip_norm_grid(int64_t chunks, int sms) {
+// Four CTAs of 256 threads an SM: 128 KB of loads in flight.
+int clip_grid(int64_t chunks, int sms) {
   const int64_t most = (int64_t)sms * 4;
   return (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);
 }
 
 cudaError_t launch_clip_norm(const ClipTable& tab, double* part, int grid, cudaStream_t st) {
-  clip_norm_kernel<<<grid, kClipThreads, 0, st>>>(tab, part);
-  return cudaGetLastError();
+  return launch_pdl(clip_norm_kernel, dim3(grid), dim3(kThreads), 0, st, tab, part);
 }
 
 cudaError_t launch_clip_coef(const double* part, int n_part, float max_norm, float* norm_coef,
                              unsigned int* status, cudaStream_t st) {
-  clip_coef_kernel<<<1, kClipThreads, 0, st>>>(part, n_part, max_norm, norm_coef, status);
-  return cudaGetLastError();
+  return launch_pdl(clip_coef_kernel, dim3(1), dim3(kThreads), 0, st, part, n_part, max_norm,
+                    norm_coef, status);
 }
 
 cudaError_t launch_clip_scale(const ClipTable& tab, const float* norm_coef, int grid,
                               cudaStream_t st) {
-  clip_scale_kernel<<<grid, kClipThreads, 0, st>>>(tab, norm_coef);
-  return cudaGetLastError();
+  return launch_pdl(clip_scale_kernel, dim3(grid), dim3(kThreads), 0, st, tab, norm_coef);
 }
 
 }  // namespace hlq

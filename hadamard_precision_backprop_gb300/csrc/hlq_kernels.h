@@ -180,15 +180,15 @@ struct NormBwd {
   const float *mean, *rstd;
   void* gx;
   float *gweight, *gbias;  // either may be null
-  float* part;             // [slabs][2][C] partial column sums
+  float* part;             // [slabs][2][C] partial column sums; null: not wanted
   int64_t ldgy, ldx, ldgr, ldgx, T, C;
   bool gy_bf16, x_bf16, w_bf16, gx_bf16;  // gres has the type of gx
   unsigned int* status;
 };
-int norm_bwd_slabs(int64_t T);
-cudaError_t launch_norm_bwd_x(const NormBwd& p, cudaStream_t st);
-cudaError_t launch_norm_bwd_cols(const NormBwd& p, cudaStream_t st);
-cudaError_t launch_norm_bwd_join(const NormBwd& p, cudaStream_t st);
+// g_x, and (with part) *slabs slabs of partial column sums, which the join adds.
+int norm_bwd_most_slabs(int64_t T);
+cudaError_t launch_norm_bwd(const NormBwd& p, int* slabs, cudaStream_t st);
+cudaError_t launch_norm_bwd_join(const NormBwd& p, int slabs, cudaStream_t st);
 
 struct TokenLogprobs {
   const void* logits;
@@ -199,6 +199,7 @@ struct TokenLogprobs {
   bool bf16;
   unsigned int* status;
 };
+int64_t loss_most_rows(int64_t V);  // of one launch
 cudaError_t launch_token_logprobs(const TokenLogprobs& p, cudaStream_t st);
 
 struct PolicyLoss {
@@ -221,6 +222,7 @@ cudaError_t launch_policy_stats(const PolicyLoss& p, cudaStream_t st);
 constexpr int kClipTensors = 512;
 constexpr int kClipChunk = 8192;
 constexpr unsigned char kClipInBf16 = 1, kClipOutBf16 = 2;
+constexpr unsigned char kClipInFour = 4, kClipOutFour = 8;  // aligned to four elements
 struct ClipTable {
   const void* in[kClipTensors];
   void* out[kClipTensors];
@@ -229,7 +231,7 @@ struct ClipTable {
   int n;
   int64_t chunks;
 };
-int clip_norm_grid(int64_t chunks, int sms);
+int clip_grid(int64_t chunks, int sms);
 cudaError_t launch_clip_norm(const ClipTable& tab, double* part, int grid, cudaStream_t st);
 cudaError_t launch_clip_coef(const double* part, int n_part, float max_norm, float* norm_coef,
                              unsigned int* status, cudaStream_t st);

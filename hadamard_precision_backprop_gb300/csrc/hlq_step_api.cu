@@ -12,7 +12,7 @@
 namespace hlq {
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 31;  // rows and columns of one call
+constexpr int64_t kMaxRows = (int64_t)1 << 31;  // rows, and columns, of one call
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
 bool dtype_ok(int dt) { return dt == HLQ_F32 || dt == HLQ_BF16; }
@@ -32,7 +32,7 @@ hlq_status check_rows(int64_t T, int64_t C) {
 }
 
 size_t norm_bwd_ws(int64_t T, int64_t C) {
-  return align_up((size_t)norm_bwd_slabs(T) * 2 * (size_t)C * 4);
+  return align_up((size_t)norm_bwd_most_slabs(T) * 2 * (size_t)C * 4);
 }
 
 size_t policy_ws(int64_t T) { return align_up((size_t)(T > 0 ? T : 1) * 3 * 4); }
@@ -120,15 +120,15 @@ hlq_status hlq_layer_norm_backward(const void* d_gy, int64_t ldgy, int gy_dt, co
   NormBwd p{};
   p.gy = d_gy; p.x = d_x; p.weight = d_weight; p.gres = d_gres;
   p.mean = d_mean; p.rstd = d_rstd; p.gx = d_gx; p.gweight = d_gweight; p.gbias = d_gbias;
-  p.part = static_cast<float*>(d_ws);
+  p.part = cols ? static_cast<float*>(d_ws) : nullptr;
   p.ldgy = ldgy; p.ldx = ldx; p.ldgr = ldgr; p.ldgx = ldgx; p.T = T; p.C = C;
   p.gy_bf16 = gy_dt == HLQ_BF16; p.x_bf16 = x_dt == HLQ_BF16; p.w_bf16 = w_dt == HLQ_BF16;
   p.gx_bf16 = gx_dt == HLQ_BF16;
   p.status = device_status_ptr();
   if (!p.status) return HLQ_ERR_CUDA;
-  if (cols) HLQ_LAUNCH("norm_bwd_cols", s, launch_norm_bwd_cols(p, s));
-  HLQ_LAUNCH("norm_bwd_x", s, launch_norm_bwd_x(p, s));
-  if (cols) HLQ_LAUNCH("norm_bwd_join", s, launch_norm_bwd_join(p, s));
+  int slabs = 0;
+  HLQ_LAUNCH("norm_bwd", s, launch_norm_bwd(p, &slabs, s));
+  if (cols) HLQ_LAUNCH("norm_bwd_join", s, launch_norm_bwd_join(p, slabs, s));
   return HLQ_OK;
 }
 
@@ -138,6 +138,7 @@ hlq_status hlq_token_logprobs(const void* d_logits, int64_t ld, int dt, const in
   if (!dtype_ok(dt) || !(scale > 0.f) || std::isinf(scale)) return HLQ_ERR_INVALID_ARG;
   hlq_status st = check_rows(T, V);
   if (st != HLQ_OK) return st;
+  if (T > loss_most_rows(V)) return HLQ_ERR_UNSUPPORTED;
   if (T > 0 && (!d_logits || !d_targets || !d_logp)) return HLQ_ERR_INVALID_ARG;
   if (!stride_ok(ld, T, V, true)) return HLQ_ERR_SHAPE;
   if (!aligned_to(d_logits, elem_bytes(dt)) || !aligned_to(d_targets, 8) ||
@@ -170,6 +171,7 @@ hlq_status hlq_policy_loss(const void* d_logits, int64_t ld, int dt, const int64
     return HLQ_ERR_INVALID_ARG;
   hlq_status st = check_rows(T, V);
   if (st != HLQ_OK) return st;
+  if (T > loss_most_rows(V)) return HLQ_ERR_UNSUPPORTED;
   if (!d_stats) return HLQ_ERR_INVALID_ARG;
   if (T > 0 && (!d_logits || !d_actions || !d_old_logp || !d_advantage || !d_weight))
     return HLQ_ERR_INVALID_ARG;
@@ -244,7 +246,11 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
       tab.numel[tab.n] = h_numels[i];
       tab.first[tab.n] = tab.chunks;
       tab.flags[tab.n] = (unsigned char)((h_grad_dts[i] == HLQ_BF16 ? kClipInBf16 : 0) |
-                                         (h_outs && h_out_dts[i] == HLQ_BF16 ? kClipOutBf16 : 0));
+                                         (h_outs && h_out_dts[i] == HLQ_BF16 ? kClipOutBf16 : 0) |
+                                         (aligned_to(h_grads[i], 4 * elem_bytes(h_grad_dts[i]))
+                                              ? kClipInFour : 0) |
+                                         (h_outs && aligned_to(h_outs[i], 4 * elem_bytes(h_out_dts[i]))
+                                              ? kClipOutFour : 0));
       tab.chunks += (h_numels[i] + kClipChunk - 1) / kClipChunk;
       ++tab.n;
     }
@@ -253,7 +259,7 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
   for (int64_t i = 0; i < n;) {
     i = fill(i);
     if (tab.n == 0) continue;
-    int grid = clip_norm_grid(tab.chunks, sms);
+    int grid = clip_grid(tab.chunks, sms);
     if (grid > kClipParts) grid = kClipParts;
     HLQ_LAUNCH("clip_norm", s, launch_clip_norm(tab, part + n_part, grid, s));
     n_part += grid;
@@ -263,7 +269,7 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
   for (int64_t i = 0; i < n;) {
     i = fill(i);
     if (tab.n == 0) continue;
-    int grid = clip_norm_grid(tab.chunks, sms);
+    int grid = clip_grid(tab.chunks, sms);
     HLQ_LAUNCH("clip_scale", s, launch_clip_scale(tab, d_norm_coef, grid, s));
   }
   return HLQ_OK;
