@@ -21,8 +21,8 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import array
 import ctypes
-import functools
 import os
 import threading
 
@@ -81,6 +81,8 @@ def build_library(force: bool = False) -> str:
 def lib() -> ctypes.CDLL:
     """The loaded libhlq (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -177,9 +179,15 @@ def _check(rc: int, what: str):
 # torch marshalling
 # ----------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -600,36 +608,58 @@ def hlq_ablation_gx_hla(g_y, w, rank: int = 8, block: int = 16, with_acc: bool =
 # Around the layer in a training step
 # ----------------------------------------------------------------------------
 
-def _on_stream(f):
-    """`stream`: run the call with that stream current, so that what it
-    allocates (outputs, workspace) belongs to the stream that uses it."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with _torch().cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+def _on_stream(call, args):
+    """`call` with the keyword arguments `args`, their stream current: what it
+    allocates (outputs, workspace) then belongs to the stream that uses it."""
+    stream = args.pop("stream")
+    with _torch().cuda.stream(stream):
+        return call(**args)
 
 
-def _rows(t, what, shape=None, index=None, dtype=None):
+def _raw_stream(index):
+    """torch's current stream of device `index`, as the library takes it."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
+_dtype_codes = {}
+
+
+def _code(dtype):
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: F32, torch.bfloat16: BF16})
+        code = _dtype_codes.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}: use bfloat16 or float32")
+    return code
+
+
+def _rows(t, what, index=None, shape=None, dtype=None):
     """Row stride, dtype code and address of a [rows, columns] CUDA tensor
-    whose rows are contiguous (any row stride, 0 for a repeated row), of
-    `shape`, on device `index` and of `dtype` where these are given."""
+    whose rows are contiguous (any row stride, 0 for a repeated row), on
+    device `index`, of `shape` and of `dtype` where these are given."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} must have shape "
-                         f"{'[rows, columns]' if shape is None else tuple(shape)}, "
-                         f"not {tuple(t.shape)}")
+    if shape is None:
+        if t.dim() != 2:
+            raise ValueError(f"{what} must have shape [rows, columns], not {tuple(t.shape)}")
+    elif t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     ld, step = t.stride()
     if step != 1 and t.shape[1] > 1:
         raise ValueError(f"the rows of {what} must be contiguous")
     if index is not None and t.get_device() != index:
         raise ValueError(f"{what} is on cuda:{t.get_device()}, the inputs on cuda:{index}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what} must be of dtype {dtype}, not {t.dtype}")
-    return ld, _dtype_code(t), t.data_ptr()
+    own = t.dtype
+    if dtype is not None and own != dtype:
+        raise ValueError(f"{what} must be of dtype {dtype}, not {own}")
+    return ld, _code(own), t.data_ptr()
+
+
+def _new_rows(t, cols):
+    """The same of an output that the call has just allocated."""
+    return cols, _code(t.dtype), t.data_ptr()
 
 
 def _vector(t, what, n, index, dtype=None):
@@ -640,11 +670,28 @@ def _vector(t, what, n, index, dtype=None):
         raise ValueError(f"{what} must be a contiguous CUDA tensor")
     if t.get_device() != index:
         raise ValueError(f"{what} is on cuda:{t.get_device()}, the inputs on cuda:{index}")
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{what} must have shape ({n},), not {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be of dtype {dtype}, not {t.dtype}")
     return t.data_ptr()
+
+
+def _out_vector(t, what, n, index, device):
+    """An fp32 output [n], the caller's or a new one, and its address."""
+    if t is None:
+        t = _torch().empty(n, dtype=_torch().float32, device=device)
+        return t, t.data_ptr()
+    return t, _vector(t, what, n, index, _torch().float32)
+
+
+def _workspace(ws, n, index, device):
+    """A workspace of n bytes, the caller's or a new one: the tensor (which
+    must outlive the call), its address and its size."""
+    if ws is None:
+        ws = _torch().empty(n, dtype=_torch().uint8, device=device)
+        return ws, ws.data_ptr(), n
+    return ws, ws.data_ptr(), _ws_bytes(ws, index)
 
 
 def _need_current(index):
@@ -654,126 +701,121 @@ def _need_current(index):
                          "make their device current first")
 
 
-def _affine(weight, bias, C, index):
-    """dtype code and addresses of a layer norm's weight and bias."""
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias must have one dtype")
-    some = weight if weight is not None else bias
-    return (F32 if some is None else _dtype_code(some),
-            _vector(weight, "weight", C, index), _vector(bias, "bias", C, index))
-
-
-@_on_stream
 def hlq_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None,
                    out_dtype=None, out=None, h=None, mean=None, rstd=None,
-                   with_stats: bool = True):
+                   with_stats: bool = True, stream=None):
     """Layer norm of x [T, C] (of h = x + residual where one is given): returns
     (y, mean, rstd), or (y, mean, rstd, h) with a residual.  y has `out_dtype`
     (default: x's); mean and rstd are fp32 [T], for the backward pass, and None
     with with_stats=False.  x, residual, out and h may have any row stride."""
+    if stream is not None:
+        return _on_stream(hlq_layer_norm, locals())
     torch = _torch()
     ldx, dt, px = _rows(x, "x")
-    shape, index = x.shape, x.get_device()
+    shape, index, device = x.shape, x.get_device(), x.device
     _need_current(index)
     T, C = shape
-    w_dt, pw, pb = _affine(weight, bias, C, index)
+    w_dt = F32
+    if weight is not None:
+        w_dt = _code(weight.dtype)
+    elif bias is not None:
+        w_dt = _code(bias.dtype)
+    pw = _vector(weight, "weight", C, index)
+    pb = _vector(bias, "bias", C, index)
+    if pw is not None and pb is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    ldy, y_dt, py = _rows(out, "out", shape, index, out_dtype)
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
+        ldy, y_dt, py = _new_rows(out, C)
+    else:
+        ldy, y_dt, py = _rows(out, "out", index, shape, out_dtype)
     ldr = ldh = 0
-    pr = ph = None
+    pr = ph = pm = ps = None
     if residual is not None:
-        ldr, _, pr = _rows(residual, "residual", shape, index, x.dtype)
+        ldr, _, pr = _rows(residual, "residual", index, shape, x.dtype)
         if h is None:
-            h = torch.empty(shape, dtype=x.dtype, device=x.device)
-        ldh, _, ph = _rows(h, "h", shape, index, x.dtype)
+            h = torch.empty(shape, dtype=x.dtype, device=device)
+        ldh, _, ph = _rows(h, "h", index, shape, x.dtype)
     elif h is not None:
         raise ValueError("h is written only with a residual")
     if with_stats:
-        if mean is None:
-            mean = torch.empty(T, dtype=torch.float32, device=x.device)
-        if rstd is None:
-            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        mean, pm = _out_vector(mean, "mean", T, index, device)
+        rstd, ps = _out_vector(rstd, "rstd", T, index, device)
     elif mean is not None or rstd is not None:
         raise ValueError("mean and rstd are written only with with_stats")
-    args = (
-        px, ldx, pr, ldr, dt, pw, pb, w_dt, T, C, eps, py, ldy, y_dt, ph, ldh,
-        _vector(mean, "mean", T, index, torch.float32),
-        _vector(rstd, "rstd", T, index, torch.float32), _stream(None))
-    _check(lib().hlq_layer_norm(*args), "hlq_layer_norm")
+    rc = lib().hlq_layer_norm(px, ldx, pr, ldr, dt, pw, pb, w_dt, T, C, eps, py, ldy, y_dt, ph,
+                              ldh, pm, ps, _raw_stream(index))
+    _check(rc, "hlq_layer_norm")
     return (out, mean, rstd) if residual is None else (out, mean, rstd, h)
 
 
-@_on_stream
 def hlq_layer_norm_backward(g_y, x, mean, rstd, weight=None, g_residual=None, out_dtype=None,
                             out=None, g_weight=None, g_bias=None,
-                            with_weight_grads: bool = True, ws=None):
+                            with_weight_grads: bool = True, ws=None, stream=None):
     """Backward pass of hlq_layer_norm: g_y [T, C] (bf16 or fp32, whatever x's
     type), x the normalised input (h where there was a residual) and its mean
     and rstd.  Returns (g_x, g_weight, g_bias): g_x of `out_dtype` (default:
     x's), with g_residual (of that type) added; g_weight and g_bias fp32 [C],
     None with with_weight_grads=False."""
+    if stream is not None:
+        return _on_stream(hlq_layer_norm_backward, locals())
     torch = _torch()
+    f32 = torch.float32
     ldx, x_dt, px = _rows(x, "x")
-    shape, index = x.shape, x.get_device()
+    shape, index, device = x.shape, x.get_device(), x.device
     _need_current(index)
     T, C = shape
-    ldgy, gy_dt, pgy = _rows(g_y, "g_y", shape, index)
-    w_dt, pw, _ = _affine(weight, None, C, index)
+    ldgy, gy_dt, pgy = _rows(g_y, "g_y", index, shape)
+    pm = _vector(mean, "mean", T, index, f32)
+    ps = _vector(rstd, "rstd", T, index, f32)
+    pw = _vector(weight, "weight", C, index)
+    w_dt = F32 if weight is None else _code(weight.dtype)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    ldgx, gx_dt, pgx = _rows(out, "out", shape, index, out_dtype)
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
+        ldgx, gx_dt, pgx = _new_rows(out, C)
+    else:
+        ldgx, gx_dt, pgx = _rows(out, "out", index, shape, out_dtype)
     ldgr, pgr = 0, None
     if g_residual is not None:
-        ldgr, _, pgr = _rows(g_residual, "g_residual", shape, index, out.dtype)
-    pws, n_ws = None, 0
+        ldgr, _, pgr = _rows(g_residual, "g_residual", index, shape, out.dtype)
+    pgw = pgb = pws = None
+    n_ws = 0
     if with_weight_grads:
-        if g_weight is None:
-            g_weight = torch.empty(C, dtype=torch.float32, device=x.device)
-        if g_bias is None:
-            g_bias = torch.empty(C, dtype=torch.float32, device=x.device)
+        g_weight, pgw = _out_vector(g_weight, "g_weight", C, index, device)
+        g_bias, pgb = _out_vector(g_bias, "g_bias", C, index, device)
         if ws is None:
-            ws = torch.empty(lib().hlq_layer_norm_backward_workspace_bytes(T, C),
-                             dtype=torch.uint8, device=x.device)
-        pws, n_ws = ws.data_ptr(), _ws_bytes(ws, index)
+            n_ws = lib().hlq_layer_norm_backward_workspace_bytes(T, C)
+        ws, pws, n_ws = _workspace(ws, n_ws, index, device)
     elif g_weight is not None or g_bias is not None:
         raise ValueError("g_weight and g_bias are written only with with_weight_grads")
-    f32 = torch.float32
-    args = (
-        pgy, ldgy, gy_dt, px, ldx, x_dt, _vector(mean, "mean", T, index, f32),
-        _vector(rstd, "rstd", T, index, f32), pw, w_dt, pgr, ldgr, T, C, pgx, ldgx, gx_dt,
-        _vector(g_weight, "g_weight", C, index, f32), _vector(g_bias, "g_bias", C, index, f32),
-        pws, n_ws, _stream(None))
-    _check(lib().hlq_layer_norm_backward(*args), "hlq_layer_norm_backward")
+    rc = lib().hlq_layer_norm_backward(pgy, ldgy, gy_dt, px, ldx, x_dt, pm, ps, pw, w_dt, pgr,
+                                       ldgr, T, C, pgx, ldgx, gx_dt, pgw, pgb, pws, n_ws,
+                                       _raw_stream(index))
+    _check(rc, "hlq_layer_norm_backward")
     return out, g_weight, g_bias
 
 
-@_on_stream
-def hlq_token_logprobs(logits, targets, scale: float = 1.0, logp=None, lse=None):
+def hlq_token_logprobs(logits, targets, scale: float = 1.0, logp=None, lse=None, stream=None):
     """log softmax(scale * logits) [T, V] at targets (int64 [T]) and the rows'
     log-sum-exp: (logp, lse), fp32 [T]."""
-    torch = _torch()
+    if stream is not None:
+        return _on_stream(hlq_token_logprobs, locals())
     ld, dt, pl = _rows(logits, "logits")
     T, V = logits.shape
-    index = logits.get_device()
+    index, device = logits.get_device(), logits.device
     _need_current(index)
-    if logp is None:
-        logp = torch.empty(T, dtype=torch.float32, device=logits.device)
-    if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=logits.device)
-    args = (
-        pl, ld, dt, _vector(targets, "targets", T, index, torch.int64), T, V, scale,
-        _vector(logp, "logp", T, index, torch.float32),
-        _vector(lse, "lse", T, index, torch.float32), _stream(None))
-    _check(lib().hlq_token_logprobs(*args), "hlq_token_logprobs")
+    pt = _vector(targets, "targets", T, index, _torch().int64)
+    logp, pp = _out_vector(logp, "logp", T, index, device)
+    lse, ps = _out_vector(lse, "lse", T, index, device)
+    rc = lib().hlq_token_logprobs(pl, ld, dt, pt, T, V, scale, pp, ps, _raw_stream(index))
+    _check(rc, "hlq_token_logprobs")
     return logp, lse
 
 
-@_on_stream
 def hlq_policy_loss(logits, actions, old_logp, advantages, weights, ref_logp=None,
                     clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                     scale: float = 1.0, grad_scale: float = 1.0, with_grad: bool = True,
-                    stats=None, logp=None, out=None, ws=None):
+                    stats=None, logp=None, out=None, ws=None, stream=None):
     """Clipped policy loss with a KL term to a reference (see include/hlq.h for
     the formulas) over logits [T, V], and its gradient: (stats, logp, g).
     stats fp32 [4]: loss, policy term, KL term, clipped share of the weights;
@@ -781,89 +823,86 @@ def hlq_policy_loss(logits, actions, old_logp, advantages, weights, ref_logp=Non
     of the loss (None with with_grad=False; out=logits overwrites them).
     actions int64 [T]; old_logp, advantages, weights, ref_logp fp32 [T]; a row
     of weight 0 takes no part and is not read."""
+    if stream is not None:
+        return _on_stream(hlq_policy_loss, locals())
     torch = _torch()
     f32 = torch.float32
     ld, dt, pl = _rows(logits, "logits")
-    shape, index = logits.shape, logits.get_device()
+    shape, index, device = logits.shape, logits.get_device(), logits.device
     _need_current(index)
     T, V = shape
-    dev = logits.device
-    if stats is None:
-        stats = torch.empty(4, dtype=f32, device=dev)
-    if logp is None:
-        logp = torch.empty(T, dtype=f32, device=dev)
+    pa = _vector(actions, "actions", T, index, torch.int64)
+    po = _vector(old_logp, "old_logp", T, index, f32)
+    pr = _vector(ref_logp, "ref_logp", T, index, f32)
+    pv = _vector(advantages, "advantages", T, index, f32)
+    pw = _vector(weights, "weights", T, index, f32)
+    stats, ps = _out_vector(stats, "stats", 4, index, device)
+    logp, pp = _out_vector(logp, "logp", T, index, device)
     ldg, pg = 0, None
     if with_grad:
         if out is None:
-            out = torch.empty(shape, dtype=logits.dtype, device=dev)
-        ldg, _, pg = _rows(out, "out", shape, index, logits.dtype)
+            out = torch.empty(shape, dtype=logits.dtype, device=device)
+            ldg, _, pg = _new_rows(out, V)
+        else:
+            ldg, _, pg = _rows(out, "out", index, shape, logits.dtype)
     elif out is not None:
         raise ValueError("out is written only with with_grad")
-    if ws is None:
-        ws = torch.empty(lib().hlq_policy_loss_workspace_bytes(T, V), dtype=torch.uint8,
-                         device=dev)
-    args = (
-        pl, ld, dt, _vector(actions, "actions", T, index, torch.int64),
-        _vector(old_logp, "old_logp", T, index, f32),
-        _vector(ref_logp, "ref_logp", T, index, f32),
-        _vector(advantages, "advantages", T, index, f32),
-        _vector(weights, "weights", T, index, f32), T, V, scale, clip_low, clip_high, kl_coef,
-        grad_scale, _vector(stats, "stats", 4, index, f32),
-        _vector(logp, "logp", T, index, f32), pg, ldg, ws.data_ptr(), _ws_bytes(ws, index),
-        _stream(None))
-    _check(lib().hlq_policy_loss(*args), "hlq_policy_loss")
+    n_ws = lib().hlq_policy_loss_workspace_bytes(T, V) if ws is None else 0
+    ws, pws, n_ws = _workspace(ws, n_ws, index, device)
+    rc = lib().hlq_policy_loss(pl, ld, dt, pa, po, pr, pv, pw, T, V, scale, clip_low, clip_high,
+                               kl_coef, grad_scale, ps, pp, pg, ldg, pws, n_ws,
+                               _raw_stream(index))
+    _check(rc, "hlq_policy_loss")
     return stats, logp, out
 
 
-@_on_stream
+def _table(ts, what, index):
+    """Addresses, dtype codes and element counts of contiguous tensors on
+    device `index`, as the arrays the library takes."""
+    if not all([t.is_contiguous() for t in ts]):
+        raise ValueError(f"{what} must be contiguous CUDA tensors")
+    if {t.get_device() for t in ts} - {index}:
+        if not all([t.is_cuda for t in ts]):
+            raise ValueError(f"{what} must be contiguous CUDA tensors")
+        raise ValueError(f"{what} must be on one device")
+    return (array.array("Q", [t.data_ptr() for t in ts]),
+            array.array("i", [_code(t.dtype) for t in ts]),
+            array.array("q", [t.numel() for t in ts]))
+
+
 def hlq_clip_grad_norm(grads, max_norm: float, outs=None, norm_only: bool = False,
-                       norm_coef=None, ws=None):
+                       norm_coef=None, ws=None, stream=None):
     """Global norm of `grads` (contiguous bf16 / fp32 CUDA tensors of any
     shapes) and their clipping to max_norm: writes coef * g to `outs` (tensors
     of as many elements, bf16 or fp32), or over the gradients themselves by
     default, or nowhere with norm_only.  Returns fp32 [2]: norm, coef."""
+    if stream is not None:
+        return _on_stream(hlq_clip_grad_norm, locals())
     torch = _torch()
     grads = list(grads)
     n = len(grads)
     if norm_only and outs is not None:
         raise ValueError("norm_only writes no outs")
-    dsts = None if norm_only else grads if outs is None else list(outs)
-    if dsts is not None and len(dsts) != n:
-        raise ValueError(f"{len(dsts)} outs for {n} gradients")
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError(f"{len(outs)} outs for {n} gradients")
     index = grads[0].get_device() if n else torch.cuda.current_device()
     _need_current(index)
-    dts = {torch.float32: F32, torch.bfloat16: BF16}
-
-    def table(ts, what):
-        for t in ts:
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{what} must be contiguous CUDA tensors")
-            if t.get_device() != index:
-                raise ValueError(f"{what} must be on one device")
-            if t.dtype not in dts:
-                raise TypeError(f"unsupported dtype {t.dtype}: use bfloat16 or float32")
-        return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
-                (ctypes.c_int32 * n)(*[dts[t.dtype] for t in ts]))
-
-    numels = [t.numel() for t in grads]
-    g_ptr, g_dt = table(grads, "grads")
-    o_ptr = o_dt = None
-    if dsts is grads:
-        o_ptr, o_dt = g_ptr, g_dt
-    elif dsts is not None:
-        if [t.numel() for t in dsts] != numels:
+    g_ptr, g_dt, numels = _table(grads, "grads", index)
+    o_ptr, o_dt = (None, None) if norm_only else (g_ptr, g_dt)
+    if outs is not None:
+        o_ptr, o_dt, o_numels = _table(outs, "outs", index)
+        if o_numels != numels:
             raise ValueError("outs must have as many elements as the gradients")
-        o_ptr, o_dt = table(dsts, "outs")
-    if norm_coef is None:
-        norm_coef = torch.empty(2, dtype=torch.float32, device=f"cuda:{index}")
-    if ws is None:
-        ws = torch.empty(lib().hlq_clip_grad_norm_workspace_bytes(n), dtype=torch.uint8,
-                         device=norm_coef.device)
-    args = (
-        n, g_ptr, g_dt, o_ptr, o_dt, (ctypes.c_int64 * n)(*numels), max_norm,
-        _vector(norm_coef, "norm_coef", 2, index, torch.float32), ws.data_ptr(),
-        _ws_bytes(ws, index), _stream(None))
-    _check(lib().hlq_clip_grad_norm(*args), "hlq_clip_grad_norm")
+    device = torch.device("cuda", index)
+    norm_coef, pn = _out_vector(norm_coef, "norm_coef", 2, index, device)
+    n_ws = lib().hlq_clip_grad_norm_workspace_bytes(n) if ws is None else 0
+    ws, pws, n_ws = _workspace(ws, n_ws, index, device)
+    at = lambda a: None if a is None else a.buffer_info()[0]  # noqa: E731
+    rc = lib().hlq_clip_grad_norm(n, at(g_ptr), at(g_dt), at(o_ptr), at(o_dt), at(numels),
+                                  max_norm, pn, pws, n_ws, _raw_stream(index))
+    _check(rc, "hlq_clip_grad_norm")
     return norm_coef
 
 

@@ -20,7 +20,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libhlq.so")
 
 SOURCES = ["hlq_api.cu", "hlq_quant.cu", "hlq_gemm_simple.cu", "hlq_gemm_tc.cu",
-           "hlq_step_api.cu", "hlq_norm.cu", "hlq_loss.cu", "hlq_clip.cu",
+           "hlq_step_api.cu", "hlq_norm.cu", "hlq_norm_ring_bf16.cu",
+           "hlq_norm_ring_f32.cu", "hlq_loss.cu", "hlq_clip.cu",
            "hlq_noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

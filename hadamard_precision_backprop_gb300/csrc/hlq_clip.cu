@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads)
     clip_norm_kernel(const __grid_constant__ ClipTable tab, double* part) {
   __shared__ double red[32];
   pdl_wait();
+  pdl_trigger();
   const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
   const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
   int i = tensor_of(tab, k0);
@@ -119,7 +120,6 @@ __global__ void __launch_bounds__(kThreads)
                min((int64_t)kClipChunk, tab.numel[i] - e0), v);
     acc += sum_of_squares(v);
   }
-  pdl_trigger();
   acc = cta_sum_f64(acc, red);
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }

@@ -9,17 +9,23 @@
 //   dl/dlp = -r A [the unclipped branch holds] + beta (1 - exp(d)),
 //   g[t, v] = grad_scale w_t dl/dlp scale ([v == a] - p_v).
 //
-// A cluster of 1 to 8 CTAs holds a row in registers, 64 elements a thread:
-// the row is read once, each thread takes the maximum of its elements and the
-// sum of exp(z - maximum), these pairs are joined over the warp, the CTA and
-// (through distributed shared memory) the cluster, and the gradient is
-// computed from the registers and written.  The split depends on the row's
-// length and alignment alone, not on the number of rows or on the operator: a
-// token's log-probability has the same bits in both, so that the ratio of an
-// unchanged policy is exactly 1.
+// A row is cut into 1, 2, 4 or 8 slices; 256 threads take a slice, each up to
+// 64 elements in groups of 16, which it holds in registers, and keep a running
+// maximum and the sum of exp(z - maximum).  These pairs are joined over the
+// warp, the slice's warps and the slices, always in the same order: a token's
+// log-probability has the same bits whatever the number of rows and in both
+// operators, so that the ratio of an unchanged policy is exactly 1.
+//   policy loss: a cluster of CTAs, one for a slice, joins the slices through
+//     distributed shared memory; the gradient is computed from the registers,
+//     so that the row is read once;
+//   log-probabilities: the same where there are few rows, else one CTA takes
+//     all slices of its rows one after another, the loads of the next slice
+//     under way while one is summed.
+#include <cfloat>
 #include <type_traits>
 
 #include "hlq_device.cuh"
+#include "hlq_host.h"
 #include "hlq_kernels.h"
 #include "hlq_rows.cuh"
 #include "hlq_tma.cuh"
@@ -28,9 +34,9 @@ namespace hlq {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kHeld = 64;                      // elements a thread holds
-constexpr int kMostCtas = 8;
-constexpr int kCtaElems = kThreads * kHeld;    // elements a CTA holds
+constexpr int kGroups = 4;                          // groups of 16 elements a thread holds
+constexpr int kMostSlices = 8;
+constexpr int kSliceElems = kThreads * kGroups * 16;
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -38,112 +44,118 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// sum_i exp2(c z_i) as exp2(c m) s, m the maximum (-inf: nothing yet).
+// sum_i exp2(c z_i) as exp2(c m) s with m the maximum (-FLT_MAX and 0 before
+// the first term: then no difference below is -inf + inf).
 struct MaxSum {
   float m, s;
 };
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
   const float m = fmaxf(a.m, b.m);
-  const float fa = a.m == m ? 1.f : ex2((a.m - m) * c);
-  const float fb = b.m == m ? 1.f : ex2((b.m - m) * c);
-  return {m, a.s * fa + b.s * fb};
+  // no fma: join(a, b) and join(b, a) are the same bits
+  return {m, __fadd_rn(__fmul_rn(a.s, ex2((a.m - m) * c)), __fmul_rn(b.s, ex2((b.m - m) * c)))};
 }
 
-// exp2(c (z - m)) as exp2(fma(z, c, bias)) * fix: bias = -(c m) rounded, fix
-// the exact rest of that product, so that one fma a term loses nothing.
-struct ExpArg {
-  float bias, fix;
-};
-__device__ __forceinline__ ExpArg exp_arg(float m, float c) {
-  const float bias = -(m * c);
-  return {bias, ex2(-fmaf(m, c, bias))};
-}
-
-// One CTA's part of a row: `n` 16-byte vectors from element `e0` of the row,
-// and on the first CTA the up to 2 x 7 single elements before the first and
-// after the last vector of the row (thread j < 8: element j, j >= 8: the
-// (j - 8)th after the vectors).
+// One slice of a row: `n` 16-byte vectors from element `e0` of the row, and
+// for slice 0 the up to 2 x 7 single elements before the first and after the
+// last vector of the row (thread j < 8: element j, j >= 8: the (j - 8)th after
+// the vectors).
 template <bool kBf16>
 struct Slice {
-  static constexpr int kVec = kBf16 ? 8 : 4, kNum = kHeld / kVec;
+  static constexpr int kSize = kBf16 ? 2 : 4, kVec = 16 / kSize;
+  static constexpr int kGroup = 16 / kVec;  // vectors of a group
   const char* row;
-  int64_t e0;
+  int64_t e0, edge;  // edge: this thread's single element, -1: none
   int n;
-  int64_t edge;  // this thread's single element; -1: none
-  __device__ __forceinline__ Slice(const void* base, int64_t offset, int64_t V, int rank, int ctas) {
-    constexpr int kSize = kBf16 ? 2 : 4;
+  __device__ __forceinline__ Slice(const void* base, int64_t offset, int64_t V, int slice,
+                                   int log_slices) {
     row = static_cast<const char*>(base) + offset * kSize;
     int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / kSize;
     if (head > V) head = V;
-    const int64_t vecs = (V - head) / kVec, per = (vecs + ctas - 1) / ctas;
-    const int64_t v0 = min(rank * per, vecs), v1 = min(v0 + per, vecs);
+    const int64_t vecs = (V - head) / kVec, per = (vecs + (1 << log_slices) - 1) >> log_slices;
+    const int64_t v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
     e0 = head + v0 * kVec;
     n = (int)(v1 - v0);
     edge = -1;
-    if (rank == 0 && threadIdx.x < 16) {
+    if (slice == 0 && threadIdx.x < 16) {
       const int64_t j = threadIdx.x, after = head + vecs * kVec + j - 8;
       if (j < 8 ? j < head : after < V) edge = j < 8 ? j : after;
     }
   }
-  __device__ __forceinline__ const uint4* vec(int i) const {
-    return reinterpret_cast<const uint4*>(row + e0 * (kBf16 ? 2 : 4)) + i;
+  // vector j of the slice; -inf past its end
+  __device__ __forceinline__ uint4 vec(int j) const {
+    constexpr uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
+    if (j >= n) return make_uint4(none, none, none, none);
+    return reinterpret_cast<const uint4*>(row + e0 * kSize)[j];
   }
   __device__ __forceinline__ float elem(int64_t e) const { return load_elem(row, kBf16, e); }
 };
 
 template <bool kBf16>
-__device__ __forceinline__ void widen(uint4 r, float* v) {
+__device__ __forceinline__ void widen(uint4 r, F2* v) {
   if constexpr (kBf16) {
-    const F8 f = widen8(r);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = f.v[k];
+    v[0] = widen2(r.x), v[1] = widen2(r.y), v[2] = widen2(r.z), v[3] = widen2(r.w);
   } else {
-    v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y);
-    v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+    v[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+    v[1] = f2(__uint_as_float(r.z), __uint_as_float(r.w));
+  }
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ float max_of(uint4 r) {
+  if constexpr (kBf16) {
+    const uint32_t m = max_bf16x2(max_bf16x2(r.x, r.y), max_bf16x2(r.z, r.w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
 }
 
-// The CTA's pair over its slice, in thread 0's warp.  With kResident the
-// slice fits the registers `raw`; otherwise they are reused block by block.
-template <bool kBf16, bool kResident>
-__device__ __forceinline__ MaxSum slice_pair(const Slice<kBf16>& sl, float c, uint4* raw,
-                                             float& edge, MaxSum* warp_pair) {
-  using S = Slice<kBf16>;
-  const int tid = threadIdx.x, lane = tid & 31;
-  MaxSum p = {-INFINITY, 0.f};
-  edge = -INFINITY;
-  if (sl.edge >= 0) edge = sl.elem(sl.edge);
-  for (int b = 0; b < (kResident ? 1 : sl.n); b += S::kNum * kThreads) {
+// The running pair of a thread, the sum in two halves.
+struct Running {
+  float m = -FLT_MAX;
+  F2 s = f2(0.f);
+  // One group of 16.  The difference to the maximum comes first, so that the
+  // maximum itself counts exactly 1.
+  template <bool kBf16>
+  __device__ __forceinline__ void add(const uint4* raw, float c) {
+    using S = Slice<kBf16>;
+    float top = m;
 #pragma unroll
-    for (int i = 0; i < S::kNum; ++i) {
-      const int j = b + i * kThreads + tid;
-      if (j < sl.n) raw[i] = *sl.vec(j);
-    }
-    float m = -INFINITY;
+    for (int i = 0; i < S::kGroup; ++i) top = fmaxf(top, max_of<kBf16>(raw[i]));
+    s = s * f2(ex2((m - top) * c));
+    const F2 neg = f2(-top), c2 = f2(c);
 #pragma unroll
-    for (int i = 0; i < S::kNum; ++i) {
-      if (b + i * kThreads + tid < sl.n) {
-        float v[S::kVec];
-        widen<kBf16>(raw[i], v);
+    for (int i = 0; i < S::kGroup; ++i) {
+      F2 v[S::kVec / 2];
+      widen<kBf16>(raw[i], v);
 #pragma unroll
-        for (int k = 0; k < S::kVec; ++k) m = fmaxf(m, v[k]);
+      for (int k = 0; k < S::kVec / 2; ++k) {
+        const float2 d = split((v[k] + neg) * c2);
+        s = s + f2(ex2(d.x), ex2(d.y));
       }
     }
-    // the difference first: the maximum itself counts exactly 1
-    const float top = m == -INFINITY ? 0.f : m;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < S::kNum; ++i) {
-      if (b + i * kThreads + tid < sl.n) {
-        float v[S::kVec];
-        widen<kBf16>(raw[i], v);
-#pragma unroll
-        for (int k = 0; k < S::kVec; ++k) s += ex2((v[k] - top) * c);
-      }
-    }
-    p = kResident ? MaxSum{m, s} : join(p, {m, s}, c);
+    m = top;
   }
-  if (sl.edge >= 0) p = join(p, {edge, edge == -INFINITY ? 0.f : ex2((edge - edge) * c)}, c);
+  __device__ __forceinline__ MaxSum pair() const {
+    const float2 h = split(s);
+    return {m, h.x + h.y};
+  }
+};
+
+// The CTA's pair, in its first warp; `warp_pair` may be written again after
+// the next __syncthreads but one.
+__device__ __forceinline__ MaxSum cta_pair(MaxSum p, bool has_edge, float edge, float c,
+                                           MaxSum* warp_pair) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (has_edge) {
+    const float m = fmaxf(edge, -FLT_MAX);
+    p = join(p, {m, ex2((edge - m) * c)}, c);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     p = join(p, {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)}, c);
@@ -159,100 +171,204 @@ __device__ __forceinline__ MaxSum slice_pair(const Slice<kBf16>& sl, float c, ui
 }
 
 // The row's pair, in the first warp of every CTA of the cluster.
-__device__ __forceinline__ MaxSum row_pair(MaxSum p, float c, int rank, int ctas, MaxSum* slots) {
-  if (ctas == 1) return p;
-  if ((int)threadIdx.x < ctas) {
-    const uint32_t at = cluster_map(saddr(slots + rank), threadIdx.x);
+__device__ __forceinline__ MaxSum cluster_pair(MaxSum p, float c, int slice, int log_slices,
+                                               MaxSum* slots) {
+  if (log_slices == 0) return p;
+  if ((int)threadIdx.x < (1 << log_slices)) {
+    const uint32_t at = cluster_map(saddr(slots + slice), threadIdx.x);
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(p.m), "f"(p.s)
                  : "memory");
   }
+  __syncwarp();
   cluster_sync();
   p = slots[0];
-  for (int i = 1; i < ctas; ++i) p = join(p, slots[i], c);
+  for (int i = 1; i < (1 << log_slices); ++i) p = join(p, slots[i], c);
   return p;
+}
+
+// A CTA's part of a cluster's row.  kHeld: the slice stays in `raw`;
+// otherwise `raw` is filled again and again.
+template <bool kBf16, bool kHeld>
+__device__ __forceinline__ MaxSum slice_pair(
+    const Slice<kBf16>& sl, float c, uint4 (&raw)[kGroups][Slice<kBf16>::kGroup], float& edge,
+    MaxSum* warp_pair) {
+  using S = Slice<kBf16>;
+  edge = sl.edge >= 0 ? sl.elem(sl.edge) : 0.f;
+  Running run;
+  for (int b = 0; b < (kHeld ? 1 : sl.n); b += kGroups * S::kGroup * kThreads) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int i = 0; i < S::kGroup; ++i)
+        raw[g][i] = sl.vec(b + (g * S::kGroup + i) * kThreads + (int)threadIdx.x);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+      if (b + g * S::kGroup * kThreads < sl.n) run.add<kBf16>(raw[g], c);
+  }
+  return cta_pair(run.pair(), sl.edge >= 0, edge, c, warp_pair);
 }
 
 __device__ __forceinline__ float token_logp(float logit, MaxSum p, float scale) {
   return scale * (logit - p.m) - logf(p.s);
 }
 
-template <bool kBf16, bool kResident>
-__global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) token_logprobs_kernel(TokenLogprobs p, int ctas) {
-  __shared__ MaxSum warp_pair[kWarps], slots[kMostCtas];
-  const int rank = ctas > 1 ? (int)cluster_rank() : 0;
-  const int64_t t = blockIdx.x / ctas;
-  const float c = p.scale * 1.4426950408889634f;
+__device__ __forceinline__ void write_logprob(const TokenLogprobs& p, int64_t t, int64_t a,
+                                              float logit, MaxSum pair) {
+  const bool known = a >= 0 && a < p.V;
+  p.logp[t] = known ? token_logp(logit, pair, p.scale) : NAN;
+  const float lse = p.scale * pair.m + logf(pair.s);
+  if (p.lse) p.lse[t] = lse;
+  if (!known) raise_flag(p.status, HLQ_DEV_BADCODE);
+  if (!isfinite(lse)) raise_flag(p.status, HLQ_DEV_NONFINITE);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads) logprobs_cluster_kernel(TokenLogprobs p,
+                                                                    int log_slices) {
+  using S = Slice<kBf16>;
+  __shared__ MaxSum warp_pair[kWarps], slots[kMostSlices];
+  const int slice = blockIdx.x & ((1 << log_slices) - 1);
+  const int64_t t = blockIdx.x >> log_slices;
+  const float c = p.scale * kLog2e;
   pdl_wait();
-  const Slice<kBf16> sl(p.logits, t * p.ld, p.V, rank, ctas);
+  pdl_trigger();
+  const S sl(p.logits, t * p.ld, p.V, slice, log_slices);
   int64_t a = -1;
   float logit = 0.f;
-  if (rank == 0 && threadIdx.x == 0) {
+  if (slice == 0 && threadIdx.x == 0) {
     a = p.targets[t];
     if (a >= 0 && a < p.V) logit = sl.elem(a);
   }
-  uint4 raw[Slice<kBf16>::kNum];
+  uint4 raw[kGroups][S::kGroup];
   float edge;
-  MaxSum pair = slice_pair<kBf16, kResident>(sl, c, raw, edge, warp_pair);
-  pair = row_pair(pair, c, rank, ctas, slots);
+  MaxSum pair = slice_pair<kBf16, false>(sl, c, raw, edge, warp_pair);
+  pair = cluster_pair(pair, c, slice, log_slices, slots);
+  if (slice == 0 && threadIdx.x == 0) write_logprob(p, t, a, logit, pair);
+}
+
+// One CTA a row, slice after slice.  A group's registers are loaded with the
+// next slice's (or row's) elements as soon as the group is summed.
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
+    logprobs_stream_kernel(TokenLogprobs p, int log_slices) {
+  using S = Slice<kBf16>;
+  __shared__ MaxSum warp_pair[2][kWarps];
+  const float c = p.scale * kLog2e;
+  const int tid = threadIdx.x;
+  pdl_wait();
   pdl_trigger();
-  if (rank == 0 && threadIdx.x == 0) {
-    const bool known = a >= 0 && a < p.V;
-    p.logp[t] = known ? token_logp(logit, pair, p.scale) : NAN;
-    const float lse = p.scale * pair.m + logf(pair.s);
-    if (p.lse) p.lse[t] = lse;
-    if (!known) raise_flag(p.status, HLQ_DEV_BADCODE);
-    if (!isfinite(lse)) raise_flag(p.status, HLQ_DEV_NONFINITE);
+  int64_t t = blockIdx.x;
+  if (t >= p.T) return;
+  int slice = 0, flip = 0;
+  S sl(p.logits, t * p.ld, p.V, 0, log_slices);
+  constexpr int kStep = kGroups * S::kGroup * kThreads;
+  int b = 0;
+  uint4 raw[kGroups][S::kGroup];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+    for (int i = 0; i < S::kGroup; ++i) raw[g][i] = sl.vec((g * S::kGroup + i) * kThreads + tid);
+  float edge = sl.edge >= 0 ? sl.elem(sl.edge) : 0.f;
+  int64_t a = -1;
+  float logit = 0.f;
+  Running run;
+  MaxSum row = {-FLT_MAX, 0.f};
+  while (true) {
+    if (tid == 0 && slice == 0 && b == 0) {
+      a = p.targets[t];
+      logit = a >= 0 && a < p.V ? sl.elem(a) : 0.f;
+    }
+    // what comes after these groups: more of the slice, a slice, a row, nothing
+    const bool slice_ends = b + kStep >= sl.n;
+    const bool row_ends = slice_ends && slice + 1 == 1 << log_slices;
+    const int64_t t_next = row_ends ? t + gridDim.x : t;
+    const int slice_next = row_ends ? 0 : slice_ends ? slice + 1 : slice;
+    const int b_next = slice_ends ? 0 : b + kStep;
+    const bool more = t_next < p.T;
+    S next = sl;
+    if (slice_ends && more) next = S(p.logits, t_next * p.ld, p.V, slice_next, log_slices);
+    float edge_next = edge;
+    if (slice_ends && more && next.edge >= 0) edge_next = next.elem(next.edge);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (b + g * S::kGroup * kThreads < sl.n) run.add<kBf16>(raw[g], c);
+      if (more) {
+#pragma unroll
+        for (int i = 0; i < S::kGroup; ++i)
+          raw[g][i] = next.vec(b_next + (g * S::kGroup + i) * kThreads + tid);
+      }
+    }
+    if (slice_ends) {
+      const MaxSum pair = cta_pair(run.pair(), sl.edge >= 0, edge, c, warp_pair[flip]);
+      flip ^= 1;
+      row = slice == 0 ? pair : join(row, pair, c);
+      run = Running();
+      if (row_ends && tid == 0) write_logprob(p, t, a, logit, row);
+    }
+    if (!more) break;
+    sl = next, edge = edge_next, t = t_next, slice = slice_next, b = b_next;
   }
 }
 
-// What the first warp hands to its CTA: p_v = exp2(fma(z, c, bias)) * k, and
-// the gradient -coef p_v except at the action.
+// What the first warp hands to its CTA: the gradient -coef p_v is
+// exp2(fma(z, c, bias)) k except at the action.  bias = -(c m) is rounded; the
+// exact rest of that product is in k.
 struct RowGrad {
   float bias, k, at_action;
   int64_t action;
 };
 
 template <bool kBf16>
-__device__ __forceinline__ uint4 narrow(const float* v) {
-  if constexpr (kBf16)
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                      pack_bf16(v[6], v[7]));
-  else
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3]));
+__device__ __forceinline__ uint4 narrow(const F2* v) {
+  if constexpr (kBf16) {
+    return make_uint4(pack_bf16(v[0]), pack_bf16(v[1]), pack_bf16(v[2]), pack_bf16(v[3]));
+  } else {
+    const float2 a = split(v[0]), b = split(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                      __float_as_uint(b.y));
+  }
 }
 
-// g's rows begin at the same offset from a 16-byte boundary as the logits'
-// (kAligned), or are written element by element.
-template <bool kBf16, bool kResident, bool kAligned>
-__global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) policy_rows_kernel(PolicyLoss p, int ctas) {
+// kHeld: the slice is kept in registers between the two passes, else read
+// again.  kAligned: g's rows begin at the same offset from a 16-byte boundary
+// as the logits'; else g is written element by element.
+template <bool kBf16, bool kHeld, bool kAligned>
+__global__ void __launch_bounds__(kThreads, kBf16 ? 4 : 2)
+    policy_rows_kernel(const __grid_constant__ PolicyLoss p, int log_slices) {
   using S = Slice<kBf16>;
-  __shared__ MaxSum warp_pair[kWarps], slots[kMostCtas];
+  __shared__ MaxSum warp_pair[kWarps], slots[kMostSlices];
   __shared__ RowGrad grad;
-  const int rank = ctas > 1 ? (int)cluster_rank() : 0;
+  const int slice = blockIdx.x & ((1 << log_slices) - 1);
   const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x / ctas;
-  const float c = p.scale * 1.4426950408889634f;
+  const int64_t t = blockIdx.x >> log_slices;
+  const float c = p.scale * kLog2e;
   pdl_wait();
+  pdl_trigger();
   const float w = p.weight[t];
-  const S sl(p.logits, t * p.ld, p.V, rank, ctas);
-  char* g = static_cast<char*>(p.g) + t * p.ldg * (kBf16 ? 2 : 4);
-  auto put = [&](int j, const float* v) {
+  const S sl(p.logits, t * p.ld, p.V, slice, log_slices);
+  char* g = static_cast<char*>(p.g) + t * p.ldg * S::kSize;
+  auto put = [&](int j, const F2* v) {
     const int64_t e = sl.e0 + (int64_t)j * S::kVec;
     if constexpr (kAligned) {
-      *reinterpret_cast<uint4*>(g + e * (kBf16 ? 2 : 4)) = narrow<kBf16>(v);
+      reinterpret_cast<uint4*>(g + sl.e0 * S::kSize)[j] = narrow<kBf16>(v);
     } else {
 #pragma unroll
-      for (int k = 0; k < S::kVec; ++k) store_elem(g, kBf16, e + k, v[k]);
+      for (int k = 0; k < S::kVec / 2; ++k) {
+        const float2 x = split(v[k]);
+        store_elem(g, kBf16, e + 2 * k, x.x);
+        store_elem(g, kBf16, e + 2 * k + 1, x.y);
+      }
     }
   };
   if (w == 0.f) {  // the same for the whole cluster
     if (p.g) {
-      float zero[S::kVec] = {};
+      const F2 zero[S::kVec / 2] = {};
       for (int j = tid; j < sl.n; j += kThreads) put(j, zero);
       if (sl.edge >= 0) store_elem(g, kBf16, sl.edge, 0.f);
     }
-    if (rank == 0 && tid == 0) {
+    if (slice == 0 && tid == 0) {
       p.part[t] = p.part[p.T + t] = p.part[2 * p.T + t] = 0.f;
       if (p.logp) p.logp[t] = 0.f;
     }
@@ -266,11 +382,10 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) policy_rows_kernel(Po
     if (p.ref_logp) ref = p.ref_logp[t];
     if (a >= 0 && a < p.V) logit = sl.elem(a);
   }
-  uint4 raw[S::kNum];
+  uint4 raw[kGroups][S::kGroup];
   float edge;
-  MaxSum pair = slice_pair<kBf16, kResident>(sl, c, raw, edge, warp_pair);
-  pair = row_pair(pair, c, rank, ctas, slots);
-  pdl_trigger();
+  MaxSum pair = slice_pair<kBf16, kHeld>(sl, c, raw, edge, warp_pair);
+  pair = cluster_pair(pair, c, slice, log_slices, slots);
   if (tid < 32) {
     const bool known = a >= 0 && a < p.V;
     const float lp = known ? token_logp(logit, pair, p.scale) : NAN;
@@ -286,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) policy_rows_kernel(Po
     }
     const float coef = w * dlp * p.grad_scale * p.scale;
     if (tid == 0) {
-      const ExpArg x = exp_arg(pair.m, c);
-      grad = {x.bias, -coef * (x.fix / pair.s), -coef * expm1f(lp), a};
-      if (rank == 0) {
+      const float bias = -(pair.m * c), fix = ex2(-fmaf(pair.m, c, bias));
+      grad = {bias, -coef * (fix / pair.s), -coef * expm1f(lp), a};
+      if (slice == 0) {
         p.part[t] = w * pg;
         p.part[p.T + t] = w * kl;
         p.part[2 * p.T + t] = clipped ? w : 0.f;
@@ -301,25 +416,31 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2) policy_rows_kernel(Po
   if (!p.g) return;
   __syncthreads();
   const RowGrad gr = grad;
-  for (int b = 0; b < (kResident ? 1 : sl.n); b += S::kNum * kThreads) {
-    if constexpr (!kResident) {
+  const F2 c2 = f2(c), bias = f2(gr.bias), k2 = f2(gr.k);
+  for (int b = 0; b < (kHeld ? 1 : sl.n); b += kGroups * S::kGroup * kThreads) {
+    if constexpr (!kHeld) {
 #pragma unroll
-      for (int i = 0; i < S::kNum; ++i) {
-        const int j = b + i * kThreads + tid;
-        if (j < sl.n) raw[i] = *sl.vec(j);
-      }
+      for (int q = 0; q < kGroups; ++q)
+#pragma unroll
+        for (int i = 0; i < S::kGroup; ++i)
+          raw[q][i] = sl.vec(b + (q * S::kGroup + i) * kThreads + tid);
     }
 #pragma unroll
-    for (int i = 0; i < S::kNum; ++i) {
-      const int j = b + i * kThreads + tid;
-      if (j < sl.n) {
-        float v[S::kVec];
-        widen<kBf16>(raw[i], v);
+    for (int q = 0; q < kGroups; ++q)
 #pragma unroll
-        for (int k = 0; k < S::kVec; ++k) v[k] = ex2(fmaf(v[k], c, gr.bias)) * gr.k;
-        put(j, v);
+      for (int i = 0; i < S::kGroup; ++i) {
+        const int j = b + (q * S::kGroup + i) * kThreads + tid;
+        if (j < sl.n) {
+          F2 v[S::kVec / 2];
+          widen<kBf16>(raw[q][i], v);
+#pragma unroll
+          for (int k = 0; k < S::kVec / 2; ++k) {
+            const float2 x = split(fma2(v[k], c2, bias));
+            v[k] = f2(ex2(x.x), ex2(x.y)) * k2;
+          }
+          put(j, v);
+        }
       }
-    }
   }
   if (sl.edge >= 0) store_elem(g, kBf16, sl.edge, ex2(fmaf(edge, c, gr.bias)) * gr.k);
   // the action's element, by the thread that has just written it
@@ -352,58 +473,60 @@ __global__ void __launch_bounds__(kThreads) policy_stats_kernel(PolicyLoss p) {
   }
 }
 
-// CTAs of a row: as many (a power of two) as hold it in registers, 8 at most.
-int row_ctas(int64_t V) {
-  int n = 1;
-  while (n < kMostCtas && V > (int64_t)n * kCtaElems) n *= 2;
+// The slices of a row: as many (a power of two, 8 at most) as threads hold.
+int row_slices_log(int64_t V) {
+  int n = 0;
+  while ((1 << n) < kMostSlices && V > ((int64_t)kSliceElems << n)) ++n;
   return n;
 }
 
 template <typename P>
-cudaError_t launch_rows(void (*kernel)(P, int), const P& p, int ctas, cudaStream_t st) {
+cudaError_t launch_clusters(void (*kernel)(P, int), const P& p, int log_slices, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.T * ctas));
+  cfg.gridDim = dim3((unsigned)(p.T << log_slices));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = 1 << log_slices;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, p, ctas);
+  cfg.numAttrs = log_slices ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, log_slices);
 }
 
 }  // namespace
 
-int64_t loss_most_rows(int64_t V) { return (((int64_t)1 << 31) - 1) / row_ctas(V); }
+int64_t loss_most_rows(int64_t V) { return (((int64_t)1 << 31) - 1) >> row_slices_log(V); }
 
 cudaError_t launch_token_logprobs(const TokenLogprobs& p, cudaStream_t st) {
-  const int ctas = row_ctas(p.V);
-  const bool resident = p.V <= (int64_t)ctas * kCtaElems;
-  return launch_rows(p.bf16 ? resident ? token_logprobs_kernel<true, true>
-                                       : token_logprobs_kernel<true, false>
-                            : resident ? token_logprobs_kernel<false, true>
-                                       : token_logprobs_kernel<false, false>,
-                     p, ctas, st);
+  const int log_slices = row_slices_log(p.V), sms = device_sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  const int64_t ctas = (int64_t)sms * (p.bf16 ? 3 : 2);
+  if (p.T < ctas)
+    return launch_clusters(p.bf16 ? logprobs_cluster_kernel<true> : logprobs_cluster_kernel<false>,
+                           p, log_slices, st);
+  return launch_pdl(p.bf16 ? logprobs_stream_kernel<true> : logprobs_stream_kernel<false>,
+                    dim3((unsigned)ctas), dim3(kThreads), 0, st, p, log_slices);
 }
 
 cudaError_t launch_policy_rows(const PolicyLoss& p, cudaStream_t st) {
-  const int ctas = row_ctas(p.V);
-  const bool resident = p.V <= (int64_t)ctas * kCtaElems;
+  const int log_slices = row_slices_log(p.V);
+  const bool held = p.V <= (int64_t)kSliceElems << log_slices;
   const uint64_t size = p.bf16 ? 2 : 4;
   const bool aligned =
       (reinterpret_cast<uintptr_t>(p.g) - reinterpret_cast<uintptr_t>(p.logits)) % 16 == 0 &&
       (p.T <= 1 || (uint64_t)(p.ldg - p.ld) * size % 16 == 0);
   auto pick = [&](auto b) {
     constexpr bool kB = decltype(b)::value;
-    return resident ? aligned ? policy_rows_kernel<kB, true, true> : policy_rows_kernel<kB, true, false>
-                    : aligned ? policy_rows_kernel<kB, false, true>
-                              : policy_rows_kernel<kB, false, false>;
+    return held ? aligned ? policy_rows_kernel<kB, true, true> : policy_rows_kernel<kB, true, false>
+                : aligned ? policy_rows_kernel<kB, false, true>
+                          : policy_rows_kernel<kB, false, false>;
   };
-  return launch_rows(p.bf16 ? pick(std::true_type{}) : pick(std::false_type{}), p, ctas, st);
+  return launch_clusters(p.bf16 ? pick(std::true_type{}) : pick(std::false_type{}), p, log_slices,
+                         st);
 }
 
 cudaError_t launch_policy_stats(const PolicyLoss& p, cudaStream_t st) {

@@ -10,8 +10,8 @@
 #include "hlq_device.cuh"
 #include "hlq_host.h"
 #include "hlq_kernels.h"
+#include "hlq_norm_ring.cuh"
 #include "hlq_rows.cuh"
-#include "hlq_tma.cuh"
 
 namespace hlq {
 namespace {
@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kTeam < 128 ? 128 : kTeam) norm_fwd_kernel(Nor
   const bool live = t < p.T;
   const int C = (int)p.C;
   pdl_wait();
+  pdl_trigger();
   float v[kHeld];
 #pragma unroll
   for (int i = 0; i < kNum; ++i) {
@@ -98,7 +99,6 @@ __global__ void __launch_bounds__(kTeam < 128 ? 128 : kTeam) norm_fwd_kernel(Nor
     }
   }
   const float rstd = 1.f / sqrtf(team_sum<kTeam>(s, red[1]) / (float)C + p.eps);
-  pdl_trigger();
   if (!live) return;
 #pragma unroll
   for (int i = 0; i < kNum; ++i) {
@@ -169,198 +169,6 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(NormFwd p) 
     }
     __syncthreads();  // red[0] is written again in the next row
   }
-}
-
-// ---------------------------------------------------------------------------
-// Backward, rows of aligned groups of eight.  One CTA per SM; a team of
-// kTeam threads takes every (teams)-th row.  The rows of g_y, x and the
-// residual's gradient come into a ring of shared-memory stages by bulk
-// copies, several rows ahead; each thread owns up to kNum groups of eight
-// columns and keeps their sums for g_w and g_b in registers over all its
-// rows.  The CTA's teams add their sums in shared memory and write one slab
-// of partial sums.
-// ---------------------------------------------------------------------------
-struct RingPlan {
-  int teams, stages, stage_bytes, grid;
-  int w_bytes;  // the weights as fp32 in shared memory; 0: read from global
-  size_t smem;
-};
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(saddr(bar))
-      : "memory");
-}
-
-template <int kTeam>
-__device__ __forceinline__ void team_sync(int team) {
-  if constexpr (kTeam == 32)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam) : "memory");
-}
-
-template <int kTeam, int kNum>
-__global__ void __launch_bounds__(kTeam == 32 ? 256 : 512)
-    norm_bwd_ring_kernel(const __grid_constant__ NormBwd p, const __grid_constant__ RingPlan plan) {
-  constexpr int kWarps = kTeam / 32;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam;
-  const int lane = threadIdx.x & 31, warp = tid >> 5;
-  const int C = (int)p.C, sx = p.x_bf16 ? 2 : 4, sg = p.gy_bf16 ? 2 : 4, sr = p.gx_bf16 ? 2 : 4;
-  float* wsm = reinterpret_cast<float*>(smem);
-  unsigned char* ring0 = smem + plan.w_bytes;
-  unsigned char* ring = ring0 + (size_t)team * plan.stages * plan.stage_bytes;
-  unsigned char* tail = ring0 + (size_t)plan.teams * plan.stages * plan.stage_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(tail) + team * plan.stages;
-  float* red = reinterpret_cast<float*>(tail + 8 * plan.teams * plan.stages) + team * 2 * kWarps;
-  __shared__ int abort_flag;
-
-  if (threadIdx.x == 0) abort_flag = 0;
-  if (tid == 0)
-    for (int s = 0; s < plan.stages; ++s) mbar_init(&full[s], 1);
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  pdl_wait();
-  if (plan.w_bytes)
-    for (int c = threadIdx.x; c < C; c += blockDim.x)
-      wsm[c] = p.weight ? load_elem(p.weight, p.w_bf16, c) : 1.f;
-  __syncthreads();
-
-  const int64_t step = (int64_t)gridDim.x * plan.teams;
-  const int64_t t0 = (int64_t)blockIdx.x * plan.teams + team;
-  auto issue = [&](int64_t t, int s) {
-    if (t >= p.T || *(volatile int*)&abort_flag) return;
-    const uint32_t dst = saddr(ring + (size_t)s * plan.stage_bytes);
-    mbar_expect_tx(&full[s], (uint32_t)plan.stage_bytes);
-    bulk_load(dst, static_cast<const char*>(p.x) + t * p.ldx * sx, C * sx, &full[s]);
-    bulk_load(dst + C * sx, static_cast<const char*>(p.gy) + t * p.ldgy * sg, C * sg, &full[s]);
-    if (p.gres)
-      bulk_load(dst + C * (sx + sg), static_cast<const char*>(p.gres) + t * p.ldgr * sr, C * sr,
-                &full[s]);
-  };
-  if (tid == 0)
-    for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
-
-  float gw[kNum * 8], gb[kNum * 8];
-#pragma unroll
-  for (int i = 0; i < kNum * 8; ++i) gw[i] = gb[i] = 0.f;
-  const float inv = 1.f / (float)C;
-  int stage = 0;
-  uint32_t parity = 0;
-  float mean = 0.f, rstd = 0.f;
-  if (t0 < p.T) mean = p.mean[t0], rstd = p.rstd[t0];
-  for (int64_t t = t0; t < p.T; t += step) {
-    float mean_next = 0.f, rstd_next = 0.f;
-    if (t + step < p.T) mean_next = p.mean[t + step], rstd_next = p.rstd[t + step];
-    mbar_wait(&full[stage], parity, &abort_flag, p.status);
-    const unsigned char* row = ring + (size_t)stage * plan.stage_bytes;
-    auto weights = [&](int c) {
-      if (plan.w_bytes) {
-        const float4* q = reinterpret_cast<const float4*>(wsm + c);
-        return join8(q[0], q[1]);
-      }
-      return p.weight ? load8(p.weight, p.w_bf16, c)
-                      : F8{{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}};
-    };
-    float sa = 0.f, sx_ = 0.f;
-#pragma unroll
-    for (int i = 0; i < kNum; ++i) {
-      const int c = (i * kTeam + tid) * 8;
-      if (c < C) {
-        const F8 x = load8(row, p.x_bf16, c), g = load8(row + C * sx, p.gy_bf16, c);
-        const F8 w = weights(c);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xhat = (x.v[k] - mean) * rstd, a = g.v[k] * w.v[k];
-          sa += a;
-          sx_ = fmaf(a, xhat, sx_);
-          gw[i * 8 + k] = fmaf(g.v[k], xhat, gw[i * 8 + k]);
-          gb[i * 8 + k] += g.v[k];
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sa += __shfl_xor_sync(0xffffffffu, sa, o);
-      sx_ += __shfl_xor_sync(0xffffffffu, sx_, o);
-    }
-    if constexpr (kWarps > 1) {
-      if (lane == 0) red[warp] = sa, red[kWarps + warp] = sx_;
-      team_sync<kTeam>(team);  // read again only after the sync at the row's end
-      sa = sx_ = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) sa += red[i], sx_ += red[kWarps + i];
-    }
-    sa *= inv;
-    sx_ *= inv;
-#pragma unroll
-    for (int i = 0; i < kNum; ++i) {
-      const int c = (i * kTeam + tid) * 8;
-      if (c < C) {
-        const F8 x = load8(row, p.x_bf16, c), g = load8(row + C * sx, p.gy_bf16, c);
-        const F8 w = weights(c);
-        F8 o;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          o.v[k] = rstd * (fmaf(g.v[k], w.v[k], -sa) - (x.v[k] - mean) * rstd * sx_);
-        if (p.gres) {
-          const F8 r = load8(row + C * (sx + sg), p.gx_bf16, c);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o.v[k] += r.v[k];
-        }
-        store8(p.gx, p.gx_bf16, t * p.ldgx + c, o);
-      }
-    }
-    if (tid == 0 && (!isfinite(sa) || !isfinite(sx_))) raise_flag(p.status, HLQ_DEV_NONFINITE);
-    team_sync<kTeam>(team);  // the stage has been read by the whole team
-    if (tid == 0) issue(t + plan.stages * step, stage);
-    mean = mean_next, rstd = rstd_next;
-    if (++stage == plan.stages) stage = 0, parity ^= 1;
-  }
-  pdl_trigger();
-  if (!p.part) return;
-  float* slab = p.part + (size_t)blockIdx.x * 2 * p.C;
-  if (plan.teams == 1) {
-#pragma unroll
-    for (int i = 0; i < kNum; ++i) {
-      const int c = (i * kTeam + tid) * 8;
-      if (c < C) {
-        F8 a, b;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a.v[k] = gw[i * 8 + k], b.v[k] = gb[i * 8 + k];
-        store8(slab, false, c, a);
-        store8(slab, false, C + c, b);
-      }
-    }
-    return;
-  }
-  // every copy has been waited for by its team: the ring is free
-  float* sum = reinterpret_cast<float*>(ring0);
-  for (int k = 0; k < plan.teams; ++k) {
-    __syncthreads();
-    if (team != k) continue;
-#pragma unroll
-    for (int i = 0; i < kNum; ++i) {
-      const int c = (i * kTeam + tid) * 8;
-      if (c < C) {
-        F8 a, b;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a.v[j] = gw[i * 8 + j], b.v[j] = gb[i * 8 + j];
-        if (k > 0) {
-          const F8 a0 = load8(sum, false, c), b0 = load8(sum, false, C + c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) a.v[j] += a0.v[j], b.v[j] += b0.v[j];
-        }
-        store8(sum, false, c, a);
-        store8(sum, false, C + c, b);
-      }
-    }
-  }
-  __syncthreads();
-  for (int c = threadIdx.x * 4; c < 2 * C; c += blockDim.x * 4)
-    *reinterpret_cast<float4*>(slab + c) = *reinterpret_cast<const float4*>(sum + c);
 }
 
 // ---------------------------------------------------------------------------
@@ -438,46 +246,6 @@ __global__ void __launch_bounds__(256) norm_bwd_join_kernel(NormBwd p, int slabs
   }
 }
 
-constexpr size_t kSmemMost = 227 * 1024 - 256;  // what the static part leaves
-
-// The ring's shape: as many stages as fit (at most 8, and no more than a team
-// has rows); the weights in shared memory unless they would leave one stage.
-// False: the rows do not fit.
-bool ring_plan(const NormBwd& p, int team_threads, int most_teams, int sms, RingPlan* out) {
-  RingPlan r{};
-  const int64_t C = p.C;
-  const int64_t size = (p.x_bf16 ? 2 : 4) + (p.gy_bf16 ? 2 : 4) + (p.gres ? (p.gx_bf16 ? 2 : 4) : 0);
-  r.stage_bytes = (int)(C * size);
-  const int64_t per_sm = (p.T + sms - 1) / sms;
-  r.teams = (int)(per_sm < most_teams ? per_sm : most_teams);
-  r.grid = (int)((p.T + r.teams - 1) / r.teams < sms ? (p.T + r.teams - 1) / r.teams : sms);
-  const int64_t rows = (p.T + (int64_t)r.grid * r.teams - 1) / ((int64_t)r.grid * r.teams);
-  const int64_t most = rows < 8 ? rows : 8;
-  const size_t fixed = 8 * 8 * r.teams + 8 * r.teams * (team_threads / 32);
-  for (int with_w = 1; with_w >= 0; --with_w) {
-    r.w_bytes = with_w ? (int)(C * 4) : 0;
-    if (fixed + r.w_bytes >= kSmemMost) continue;
-    const int64_t fit = (int64_t)(kSmemMost - fixed - r.w_bytes) / ((int64_t)r.stage_bytes * r.teams);
-    r.stages = (int)(fit < most ? fit : most);
-    if (r.stages >= (with_w && most > 1 ? 2 : 1)) break;
-  }
-  if (r.stages < 1) return false;
-  size_t ring = (size_t)r.stages * r.stage_bytes * r.teams;
-  r.smem = fixed + r.w_bytes + ring;
-  // the teams' sums are added in the ring
-  if (r.teams > 1 && ring < (size_t)C * 8) r.smem += (size_t)C * 8 - ring;
-  *out = r;
-  return r.smem <= kSmemMost;
-}
-
-template <int kTeam, int kNum>
-cudaError_t launch_ring(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
-  const cudaError_t e = allow_smem<norm_bwd_ring_kernel<kTeam, kNum>>(kSmemMost);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(norm_bwd_ring_kernel<kTeam, kNum>, dim3(r.grid), dim3(kTeam * r.teams), r.smem,
-                    st, p, r);
-}
-
 template <bool kXBf16>
 cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
   auto go = [&](auto kernel, int team) {
@@ -500,7 +268,41 @@ cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
 
 }  // namespace
 
-int norm_bwd_most_slabs(int64_t T) { return (int)(T < 256 ? (T < 1 ? 1 : T) : 256); }
+int norm_bwd_most_slabs(int64_t T) { return (int)(T < kMostSlabs ? (T < 1 ? 1 : T) : kMostSlabs); }
+
+// The ring's shape: as many stages as fit (at most 8, and no more than a team
+// has rows).  False: the rows are not for the ring, or do not fit.
+bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out) {
+  if (sms <= 0 || p.C > 512 * kMostUnits * 4 || !rows_of_eight(p.x, p.ldx, p.x_bf16, p.T, p.C) ||
+      !rows_of_eight(p.gy, p.ldgy, p.gy_bf16, p.T, p.C) ||
+      !rows_of_eight(p.gres, p.ldgr, p.gx_bf16, p.T, p.C) ||
+      !rows_of_eight(p.gx, p.ldgx, p.gx_bf16, p.T, p.C) ||
+      !rows_of_eight(p.weight, 0, p.w_bf16, 1, p.C))
+    return false;
+  if (sms > kMostSlabs) sms = kMostSlabs;
+  RingPlan r{};
+  const int64_t C = p.C;
+  r.team = C <= 32 * kMostUnits * 4 ? 32 : C <= 128 * kMostUnits * 4 ? 128 : 512;
+  const int most_teams = r.team == 32 ? 8 : r.team == 128 ? 4 : 1;
+  r.units = (int)((C + r.team * 4 - 1) / (r.team * 4));
+  r.stage_bytes =
+      (int)(C * ((p.x_bf16 ? 2 : 4) + (p.gy_bf16 ? 2 : 4) + (p.gres ? (p.gx_bf16 ? 2 : 4) : 0)));
+  const int64_t per_sm = (p.T + sms - 1) / sms;
+  r.teams = (int)(per_sm < most_teams ? per_sm : most_teams);
+  const int64_t ctas = (p.T + r.teams - 1) / r.teams;
+  r.grid = (int)(ctas < sms ? ctas : sms);
+  const int64_t rows = (p.T + (int64_t)r.grid * r.teams - 1) / ((int64_t)r.grid * r.teams);
+  const size_t fixed = 8 * 8 * r.teams + 8 * r.teams * (r.team / 32);
+  int64_t fit = (int64_t)(kRingSmem - fixed) / ((int64_t)r.stage_bytes * r.teams);
+  if (fit > 8) fit = 8;
+  r.stages = (int)(fit < rows ? fit : rows);
+  if (r.stages < 1) return false;
+  size_t ring = (size_t)r.stages * r.stage_bytes * r.teams;
+  if (r.teams > 1 && ring < (size_t)C * 8) ring = (size_t)C * 8;  // the teams' sums are added there
+  r.smem = fixed + ring;
+  *out = r;
+  return r.smem <= kRingSmem;
+}
 
 cudaError_t launch_norm_fwd(const NormFwd& p, cudaStream_t st) {
   const bool eight = rows_of_eight(p.x, p.ldx, p.x_bf16, p.T, p.C) &&
@@ -513,25 +315,10 @@ cudaError_t launch_norm_fwd(const NormFwd& p, cudaStream_t st) {
 }
 
 cudaError_t launch_norm_bwd(const NormBwd& p, int* slabs, cudaStream_t st) {
-  const bool eight = rows_of_eight(p.x, p.ldx, p.x_bf16, p.T, p.C) &&
-                     rows_of_eight(p.gy, p.ldgy, p.gy_bf16, p.T, p.C) &&
-                     rows_of_eight(p.gres, p.ldgr, p.gx_bf16, p.T, p.C) &&
-                     rows_of_eight(p.gx, p.ldgx, p.gx_bf16, p.T, p.C) &&
-                     rows_of_eight(p.weight, 0, p.w_bf16, 1, p.C);
-  int sms = device_sm_count();
-  if (sms <= 0) return cudaErrorUnknown;
-  if (sms > 256) sms = 256;
   RingPlan r;
-  const int team = p.C <= 1024 ? 32 : p.C <= 4096 ? 128 : 512;
-  if (eight && p.C <= 512 * 32 && ring_plan(p, team, team == 32 ? 8 : team == 128 ? 4 : 1, sms, &r)) {
+  if (norm_bwd_ring_plan(p, device_sm_count(), &r)) {
     *slabs = r.grid;
-    const int num = (int)((p.C + team * 8 - 1) / (team * 8));
-#define RING(TEAM, NUM) \
-  if (team == TEAM && num == NUM) return launch_ring<TEAM, NUM>(p, r, st)
-    RING(32, 1); RING(32, 2); RING(32, 3); RING(32, 4);
-    RING(128, 2); RING(128, 3); RING(128, 4);
-    RING(512, 2); RING(512, 3); RING(512, 4);
-#undef RING
+    return p.x_bf16 ? launch_norm_bwd_ring_bf16(p, r, st) : launch_norm_bwd_ring_f32(p, r, st);
   }
   if (p.part) {
     *slabs = (int)(p.T < 128 ? p.T : 128);

@@ -1,0 +1,23 @@
+// hlq_norm_ring.cuh -- the layer norm's backward pass over rows of aligned
+// groups of eight elements: the plan that host and kernel share, and the
+// launchers, one file for each type of x.
+#pragma once
+
+#include "hlq_kernels.h"
+
+namespace hlq {
+
+constexpr int kMostUnits = 8;    // groups of four columns a thread owns
+constexpr int kMostSlabs = 256;  // CTAs of the ring, and slabs of partial sums
+constexpr size_t kRingSmem = 227 * 1024 - 256;  // what the static part leaves
+
+struct RingPlan {
+  int team, units;  // threads of a team, groups of four columns of each
+  int teams, stages, stage_bytes, grid;
+  size_t smem;
+};
+bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out);
+cudaError_t launch_norm_bwd_ring_bf16(const NormBwd& p, const RingPlan& r, cudaStream_t st);
+cudaError_t launch_norm_bwd_ring_f32(const NormBwd& p, const RingPlan& r, cudaStream_t st);
+
+}  // namespace hlq

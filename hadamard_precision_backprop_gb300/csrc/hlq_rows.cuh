@@ -49,6 +49,67 @@ __device__ __forceinline__ void store8(void* p, bool bf16, int64_t i, const F8& 
   }
 }
 
+// Two fp32 in one register pair: one instruction for both.
+struct F2 {
+  unsigned long long b;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.b));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+  return r;
+}
+__device__ __forceinline__ F2 widen2(uint32_t pair) { return f2(bf16_lo(pair), bf16_hi(pair)); }
+__device__ __forceinline__ uint32_t pack_bf16(F2 a) {
+  const float2 v = split(a);
+  return pack_bf16(v.x, v.y);
+}
+
+// Four consecutive elements (aligned to four): one access of 8 bytes of bf16
+// or 16 of fp32.
+struct Quad {
+  F2 v[2];
+};
+template <bool kBf16>
+__device__ __forceinline__ Quad load4(const void* p, int64_t i) {
+  if constexpr (kBf16) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    return {{widen2(r.x), widen2(r.y)}};
+  } else {
+    const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(static_cast<const float*>(p) + i);
+    return {{{r.x}, {r.y}}};
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ void store4(void* p, int64_t i, const Quad& q) {
+  if constexpr (kBf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+        make_uint2(pack_bf16(q.v[0]), pack_bf16(q.v[1]));
+  else
+    *reinterpret_cast<ulonglong2*>(static_cast<float*>(p) + i) =
+        make_ulonglong2(q.v[0].b, q.v[1].b);
+}
+
 __device__ __forceinline__ float load_elem(const void* p, bool bf16, int64_t i) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
               : static_cast<const float*>(p)[i];
