@@ -3,7 +3,9 @@
 The compute lives in ``libhlq.so`` (hand-written sm_103a CUDA behind the C
 ABI of ``include/hlq.h``); this module is the thin Python binding: it
 marshals torch tensors to pointers, allocates outputs and workspaces with
-torch, and passes torch's current CUDA stream.  Every step of the path runs
+torch, and passes torch's current CUDA stream.  The operators around the layer
+do the same in an extension module (``csrc/hlq_torch.cpp``) where a call's
+arguments are all in order.  Every step of the path runs
 in libhlq's kernels; there is no CPU or PyTorch fallback, and loading fails
 loudly when the library has not been built.
 
@@ -23,6 +25,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -608,6 +611,25 @@ def hlq_ablation_gx_hla(g_y, w, rank: int = 8, block: int = 16, with_acc: bool =
 # Around the layer in a training step
 # ----------------------------------------------------------------------------
 
+_ext = None
+
+
+def _load_ext():
+    """The extension module that checks, allocates and calls in one step: what
+    it does not take at once, or the library refuses, it answers with
+    NotImplemented, and the entry point goes on in Python."""
+    global _ext
+    _torch()
+    path = os.path.join(os.path.dirname(LIB_PATH), "_hlq_torch.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"the binding's extension is not built ({path} missing); run "
+                           "`python -m hadamard_precision_backprop_gb300.build`")
+    spec = importlib.util.spec_from_file_location("_hlq_torch", path)
+    _ext = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_ext)
+    return _ext
+
+
 def _on_stream(call, args):
     """`call` with the keyword arguments `args`, their stream current: what it
     allocates (outputs, workspace) then belongs to the stream that uses it."""
@@ -710,6 +732,11 @@ def hlq_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None,
     with with_stats=False.  x, residual, out and h may have any row stride."""
     if stream is not None:
         return _on_stream(hlq_layer_norm, locals())
+    if out is None and h is None and mean is None and rstd is None:
+        got = (_ext or _load_ext()).layer_norm(x, weight, bias, eps, residual, out_dtype,
+                                               with_stats)
+        if got is not NotImplemented:
+            return got
     torch = _torch()
     ldx, dt, px = _rows(x, "x")
     shape, index, device = x.shape, x.get_device(), x.device
@@ -759,6 +786,11 @@ def hlq_layer_norm_backward(g_y, x, mean, rstd, weight=None, g_residual=None, ou
     None with with_weight_grads=False."""
     if stream is not None:
         return _on_stream(hlq_layer_norm_backward, locals())
+    if out is None and g_weight is None and g_bias is None and ws is None:
+        got = (_ext or _load_ext()).layer_norm_backward(g_y, x, mean, rstd, weight, g_residual,
+                                                        out_dtype, with_weight_grads)
+        if got is not NotImplemented:
+            return got
     torch = _torch()
     f32 = torch.float32
     ldx, x_dt, px = _rows(x, "x")
@@ -800,6 +832,10 @@ def hlq_token_logprobs(logits, targets, scale: float = 1.0, logp=None, lse=None,
     log-sum-exp: (logp, lse), fp32 [T]."""
     if stream is not None:
         return _on_stream(hlq_token_logprobs, locals())
+    if logp is None and lse is None:
+        got = (_ext or _load_ext()).token_logprobs(logits, targets, scale)
+        if got is not NotImplemented:
+            return got
     ld, dt, pl = _rows(logits, "logits")
     T, V = logits.shape
     index, device = logits.get_device(), logits.device
@@ -825,6 +861,12 @@ def hlq_policy_loss(logits, actions, old_logp, advantages, weights, ref_logp=Non
     of weight 0 takes no part and is not read."""
     if stream is not None:
         return _on_stream(hlq_policy_loss, locals())
+    if stats is None and logp is None and out is None and ws is None:
+        got = (_ext or _load_ext()).policy_loss(logits, actions, old_logp, advantages, weights,
+                                                ref_logp, clip_low, clip_high, kl_coef, scale,
+                                                grad_scale, with_grad)
+        if got is not NotImplemented:
+            return got
     torch = _torch()
     f32 = torch.float32
     ld, dt, pl = _rows(logits, "logits")
@@ -878,8 +920,12 @@ def hlq_clip_grad_norm(grads, max_norm: float, outs=None, norm_only: bool = Fals
     default, or nowhere with norm_only.  Returns fp32 [2]: norm, coef."""
     if stream is not None:
         return _on_stream(hlq_clip_grad_norm, locals())
-    torch = _torch()
     grads = list(grads)
+    if norm_coef is None and ws is None:
+        got = (_ext or _load_ext()).clip_grad_norm(grads, max_norm, outs, norm_only)
+        if got is not NotImplemented:
+            return got
+    torch = _torch()
     n = len(grads)
     if norm_only and outs is not None:
         raise ValueError("norm_only writes no outs")

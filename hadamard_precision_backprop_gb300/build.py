@@ -1,8 +1,9 @@
-"""Build libhlq.so (the CUDA kernels + C ABI) in-tree for sm_103a with nvcc.
+"""Build libhlq.so (the CUDA kernels + C ABI) in-tree for sm_103a with nvcc,
+and the binding's extension module (host code against torch's headers).
 
 Run ``python -m hadamard_precision_backprop_gb300.build`` or call
-``build()``.  Translation units compile in parallel; the shared library is
-written to ``hadamard_precision_backprop_gb300/_build/libhlq.so``.
+``build()``.  Translation units compile in parallel; the shared libraries are
+written to ``hadamard_precision_backprop_gb300/_build/``.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libhlq.so")
+EXT = os.path.join(OUT_DIR, "_hlq_torch.so")
 
 SOURCES = ["hlq_api.cu", "hlq_quant.cu", "hlq_gemm_simple.cu", "hlq_gemm_tc.cu",
            "hlq_step_api.cu", "hlq_norm.cu", "hlq_norm_ring_bf16.cu",
@@ -39,6 +41,35 @@ def _flags():
                    "--expt-relaxed-constexpr"]
 
 
+def _build_ext(link_after) -> None:
+    """Compile the extension module; it is linked against libhlq.so (found
+    beside it) once `link_after` has returned."""
+    import sysconfig
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cxx = shutil.which("g++") or "g++"
+    obj, tmp = os.path.join(OUT_DIR, "hlq_torch.o"), EXT + f".tmp{os.getpid()}"
+    inc = [os.path.join(top, "include"), sysconfig.get_paths()["include"],
+           os.path.join(cuda, "include"), INCLUDE]
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[a for d in inc for a in ("-isystem", d)],
+          "-c", os.path.join(CSRC, "hlq_torch.cpp"), "-o", obj], "g++")
+    link_after()
+    libs = os.path.join(top, "lib")
+    _run([cxx, "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lhlq", "-Wl,-rpath,$ORIGIN",
+          "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+          "-ltorch", "-lc10_cuda", "-lc10"], "link of the extension")
+    os.replace(tmp, EXT)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "hlq.h"))
@@ -46,30 +77,33 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
+                         for f in (LIB, EXT)):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
         cmd = [nvcc] + _flags() + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        _run(cmd, f"nvcc on {src}")
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        objs = [ex.submit(compile_one, src) for src in SOURCES]
+        linked = cf.Future()
+        ext = ex.submit(_build_ext, linked.result)
+        try:
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run([nvcc] + ARCH + ["-shared", "-o", tmp] + [o.result() for o in objs], "link")
+            os.replace(tmp, LIB)
+        except BaseException as e:
+            linked.set_exception(e)
+            raise
+        linked.set_result(None)
+        ext.result()
     return LIB
 
 

@@ -124,30 +124,40 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
-__global__ void __launch_bounds__(kThreads)
-    clip_coef_kernel(const double* part, int n_part, float max_norm, float* norm_coef,
-                     unsigned int* status) {
+// The coefficient from the partial sums, in every thread of the CTA; the one
+// CTA with `write` also writes norm and coefficient.
+__device__ __forceinline__ float clip_coef(const ClipSums& q, bool write, double* red) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < q.n; i += kThreads) s += ld_dep_f64(q.part + i);
+  s = cta_sum_f64(s, red);
+  const float norm = (float)sqrt(s);
+  float coef = q.max_norm / (norm + 1e-6f);
+  coef = coef > 1.f ? 1.f : coef;  // a NaN stays
+  if (write && threadIdx.x == 0) {
+    q.norm_coef[0] = norm;
+    q.norm_coef[1] = coef;
+    if (!isfinite(norm)) raise_flag(q.status, HLQ_DEV_NONFINITE);
+  }
+  return coef;
+}
+
+// The norm and the coefficient alone.
+__global__ void __launch_bounds__(kThreads) clip_coef_kernel(ClipSums q) {
   __shared__ double red[32];
   pdl_wait();
-  pdl_trigger();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n_part; i += kThreads) s += ld_dep_f64(part + i);
-  s = cta_sum_f64(s, red);
-  if (threadIdx.x == 0) {
-    const float norm = (float)sqrt(s);
-    const float c = max_norm / (norm + 1e-6f);
-    norm_coef[0] = norm;
-    norm_coef[1] = c > 1.f ? 1.f : c;  // a NaN stays
-    if (!isfinite(norm)) raise_flag(status, HLQ_DEV_NONFINITE);
-  }
+  clip_coef(q, true, red);
 }
 
 // The runs and their chunks in the opposite order of the norm's pass: what
-// that pass read last is still in L2.
+// that pass read last is still in L2.  Each CTA adds the partial sums itself
+// (a few thousand at most, from L2), which costs less than a launch between.
 __global__ void __launch_bounds__(kThreads)
-    clip_scale_kernel(const __grid_constant__ ClipTable tab, const float* norm_coef) {
+    clip_scale_kernel(const __grid_constant__ ClipTable tab, const __grid_constant__ ClipSums q,
+                      int first) {
+  __shared__ double red[32];
   pdl_wait();
-  const float coef = ld_dep_f32(norm_coef + 1);
+  pdl_trigger();
+  const float coef = clip_coef(q, first && blockIdx.x == 0, red);
   const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
   const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
   if (k1 == k0) return;
@@ -201,15 +211,13 @@ cudaError_t launch_clip_norm(const ClipTable& tab, double* part, int grid, cudaS
   return launch_pdl(clip_norm_kernel, dim3(grid), dim3(kThreads), 0, st, tab, part);
 }
 
-cudaError_t launch_clip_coef(const double* part, int n_part, float max_norm, float* norm_coef,
-                             unsigned int* status, cudaStream_t st) {
-  return launch_pdl(clip_coef_kernel, dim3(1), dim3(kThreads), 0, st, part, n_part, max_norm,
-                    norm_coef, status);
+cudaError_t launch_clip_coef(const ClipSums& q, cudaStream_t st) {
+  return launch_pdl(clip_coef_kernel, dim3(1), dim3(kThreads), 0, st, q);
 }
 
-cudaError_t launch_clip_scale(const ClipTable& tab, const float* norm_coef, int grid,
+cudaError_t launch_clip_scale(const ClipTable& tab, const ClipSums& q, bool first, int grid,
                               cudaStream_t st) {
-  return launch_pdl(clip_scale_kernel, dim3(grid), dim3(kThreads), 0, st, tab, norm_coef);
+  return launch_pdl(clip_scale_kernel, dim3(grid), dim3(kThreads), 0, st, tab, q, first ? 1 : 0);
 }
 
 }  // namespace hlq

@@ -37,11 +37,13 @@ size_t norm_bwd_ws(int64_t T, int64_t C) {
 
 size_t policy_ws(int64_t T) { return align_up((size_t)(T > 0 ? T : 1) * 3 * 4); }
 
-// Partial sums of one clip_norm launch (its grid is smaller).
-constexpr int kClipParts = 1024;
+// Partial sums of a clipping call: every CTA that scales adds them all, so
+// they are few, and each launch over up to kClipTensors tensors gets its share.
+constexpr int64_t kClipParts = 4096;
+int64_t clip_launches(int64_t n) { return n > 0 ? (n + kClipTensors - 1) / kClipTensors : 1; }
 size_t clip_ws(int64_t n) {
-  const size_t launches = n > 0 ? (size_t)(n + kClipTensors - 1) / kClipTensors : 1;
-  return align_up(launches * kClipParts * sizeof(double));
+  const int64_t parts = 1024 * clip_launches(n);
+  return (size_t)(parts < kClipParts ? parts : kClipParts) * sizeof(double);
 }
 
 }  // namespace
@@ -212,6 +214,7 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
                               const int64_t* h_numels, float max_norm, float* d_norm_coef,
                               void* d_ws, size_t ws_bytes, void* stream) {
   if (n < 0 || !(max_norm >= 0.f) || !d_norm_coef) return HLQ_ERR_INVALID_ARG;
+  if (clip_launches(n) > kClipParts) return HLQ_ERR_UNSUPPORTED;
   if (n > 0 && (!h_grads || !h_grad_dts || !h_numels)) return HLQ_ERR_INVALID_ARG;
   if (n > 0 && h_outs && !h_out_dts) return HLQ_ERR_INVALID_ARG;
   if (!aligned_to(d_norm_coef, 4)) return HLQ_ERR_ALIGN;
@@ -232,6 +235,7 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
   if (!status || sms <= 0) return HLQ_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* part = static_cast<double*>(d_ws);
+  const int64_t parts_each = (int64_t)(clip_ws(n) / sizeof(double)) / clip_launches(n);
   int n_part = 0;
   ClipTable tab;
   // the tensors from i0 on that fill one table; returns the next i0
@@ -260,17 +264,22 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
     i = fill(i);
     if (tab.n == 0) continue;
     int grid = clip_grid(tab.chunks, sms);
-    if (grid > kClipParts) grid = kClipParts;
+    if (grid > parts_each) grid = (int)parts_each;
     HLQ_LAUNCH("clip_norm", s, launch_clip_norm(tab, part + n_part, grid, s));
     n_part += grid;
   }
-  HLQ_LAUNCH("clip_coef", s, launch_clip_coef(part, n_part, max_norm, d_norm_coef, status, s));
-  if (!h_outs) return HLQ_OK;
+  const ClipSums q = {part, n_part, max_norm, d_norm_coef, status};
+  if (!h_outs || n_part == 0) {
+    HLQ_LAUNCH("clip_coef", s, launch_clip_coef(q, s));
+    return HLQ_OK;
+  }
+  bool first = true;
   for (int64_t i = 0; i < n;) {
     i = fill(i);
     if (tab.n == 0) continue;
-    int grid = clip_grid(tab.chunks, sms);
-    HLQ_LAUNCH("clip_scale", s, launch_clip_scale(tab, d_norm_coef, grid, s));
+    const int grid = clip_grid(tab.chunks, sms);
+    HLQ_LAUNCH("clip_scale", s, launch_clip_scale(tab, q, first, grid, s));
+    first = false;
   }
   return HLQ_OK;
 }
