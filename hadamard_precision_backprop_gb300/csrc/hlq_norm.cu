@@ -381,8 +381,6 @@ cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
 
 }  // namespace
 
-int norm_bwd_most_slabs(int64_t T) { return (int)(T < kMostSlabs ? (T < 1 ? 1 : T) : kMostSlabs); }
-
 // The ring's shape: as many stages as fit (at most 8, and no more than a team
 // has rows).  False: the rows are not for the ring, or do not fit.
 bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out) {
@@ -392,30 +390,36 @@ bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out) {
       !rows_of_eight(p.gx, p.ldgx, p.gx_bf16, p.T, p.C) ||
       !rows_of_eight(p.weight, 0, p.w_bf16, 1, p.C))
     return false;
-  if (sms > kMostSlabs) sms = kMostSlabs;
   RingPlan r{};
   const int64_t C = p.C;
-  r.team = C <= 32 * kMostUnits * 4 ? 32 : C <= 128 * kMostUnits * 4 ? 128 : 512;
-  const int most_teams = r.team == 32 ? 8 : r.team == 128 ? 4 : 1;
+  r.team = C <= 32 * kMostUnits * 4 ? 32 : C <= 2048 ? 128 : C <= 4096 ? 256 : 512;
+  const int per_sm = r.team == 32 ? 1 : 512 / r.team;
+  if (sms * per_sm > kMostSlabs) sms = kMostSlabs / per_sm;
+  // of the SM's 228 KB a CTA takes 1 KB more than it asks for
+  r.smem_most = (size_t)(228 / per_sm - 1) * 1024 - 256;
   r.units = (int)((C + r.team * 4 - 1) / (r.team * 4));
   r.stage_bytes =
       (int)(C * ((p.x_bf16 ? 2 : 4) + (p.gy_bf16 ? 2 : 4) + (p.gres ? (p.gx_bf16 ? 2 : 4) : 0)));
-  const int64_t per_sm = (p.T + sms - 1) / sms;
-  r.teams = (int)(per_sm < most_teams ? per_sm : most_teams);
+  const int64_t ctas_most = (int64_t)sms * per_sm, rows_each = (p.T + ctas_most - 1) / ctas_most;
+  const int teams_most = ring_threads(r.team, r.units) / r.team;
+  r.teams = (int)(rows_each < teams_most ? rows_each : teams_most);
   const int64_t ctas = (p.T + r.teams - 1) / r.teams;
-  r.grid = (int)(ctas < sms ? ctas : sms);
+  r.grid = (int)(ctas < ctas_most ? ctas : ctas_most);
   const int64_t rows = (p.T + (int64_t)r.grid * r.teams - 1) / ((int64_t)r.grid * r.teams);
   const size_t fixed = 8 * 8 * r.teams + 8 * r.teams * (r.team / 32);
-  int64_t fit = (int64_t)(kRingSmem - fixed) / ((int64_t)r.stage_bytes * r.teams);
+  int64_t fit = (int64_t)(r.smem_most - fixed) / ((int64_t)r.stage_bytes * r.teams);
   if (fit > 8) fit = 8;
   r.stages = (int)(fit < rows ? fit : rows);
   if (r.stages < 1) return false;
   size_t ring = (size_t)r.stages * r.stage_bytes * r.teams;
-  if (r.teams > 1 && ring < (size_t)C * 8) ring = (size_t)C * 8;  // the teams' sums are added there
+  const size_t sums = r.teams > 1 ? (size_t)C * 8 * r.teams : 0;  // added there
+  if (ring < sums) ring = sums;
   r.smem = fixed + ring;
   *out = r;
-  return r.smem <= kRingSmem;
+  return r.smem <= r.smem_most;
 }
+
+int norm_bwd_most_slabs(int64_t T) { return (int)(T < kMostSlabs ? (T < 1 ? 1 : T) : kMostSlabs); }
 
 cudaError_t launch_norm_fwd(const NormFwd& p, cudaStream_t st) {
   const bool eight = rows_of_eight(p.x, p.ldx, p.x_bf16, p.T, p.C) &&

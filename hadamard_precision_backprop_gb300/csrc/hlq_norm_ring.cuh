@@ -8,13 +8,18 @@
 namespace hlq {
 
 constexpr int kMostUnits = 8;    // groups of four columns a thread owns
-constexpr int kMostSlabs = 256;  // CTAs of the ring, and slabs of partial sums
-constexpr size_t kRingSmem = 227 * 1024 - 256;  // what the static part leaves
+constexpr int kMostSlabs = 640;  // CTAs of the ring, and slabs of partial sums
+
+// Threads of a CTA at most: 16 warps of up to 128 registers, or 24 where two
+// groups of columns a thread leave room for that.
+constexpr int ring_threads(int team, int units) {
+  return team > 32 ? team : units <= 2 ? 768 : 512;
+}
 
 struct RingPlan {
   int team, units;  // threads of a team, groups of four columns of each
   int teams, stages, stage_bytes, grid;
-  size_t smem;
+  size_t smem, smem_most;
 };
 bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out);
 cudaError_t launch_norm_bwd_ring_bf16(const NormBwd& p, const RingPlan& r, cudaStream_t st);

@@ -1,13 +1,16 @@
 // hlq_norm_ring_impl.cuh -- the kernel of hlq_norm_ring.cuh.
 //
-// One CTA per SM; a team of kTeam threads takes every (number of teams)-th
-// row.  The rows of x, g_y and the residual's gradient come into a ring of
+// A team of kTeam threads takes every (number of teams)-th row: a warp, with
+// several in a CTA and one CTA per SM, or for longer rows the whole CTA, one
+// or two per SM.  The rows of x, g_y and the residual's gradient come into a ring of
 // shared-memory stages by bulk copies, several rows ahead; each thread owns up
 // to kUnits groups of four columns and keeps their weights, and their sums
 // for g_w and g_b over all its rows, in registers.  The CTA's teams add their
 // sums in shared memory and write one slab of partial sums, which
 // norm_bwd_join_kernel adds.
 #pragma once
+
+#include <type_traits>
 
 #include "hlq_device.cuh"
 #include "hlq_norm_ring.cuh"
@@ -26,20 +29,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 template <int kTeam>
-__device__ __forceinline__ void team_sync(int team) {
+__device__ __forceinline__ void team_sync() {
   if constexpr (kTeam == 32)
     __syncwarp();
   else
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam) : "memory");
+    __syncthreads();
+}
+
+// The sums of a and b over a warp: the halves of the warp take one each, which
+// halves the shuffles.  Lane 0 ends with the sum of a, lane 16 with that of b.
+__device__ __forceinline__ float warp_sum_pair(float a, float b) {
+  const bool high = threadIdx.x & 16;
+  float v = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 template <bool kXBf16, bool kGyBf16, int kTeam, int kUnits>
-__global__ void __launch_bounds__(kTeam == 32 ? 256 : 512, 1)
+__global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 : 512 / kTeam)
     norm_bwd_ring_kernel(const __grid_constant__ NormBwd p, const __grid_constant__ RingPlan plan) {
   constexpr int kWarps = kTeam / 32, kPairs = kUnits * 2;
-  // the first pass's x - mean and g_y w kept for the second, where a thread
-  // has the registers (256 threads a CTA)
-  constexpr bool kKeep = kTeam == 32;
   constexpr int kSx = kXBf16 ? 2 : 4, kSg = kGyBf16 ? 2 : 4;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int abort_flag;
@@ -71,8 +81,11 @@ __global__ void __launch_bounds__(kTeam == 32 ? 256 : 512, 1)
       bulk_load(dst + C * (kSx + kSg), static_cast<const char*>(p.gres) + t * p.ldgr * sr, C * sr,
                 &full[s]);
   };
+  // The warp goes on together: lanes that spun on a stage ahead of the lane
+  // that fills it could keep that lane from running.
   if (tid == 0)
     for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
+  __syncwarp();
 
   F2 gw[kPairs], gb[kPairs], w[kPairs];
 #pragma unroll
@@ -86,88 +99,76 @@ __global__ void __launch_bounds__(kTeam == 32 ? 256 : 512, 1)
   const float inv = 1.f / (float)C;
   int stage = 0;
   uint32_t parity = 0;
-  float mean = 0.f, rstd = 0.f;
-  if (t0 < p.T) mean = p.mean[t0], rstd = p.rstd[t0];
+  float mean_next = 0.f, rstd_next = 0.f;
+  if (t0 < p.T) mean_next = p.mean[t0], rstd_next = p.rstd[t0];
   for (int64_t t = t0; t < p.T; t += step) {
-    float mean_next = 0.f, rstd_next = 0.f;
+    const float mean = mean_next, rstd = rstd_next;
     if (t + step < p.T) mean_next = p.mean[t + step], rstd_next = p.rstd[t + step];
     // after a wait that gave up, the others return at once and the loop runs
     // to its end: every barrier is still met
     mbar_wait(&full[stage], parity, &abort_flag, p.status);
     const unsigned char* row = ring + (size_t)stage * plan.stage_bytes;
+    const unsigned char *xs = row + tid * 4 * kSx, *gs = row + C * kSx + tid * 4 * kSg;
     const F2 neg_mean = f2(-mean), rstd2 = f2(rstd);
-    F2 keep_d[kKeep ? kPairs : 1], keep_a[kKeep ? kPairs : 1];
     F2 sa2 = f2(0.f), sx2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int c = (i * kTeam + tid) * 4;
-      if (c < C) {
-        const Quad x = load4<kXBf16>(row, c), g = load4<kGyBf16>(row + C * kSx, c);
+      if ((i * kTeam + tid) * 4 < C) {
+        const Quad x = load4<kXBf16>(xs, i * kTeam * 4), g = load4<kGyBf16>(gs, i * kTeam * 4);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const F2 d = x.v[k] + neg_mean, xhat = d * rstd2, a = g.v[k] * w[i * 2 + k];
+          const F2 xhat = (x.v[k] + neg_mean) * rstd2, a = g.v[k] * w[i * 2 + k];
           sa2 = sa2 + a;
           sx2 = fma2(a, xhat, sx2);
           gw[i * 2 + k] = fma2(g.v[k], xhat, gw[i * 2 + k]);
           gb[i * 2 + k] = gb[i * 2 + k] + g.v[k];
-          if constexpr (kKeep) keep_d[i * 2 + k] = d, keep_a[i * 2 + k] = a;
         }
       }
     }
     const float2 pa = split(sa2), px = split(sx2);
-    float sa = pa.x + pa.y, sx = px.x + px.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sa += __shfl_xor_sync(0xffffffffu, sa, o);
-      sx += __shfl_xor_sync(0xffffffffu, sx, o);
-    }
+    float sum = warp_sum_pair(pa.x + pa.y, px.x + px.y), sa, sx;
     if constexpr (kWarps > 1) {
-      if (lane == 0) red[warp] = sa, red[kWarps + warp] = sx;
-      team_sync<kTeam>(team);  // written again only after the sync at the row's end
-      sa = lane < kWarps ? red[lane] : 0.f;
-      sx = lane < kWarps ? red[kWarps + lane] : 0.f;
+      if ((lane & 15) == 0) red[(lane >> 4) * kWarps + warp] = sum;
+      team_sync<kTeam>();  // written again only after the sync at the row's end
+      sum = (lane & 15) < kWarps ? red[(lane >> 4) * kWarps + (lane & 15)] : 0.f;
 #pragma unroll
-      for (int o = kWarps / 2; o > 0; o >>= 1) {
-        sa += __shfl_xor_sync(0xffffffffu, sa, o);
-        sx += __shfl_xor_sync(0xffffffffu, sx, o);
-      }
-      sa = __shfl_sync(0xffffffffu, sa, 0);
-      sx = __shfl_sync(0xffffffffu, sx, 0);
+      for (int o = kWarps / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    sa *= inv;
-    sx *= inv;
-    // g_x = rstd a - rstd sa - (x - mean) rstd^2 sx
+    sa = __shfl_sync(0xffffffffu, sum, 0) * inv;
+    sx = __shfl_sync(0xffffffffu, sum, 16) * inv;
+    // g_x = rstd a - rstd sa - (x - mean) rstd^2 sx (+ g_residual)
     const F2 shift = f2(-rstd * sa), slope = f2(-rstd * rstd * sx);
+    auto write = [&](auto out_bf16, auto with_residual) {
+      constexpr bool kOut = decltype(out_bf16)::value;
+      constexpr int kSr = kOut ? 2 : 4;
+      char* to = static_cast<char*>(p.gx) + (t * p.ldgx + tid * 4) * kSr;
+      const unsigned char* rs = row + C * (kSx + kSg) + tid * 4 * kSr;
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int c = (i * kTeam + tid) * 4;
-      if (c < C) {
-        Quad o = {{shift, shift}};
-        if (p.gres) {
-          const void* r = row + C * (kSx + kSg);
-          o = p.gx_bf16 ? load4<true>(r, c) : load4<false>(r, c);
-          o.v[0] = o.v[0] + shift, o.v[1] = o.v[1] + shift;
-        }
-        if constexpr (kKeep) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            o.v[k] = fma2(keep_d[i * 2 + k], slope, fma2(keep_a[i * 2 + k], rstd2, o.v[k]));
-        } else {
-          const Quad x = load4<kXBf16>(row, c), g = load4<kGyBf16>(row + C * kSx, c);
+      for (int i = 0; i < kUnits; ++i) {
+        if ((i * kTeam + tid) * 4 < C) {
+          const Quad x = load4<kXBf16>(xs, i * kTeam * 4), g = load4<kGyBf16>(gs, i * kTeam * 4);
+          Quad o = {{shift, shift}};
+          if constexpr (decltype(with_residual)::value) {
+            o = load4<kOut>(rs, i * kTeam * 4);
+            o.v[0] = o.v[0] + shift, o.v[1] = o.v[1] + shift;
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             o.v[k] = fma2(x.v[k] + neg_mean, slope, fma2(g.v[k] * w[i * 2 + k], rstd2, o.v[k]));
+          store4<kOut>(to, i * kTeam * 4, o);
         }
-        if (p.gx_bf16)
-          store4<true>(p.gx, t * p.ldgx + c, o);
-        else
-          store4<false>(p.gx, t * p.ldgx + c, o);
       }
-    }
-    if (tid == 0 && (!isfinite(sa) || !isfinite(sx))) raise_flag(p.status, HLQ_DEV_NONFINITE);
-    team_sync<kTeam>(team);  // the stage has been read by the whole team
+    };
+    if (p.gx_bf16)
+      p.gres ? write(std::true_type{}, std::true_type{}) : write(std::true_type{}, std::false_type{});
+    else
+      p.gres ? write(std::false_type{}, std::true_type{})
+             : write(std::false_type{}, std::false_type{});
+    if (tid == 0 && !(fabsf(sa) < INFINITY && fabsf(sx) < INFINITY))
+      raise_flag(p.status, HLQ_DEV_NONFINITE);
+    team_sync<kTeam>();  // the stage has been read by the whole team
     if (tid == 0) issue(t + plan.stages * step, stage);
-    mean = mean_next, rstd = rstd_next;
+    __syncwarp();
     if (++stage == plan.stages) stage = 0, parity ^= 1;
   }
   if (!p.part) return;
@@ -183,34 +184,32 @@ __global__ void __launch_bounds__(kTeam == 32 ? 256 : 512, 1)
     }
     return;
   }
-  // every copy has been waited for by its team: the ring is free
-  float* sum = reinterpret_cast<float*>(smem);
-  for (int k = 0; k < plan.teams; ++k) {
-    __syncthreads();
-    if (team != k) continue;
+  // Every copy has been waited for by its team: the ring is free for the
+  // teams' sums, which are added in the teams' order.
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int c = (i * kTeam + tid) * 4;
-      if (c < C) {
-        Quad a = {{gw[i * 2], gw[i * 2 + 1]}}, b = {{gb[i * 2], gb[i * 2 + 1]}};
-        if (k > 0) {
-          const Quad a0 = load4<false>(sum, c), b0 = load4<false>(sum, C + c);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) a.v[j] = a.v[j] + a0.v[j], b.v[j] = b.v[j] + b0.v[j];
-        }
-        store4<false>(sum, c, a);
-        store4<false>(sum, C + c, b);
-      }
+  for (int i = 0; i < kUnits; ++i) {
+    const int c = (i * kTeam + tid) * 4;
+    if (c < C) {
+      store4<false>(sums + team * 2 * C, c, {{gw[i * 2], gw[i * 2 + 1]}});
+      store4<false>(sums + team * 2 * C, C + c, {{gb[i * 2], gb[i * 2 + 1]}});
     }
   }
   __syncthreads();
-  for (int c = threadIdx.x * 4; c < 2 * C; c += blockDim.x * 4)
-    *reinterpret_cast<float4*>(slab + c) = *reinterpret_cast<const float4*>(sum + c);
+  for (int c = threadIdx.x * 4; c < 2 * C; c += blockDim.x * 4) {
+    Quad q = load4<false>(sums, c);
+    for (int k = 1; k < plan.teams; ++k) {
+      const Quad r = load4<false>(sums + k * 2 * C, c);
+      q.v[0] = q.v[0] + r.v[0], q.v[1] = q.v[1] + r.v[1];
+    }
+    store4<false>(slab, c, q);
+  }
 }
 
 template <bool kXBf16, bool kGyBf16, int kTeam, int kUnits>
 cudaError_t launch_ring(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
-  const cudaError_t e = allow_smem<norm_bwd_ring_kernel<kXBf16, kGyBf16, kTeam, kUnits>>(kRingSmem);
+  const cudaError_t e = allow_smem<norm_bwd_ring_kernel<kXBf16, kGyBf16, kTeam, kUnits>>(r.smem_most);
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_bwd_ring_kernel<kXBf16, kGyBf16, kTeam, kUnits>, dim3(r.grid),
                     dim3(kTeam * r.teams), r.smem, st, p, r);
@@ -225,8 +224,7 @@ cudaError_t pick_ring(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
   HLQ_RING(32, 6);
   HLQ_RING(32, 8);
   HLQ_RING(128, 4);
-  HLQ_RING(128, 6);
-  HLQ_RING(128, 8);
+  HLQ_RING(256, 4);
   HLQ_RING(512, 4);
   HLQ_RING(512, 6);
   HLQ_RING(512, 7);
