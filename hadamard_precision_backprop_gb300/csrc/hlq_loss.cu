@@ -170,10 +170,13 @@ __device__ __forceinline__ MaxSum cta_pair(MaxSum p, bool has_edge, float edge, 
   return p;
 }
 
-// The row's pair, in the first warp of every CTA of the cluster.
+// The row's pair, in the first warp of every CTA of the cluster (whose threads
+// have all called cluster_started_arrive).
 __device__ __forceinline__ MaxSum cluster_pair(MaxSum p, float c, int slice, int log_slices,
                                                MaxSum* slots) {
   if (log_slices == 0) return p;
+  __syncwarp();
+  cluster_started_wait();
   if ((int)threadIdx.x < (1 << log_slices)) {
     const uint32_t at = cluster_map(saddr(slots + slice), threadIdx.x);
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(p.m), "f"(p.s)
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_cluster_kernel(TokenLogprob
   const float c = p.scale * kLog2e;
   pdl_wait();
   pdl_trigger();
+  if (log_slices) cluster_started_arrive();
   const S sl(p.logits, t * p.ld, p.V, slice, log_slices);
   int64_t a = -1;
   float logit = 0.f;
@@ -374,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 4 : 2)
     }
     return;
   }
+  if (log_slices) cluster_started_arrive();
   int64_t a = -1;
   float logit = 0.f, old = 0.f, adv = 0.f, ref = 0.f;
   if (tid < 32) {

@@ -20,14 +20,6 @@
 namespace hlq {
 namespace {
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(saddr(bar))
-      : "memory");
-}
-
 template <int kTeam>
 __device__ __forceinline__ void team_sync() {
   if constexpr (kTeam == 32)
@@ -62,9 +54,12 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
   float* red = reinterpret_cast<float*>(tail + 8 * 8 * plan.teams) + team * 2 * kWarps;
 
   if (threadIdx.x == 0) abort_flag = 0;
-  if (tid == 0)
+  if (tid == 0) {
     for (int s = 0; s < plan.stages; ++s) mbar_init(&full[s], 1);
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the copies complete on the barriers through the async proxy
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
