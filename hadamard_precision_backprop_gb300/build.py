@@ -23,7 +23,7 @@ EXT = os.path.join(OUT_DIR, "_hlq_torch.so")
 
 SOURCES = ["hlq_api.cu", "hlq_quant.cu", "hlq_gemm_simple.cu", "hlq_gemm_tc.cu",
            "hlq_step_api.cu", "hlq_norm.cu", "hlq_norm_ring_bf16.cu",
-           "hlq_norm_ring_f32.cu", "hlq_loss.cu", "hlq_clip.cu",
+           "hlq_norm_ring_f32.cu", "hlq_norm_elem.cu", "hlq_loss.cu", "hlq_clip.cu",
            "hlq_noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

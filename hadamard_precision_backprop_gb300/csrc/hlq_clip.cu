@@ -17,17 +17,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kQuads = kClipChunk / kThreads / 4;  // groups of four a thread
 
-__device__ __forceinline__ double cta_sum_f64(double v, double* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
-  return s;
-}
-
 // The tensor that holds chunk `k` of the concatenation: the last one whose
 // first chunk is <= k (tensors without elements are not in the table).
 __device__ __forceinline__ int tensor_of(const ClipTable& tab, int64_t k) {
@@ -84,56 +73,112 @@ __device__ __forceinline__ void load_chunk(const void* in, bool bf16, bool four,
   }
 }
 
-// Sum of the squares of a thread's 32 elements: in fp32 where that neither
-// overflows nor loses small terms (the sum is between 2^-95 and 2^120: any
-// square that went below 2^-126 is then beneath its last bit), else in fp64.
-__device__ __forceinline__ double sum_of_squares(const float (&v)[kQuads * 4]) {
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+// Sums of squares in fp32 where that neither overflows nor loses small terms:
+// a thread's 32 elements give between 2^-95 (any square that went below 2^-126
+// is then beneath the sum's last bit) and 2^100.  Else, and that is rare, in
+// fp64, which is slow here.  `sum` and `rest` are a running fp32 sum and what
+// its roundings lost.
+struct Squares {
+  float sum = 0.f, rest = 0.f;
+  double wide = 0.0;
+  __device__ __forceinline__ void add(const float (&v)[kQuads * 4]) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < kQuads * 4; ++i) s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
-  const float f = (s[0] + s[1]) + (s[2] + s[3]);
-  if (f >= 0x1p-95f && f <= 0x1p120f) return f;
-  uint32_t any = 0;
+    for (int i = 0; i < kQuads * 4; ++i) s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
+    const float f = (s[0] + s[1]) + (s[2] + s[3]);
+    if (f >= 0x1p-95f && f <= 0x1p100f) {
+      const float y = f - rest, t = sum + y;
+      rest = (t - sum) - y;
+      sum = t;
+      return;
+    }
+    uint32_t any = 0;
 #pragma unroll
-  for (int i = 0; i < kQuads * 4; ++i) any |= __float_as_uint(v[i]) << 1;
-  if (any == 0) return 0.0;
-  double d = 0.0;
+    for (int i = 0; i < kQuads * 4; ++i) any |= __float_as_uint(v[i]) << 1;
+    if (any == 0) return;
+#pragma unroll 1
+    for (int i = 0; i < kQuads * 4; ++i) wide += square(v, i);
+  }
+  static __device__ __forceinline__ double square(const float (&v)[kQuads * 4], int i) {
+    float x = 0.f;
 #pragma unroll
-  for (int i = 0; i < kQuads * 4; ++i) d += (double)v[i] * v[i];
-  return d;
-}
+    for (int k = 0; k < kQuads * 4; ++k) x = k == i ? v[k] : x;
+    return (double)x * x;
+  }
+};
 
+// A CTA's partial result is the norm of its elements: an fp32 number wherever
+// the whole norm is one.
 __global__ void __launch_bounds__(kThreads)
-    clip_norm_kernel(const __grid_constant__ ClipTable tab, double* part) {
-  __shared__ double red[32];
+    clip_norm_kernel(const __grid_constant__ ClipTable tab, float* part) {
+  __shared__ double red[kThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
   const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
   int i = tensor_of(tab, k0);
-  double acc = 0.0;
+  Squares sq;
   for (int64_t k = k0; k < k1; ++k) {
     if (i + 1 < tab.n && tab.first[i + 1] <= k) ++i;  // every tensor has a chunk
     const int64_t e0 = (k - tab.first[i]) * kClipChunk;
     float v[kQuads * 4];
     load_chunk(tab.in[i], tab.flags[i] & kClipInBf16, tab.flags[i] & kClipInFour, e0,
                min((int64_t)kClipChunk, tab.numel[i] - e0), v);
-    acc += sum_of_squares(v);
+    sq.add(v);
   }
-  acc = cta_sum_f64(acc, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = acc;
+  // the warps' sums in fp32 (2^100 times all elements of a run could overflow
+  // there, so above 2^100 in fp64 as well)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool wide = __syncthreads_or(sq.wide != 0.0 || sq.sum > 0x1p100f);
+  float s = sq.sum - sq.rest;
+  double d = 0.0;
+  if (!wide) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[warp] = s;
+  } else {
+    d = sq.wide + (double)s;
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) red[warp] = d;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kThreads / 32; ++k) red[0] += red[k];
+    part[blockIdx.x] = (float)sqrt(red[0]);
+  }
 }
 
-// The coefficient from the partial sums, in every thread of the CTA; the one
-// CTA with `write` also writes norm and coefficient.
-__device__ __forceinline__ float clip_coef(const ClipSums& q, bool write, double* red) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < q.n; i += kThreads) s += ld_dep_f64(q.part + i);
-  s = cta_sum_f64(s, red);
-  const float norm = (float)sqrt(s);
+// The coefficient from the CTAs' norms, in the first warp; with `write` it also
+// writes norm and coefficient.
+__device__ __forceinline__ float clip_coef(const ClipSums& q, bool write) {
+  const int lane = threadIdx.x & 31;
+  float top = 0.f, s = 0.f;
+  bool nan = false;
+#pragma unroll 8
+  for (int i = lane; i < q.n; i += 32) {
+    const float v = q.part[i];
+    top = fmaxf(top, v);
+    nan |= isnan(v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  nan = __any_sync(0xffffffffu, nan);
+  float norm = nan ? NAN : top;  // 0 and infinity as they are
+  if (!nan && top > 0.f && top < INFINITY) {
+    // relative to a power of two near the largest: exact, and in range
+    const int e = ilogbf(top);
+#pragma unroll 8
+    for (int i = lane; i < q.n; i += 32) {
+      const float v = ldexpf(q.part[i], -e);
+      s = fmaf(v, v, s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    norm = ldexpf(sqrtf(s), e);
+  }
   float coef = q.max_norm / (norm + 1e-6f);
   coef = coef > 1.f ? 1.f : coef;  // a NaN stays
-  if (write && threadIdx.x == 0) {
+  if (write && lane == 0) {
     q.norm_coef[0] = norm;
     q.norm_coef[1] = coef;
     if (!isfinite(norm)) raise_flag(q.status, HLQ_DEV_NONFINITE);
@@ -141,11 +186,10 @@ __device__ __forceinline__ float clip_coef(const ClipSums& q, bool write, double
   return coef;
 }
 
-// The norm and the coefficient alone.
-__global__ void __launch_bounds__(kThreads) clip_coef_kernel(ClipSums q) {
-  __shared__ double red[32];
+// The norm and the coefficient alone: one warp.
+__global__ void __launch_bounds__(32) clip_coef_kernel(ClipSums q) {
   pdl_wait();
-  clip_coef(q, true, red);
+  clip_coef(q, true);
 }
 
 // The runs and their chunks in the opposite order of the norm's pass: what
@@ -154,10 +198,15 @@ __global__ void __launch_bounds__(kThreads) clip_coef_kernel(ClipSums q) {
 __global__ void __launch_bounds__(kThreads)
     clip_scale_kernel(const __grid_constant__ ClipTable tab, const __grid_constant__ ClipSums q,
                       int first) {
-  __shared__ double red[32];
+  __shared__ float shared_coef;
   pdl_wait();
   pdl_trigger();
-  const float coef = clip_coef(q, first && blockIdx.x == 0, red);
+  if (threadIdx.x < 32) {
+    const float c = clip_coef(q, first && blockIdx.x == 0);
+    if (threadIdx.x == 0) shared_coef = c;
+  }
+  __syncthreads();
+  const float coef = shared_coef;
   const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
   const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
   if (k1 == k0) return;
@@ -207,12 +256,12 @@ int clip_grid(int64_t chunks, int sms) {
   return (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);
 }
 
-cudaError_t launch_clip_norm(const ClipTable& tab, double* part, int grid, cudaStream_t st) {
+cudaError_t launch_clip_norm(const ClipTable& tab, float* part, int grid, cudaStream_t st) {
   return launch_pdl(clip_norm_kernel, dim3(grid), dim3(kThreads), 0, st, tab, part);
 }
 
 cudaError_t launch_clip_coef(const ClipSums& q, cudaStream_t st) {
-  return launch_pdl(clip_coef_kernel, dim3(1), dim3(kThreads), 0, st, q);
+  return launch_pdl(clip_coef_kernel, dim3(1), dim3(32), 0, st, q);
 }
 
 cudaError_t launch_clip_scale(const ClipTable& tab, const ClipSums& q, bool first, int grid,

@@ -231,16 +231,16 @@ struct ClipTable {
   int n;
   int64_t chunks;
 };
-// The norm's partial sums, and what becomes of them.
+// The CTAs' norms, and what becomes of them.
 struct ClipSums {
-  const double* part;
+  const float* part;  // norms
   int n;
   float max_norm;
   float* norm_coef;
   unsigned int* status;
 };
 int clip_grid(int64_t chunks, int sms);
-cudaError_t launch_clip_norm(const ClipTable& tab, double* part, int grid, cudaStream_t st);
+cudaError_t launch_clip_norm(const ClipTable& tab, float* part, int grid, cudaStream_t st);
 cudaError_t launch_clip_coef(const ClipSums& q, cudaStream_t st);
 // `first`: also writes norm and coefficient
 cudaError_t launch_clip_scale(const ClipTable& tab, const ClipSums& q, bool first, int grid,

@@ -81,11 +81,17 @@ struct Slice {
       if (j < 8 ? j < head : after < V) edge = j < 8 ? j : after;
     }
   }
-  // vector j of the slice; -inf past its end
-  __device__ __forceinline__ uint4 vec(int j) const {
+  // This thread's vectors of the group that begins at vector j; -inf past the
+  // slice's end.  (A branch that spares whole groups the comparison keeps the
+  // groups' loads from going out together: 323 -> 352 us at 4096 x 128256.)
+  static constexpr int kStep = kGroup * kThreads;  // vectors of a group of all threads
+  __device__ __forceinline__ void load(int j, uint4 (&raw)[kGroup]) const {
+    const uint4* at = reinterpret_cast<const uint4*>(row + e0 * kSize) + (j + (int)threadIdx.x);
     constexpr uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
-    if (j >= n) return make_uint4(none, none, none, none);
-    return reinterpret_cast<const uint4*>(row + e0 * kSize)[j];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      raw[i] = j + i * kThreads + (int)threadIdx.x < n ? at[i * kThreads]
+                                                       : make_uint4(none, none, none, none);
   }
   __device__ __forceinline__ float elem(int64_t e) const { return load_elem(row, kBf16, e); }
 };
@@ -104,14 +110,22 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// The largest of a group.
 template <bool kBf16>
-__device__ __forceinline__ float max_of(uint4 r) {
+__device__ __forceinline__ float max_of(const uint4 (&r)[Slice<kBf16>::kGroup]) {
   if constexpr (kBf16) {
-    const uint32_t m = max_bf16x2(max_bf16x2(r.x, r.y), max_bf16x2(r.z, r.w));
+    const uint32_t a = max_bf16x2(max_bf16x2(r[0].x, r[0].y), max_bf16x2(r[0].z, r[0].w));
+    const uint32_t b = max_bf16x2(max_bf16x2(r[1].x, r[1].y), max_bf16x2(r[1].z, r[1].w));
+    const uint32_t m = max_bf16x2(a, b);
     return fmaxf(bf16_lo(m), bf16_hi(m));
   } else {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
-                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+    float m = __uint_as_float(r[0].x);
+#pragma unroll
+    for (int i = 0; i < Slice<kBf16>::kGroup; ++i)
+      m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(r[i].x)),
+                      fmaxf(__uint_as_float(r[i].y), __uint_as_float(r[i].z))),
+                __uint_as_float(r[i].w));
+    return m;
   }
 }
 
@@ -122,11 +136,9 @@ struct Running {
   // One group of 16.  The difference to the maximum comes first, so that the
   // maximum itself counts exactly 1.
   template <bool kBf16>
-  __device__ __forceinline__ void add(const uint4* raw, float c) {
+  __device__ __forceinline__ void add(const uint4 (&raw)[Slice<kBf16>::kGroup], float c) {
     using S = Slice<kBf16>;
-    float top = m;
-#pragma unroll
-    for (int i = 0; i < S::kGroup; ++i) top = fmaxf(top, max_of<kBf16>(raw[i]));
+    const float top = fmaxf(m, max_of<kBf16>(raw));
     s = s * f2(ex2((m - top) * c));
     const F2 neg = f2(-top), c2 = f2(c);
 #pragma unroll
@@ -198,15 +210,12 @@ __device__ __forceinline__ MaxSum slice_pair(
   using S = Slice<kBf16>;
   edge = sl.edge >= 0 ? sl.elem(sl.edge) : 0.f;
   Running run;
-  for (int b = 0; b < (kHeld ? 1 : sl.n); b += kGroups * S::kGroup * kThreads) {
+  for (int b = 0; b < (kHeld ? 1 : sl.n); b += kGroups * S::kStep) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) sl.load(b + g * S::kStep, raw[g]);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-      for (int i = 0; i < S::kGroup; ++i)
-        raw[g][i] = sl.vec(b + (g * S::kGroup + i) * kThreads + (int)threadIdx.x);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      if (b + g * S::kGroup * kThreads < sl.n) run.add<kBf16>(raw[g], c);
+      if (b + g * S::kStep < sl.n) run.add<kBf16>(raw[g], c);
   }
   return cta_pair(run.pair(), sl.edge >= 0, edge, c, warp_pair);
 }
@@ -267,13 +276,10 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
   if (t >= p.T) return;
   int slice = 0, flip = 0;
   S sl(p.logits, t * p.ld, p.V, 0, log_slices);
-  constexpr int kStep = kGroups * S::kGroup * kThreads;
   int b = 0;
   uint4 raw[kGroups][S::kGroup];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-    for (int i = 0; i < S::kGroup; ++i) raw[g][i] = sl.vec((g * S::kGroup + i) * kThreads + tid);
+  for (int g = 0; g < kGroups; ++g) sl.load(g * S::kStep, raw[g]);
   float edge = sl.edge >= 0 ? sl.elem(sl.edge) : 0.f;
   int64_t a = -1;
   float logit = 0.f;
@@ -285,11 +291,11 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
       logit = a >= 0 && a < p.V ? sl.elem(a) : 0.f;
     }
     // what comes after these groups: more of the slice, a slice, a row, nothing
-    const bool slice_ends = b + kStep >= sl.n;
+    const bool slice_ends = b + kGroups * S::kStep >= sl.n;
     const bool row_ends = slice_ends && slice + 1 == 1 << log_slices;
     const int64_t t_next = row_ends ? t + gridDim.x : t;
     const int slice_next = row_ends ? 0 : slice_ends ? slice + 1 : slice;
-    const int b_next = slice_ends ? 0 : b + kStep;
+    const int b_next = slice_ends ? 0 : b + kGroups * S::kStep;
     const bool more = t_next < p.T;
     S next = sl;
     if (slice_ends && more) next = S(p.logits, t_next * p.ld, p.V, slice_next, log_slices);
@@ -297,12 +303,8 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
     if (slice_ends && more && next.edge >= 0) edge_next = next.elem(next.edge);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      if (b + g * S::kGroup * kThreads < sl.n) run.add<kBf16>(raw[g], c);
-      if (more) {
-#pragma unroll
-        for (int i = 0; i < S::kGroup; ++i)
-          raw[g][i] = next.vec(b_next + (g * S::kGroup + i) * kThreads + tid);
-      }
+      if (b + g * S::kStep < sl.n) run.add<kBf16>(raw[g], c);
+      if (more) next.load(b_next + g * S::kStep, raw[g]);
     }
     if (slice_ends) {
       const MaxSum pair = cta_pair(run.pair(), sl.edge >= 0, edge, c, warp_pair[flip]);
@@ -339,7 +341,7 @@ __device__ __forceinline__ uint4 narrow(const F2* v) {
 // again.  kAligned: g's rows begin at the same offset from a 16-byte boundary
 // as the logits'; else g is written element by element.
 template <bool kBf16, bool kHeld, bool kAligned>
-__global__ void __launch_bounds__(kThreads, kBf16 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
     policy_rows_kernel(const __grid_constant__ PolicyLoss p, int log_slices) {
   using S = Slice<kBf16>;
   __shared__ MaxSum warp_pair[kWarps], slots[kMostSlices];
@@ -422,30 +424,28 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 4 : 2)
   __syncthreads();
   const RowGrad gr = grad;
   const F2 c2 = f2(c), bias = f2(gr.bias), k2 = f2(gr.k);
-  for (int b = 0; b < (kHeld ? 1 : sl.n); b += kGroups * S::kGroup * kThreads) {
-    if constexpr (!kHeld) {
+  auto gradient = [&](uint4 r, F2* v) {
+    widen<kBf16>(r, v);
 #pragma unroll
-      for (int q = 0; q < kGroups; ++q)
-#pragma unroll
-        for (int i = 0; i < S::kGroup; ++i)
-          raw[q][i] = sl.vec(b + (q * S::kGroup + i) * kThreads + tid);
+    for (int k = 0; k < S::kVec / 2; ++k) {
+      const float2 x = split(fma2(v[k], c2, bias));
+      v[k] = f2(ex2(x.x), ex2(x.y)) * k2;
     }
+  };
+  for (int b = 0; b < (kHeld ? 1 : sl.n); b += kGroups * S::kStep) {
 #pragma unroll
-    for (int q = 0; q < kGroups; ++q)
+    for (int q = 0; q < kGroups; ++q) {
+      const int j = b + q * S::kStep;
+      if constexpr (!kHeld) sl.load(j, raw[q]);
 #pragma unroll
       for (int i = 0; i < S::kGroup; ++i) {
-        const int j = b + (q * S::kGroup + i) * kThreads + tid;
-        if (j < sl.n) {
+        if (j + i * kThreads + tid < sl.n) {
           F2 v[S::kVec / 2];
-          widen<kBf16>(raw[q][i], v);
-#pragma unroll
-          for (int k = 0; k < S::kVec / 2; ++k) {
-            const float2 x = split(fma2(v[k], c2, bias));
-            v[k] = f2(ex2(x.x), ex2(x.y)) * k2;
-          }
-          put(j, v);
+          gradient(raw[q][i], v);
+          put(j + i * kThreads + tid, v);
         }
       }
+    }
   }
   if (sl.edge >= 0) store_elem(g, kBf16, sl.edge, ex2(fmaf(edge, c, gr.bias)) * gr.k);
   // the action's element, by the thread that has just written it
@@ -455,26 +455,48 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 4 : 2)
   if (mine) store_elem(g, kBf16, gr.action, gr.at_action);
 }
 
-// stats = sums over the rows in a fixed order, in fp64.
-__global__ void __launch_bounds__(kThreads) policy_stats_kernel(PolicyLoss p) {
-  __shared__ double red[3][kThreads];
+// stats = sums over the rows in a fixed order (in fp32: a tree over 1024
+// partial sums; fp64 is far slower here than all the rest of this kernel).  One
+// CTA, whose time is the latency of its loads, so each thread has twelve of
+// them under way.
+constexpr int kStatsThreads = 1024;
+
+__global__ void __launch_bounds__(kStatsThreads) policy_stats_kernel(PolicyLoss p) {
+  __shared__ float red[3][kStatsThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
+  float s[3] = {0.f, 0.f, 0.f};
+  for (int64_t t = tid; t < p.T; t += 4 * kStatsThreads) {
+    float v[3][4];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = t + i * kStatsThreads;
+        v[k][i] = r < p.T ? p.part[k * p.T + r] : 0.f;
+      }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] += (v[k][0] + v[k][1]) + (v[k][2] + v[k][3]);
+  }
+#pragma unroll
   for (int k = 0; k < 3; ++k) {
-    double s = 0.0;
-    for (int64_t t = threadIdx.x; t < p.T; t += kThreads) s += ld_dep_f32(p.part + k * p.T + t);
-    red[k][threadIdx.x] = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    if (lane == 0) red[k][warp] = s[k];
   }
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    __syncthreads();
-    if ((int)threadIdx.x < o)
-      for (int k = 0; k < 3; ++k) red[k][threadIdx.x] += red[k][threadIdx.x + o];
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    s[k] = red[k][lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
   }
-  if (threadIdx.x == 0) {
-    const double pg = red[0][0], kl = red[1][0];
-    p.stats[0] = (float)(p.ref_logp && p.kl_coef != 0.f ? pg + (double)p.kl_coef * kl : pg);
-    p.stats[1] = (float)pg;
-    p.stats[2] = (float)kl;
-    p.stats[3] = (float)red[2][0];
+  if (lane == 0) {
+    p.stats[0] = p.ref_logp && p.kl_coef != 0.f ? fmaf(p.kl_coef, s[1], s[0]) : s[0];
+    p.stats[1] = s[0];
+    p.stats[2] = s[1];
+    p.stats[3] = s[2];
   }
 }
 
@@ -535,7 +557,7 @@ cudaError_t launch_policy_rows(const PolicyLoss& p, cudaStream_t st) {
 }
 
 cudaError_t launch_policy_stats(const PolicyLoss& p, cudaStream_t st) {
-  return launch_pdl(policy_stats_kernel, dim3(1), dim3(kThreads), 0, st, p);
+  return launch_pdl(policy_stats_kernel, dim3(1), dim3(kStatsThreads), 0, st, p);
 }
 
 }  // namespace hlq

@@ -42,8 +42,8 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
 // is read once and the variance is taken from the differences to the mean; all
 // of a thread's loads are in flight before the first is used.  kUnit = 8:
 // 16-byte accesses, 32 elements a thread at most.  kUnit = 1: single elements,
-// for rows that are not made of aligned groups of eight; 16 a thread, so that
-// more threads fit and as many bytes are in flight.
+// 16 a thread, for rows that are not made of aligned groups of eight and too
+// long for hlq_norm_elem.cu.
 // ---------------------------------------------------------------------------
 constexpr int kHeldVec = 32, kHeldElem = 16;
 
@@ -174,116 +174,6 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(NormFwd p) 
 }
 
 // ---------------------------------------------------------------------------
-// Backward, rows of single elements (not made of aligned groups of eight).  A
-// team of kTeam threads takes every (number of teams)-th row, a thread up to
-// 16 columns that lie kTeam apart; weights, column sums and the row's elements
-// stay in registers.
-// ---------------------------------------------------------------------------
-constexpr int kElemThreads = 512;
-
-template <int kTeam>
-__device__ __forceinline__ void load_columns(const void* p, bool bf16, int64_t at, int tid, int C,
-                                             float (&v)[kHeldElem]) {
-  if (bf16) {
-#pragma unroll
-    for (int i = 0; i < kHeldElem; ++i) {
-      const int c = i * kTeam + tid;
-      v[i] = c < C ? load_elem(p, true, at + c) : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kHeldElem; ++i) {
-      const int c = i * kTeam + tid;
-      v[i] = c < C ? load_elem(p, false, at + c) : 0.f;
-    }
-  }
-}
-
-template <int kTeam>
-__global__ void __launch_bounds__(kElemThreads, 1)
-    norm_bwd_elem_kernel(const __grid_constant__ NormBwd p) {
-  constexpr int kTeams = kElemThreads / kTeam;
-  __shared__ float red[2][32];
-  extern __shared__ float sum[];  // [2][C], with more than one team
-  const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int C = (int)p.C;
-  pdl_wait();
-  pdl_trigger();
-  float w[kHeldElem], gw[kHeldElem], gb[kHeldElem];
-#pragma unroll
-  for (int i = 0; i < kHeldElem; ++i) w[i] = 1.f, gw[i] = gb[i] = 0.f;
-  if (p.weight) load_columns<kTeam>(p.weight, p.w_bf16, 0, tid, C, w);
-  const float inv = 1.f / (float)C;
-  for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < p.T; t0 += (int64_t)gridDim.x * kTeams) {
-    const int64_t t = t0 + team;  // the teams of a CTA run together: the sums meet at barriers
-    const bool live = t < p.T;
-    float x[kHeldElem] = {}, g[kHeldElem] = {}, rstd = 0.f;
-    if (live) {
-      load_columns<kTeam>(p.x, p.x_bf16, t * p.ldx, tid, C, x);
-      load_columns<kTeam>(p.gy, p.gy_bf16, t * p.ldgy, tid, C, g);
-      rstd = p.rstd[t];
-      const float mean = p.mean[t];
-#pragma unroll
-      for (int i = 0; i < kHeldElem; ++i) x[i] = i * kTeam + tid < C ? (x[i] - mean) * rstd : 0.f;
-    }
-    float sa = 0.f, sx = 0.f;
-#pragma unroll
-    for (int i = 0; i < kHeldElem; ++i) {
-      const float a = g[i] * w[i];
-      sa += a;
-      sx = fmaf(a, x[i], sx);
-      gw[i] = fmaf(g[i], x[i], gw[i]);
-      gb[i] += g[i];
-      g[i] = a;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sa += __shfl_xor_sync(0xffffffffu, sa, o);
-      sx += __shfl_xor_sync(0xffffffffu, sx, o);
-    }
-    if constexpr (kTeam > 32) {
-      if (lane == 0) red[0][warp] = sa, red[1][warp] = sx;
-      __syncthreads();
-      sa = sx = 0.f;
-#pragma unroll
-      for (int i = 0; i < kTeam / 32; ++i) {
-        sa += red[0][team * (kTeam / 32) + i];
-        sx += red[1][team * (kTeam / 32) + i];
-      }
-      __syncthreads();
-    }
-    if (!live) continue;  // the last rows of the call: no barrier follows in the loop
-    sa *= inv;
-    sx *= inv;
-    float r[kHeldElem] = {};
-    if (p.gres) load_columns<kTeam>(p.gres, p.gx_bf16, t * p.ldgr, tid, C, r);
-#pragma unroll
-    for (int i = 0; i < kHeldElem; ++i) {
-      const int c = i * kTeam + tid;
-      if (c < C) store_elem(p.gx, p.gx_bf16, t * p.ldgx + c, fmaf(rstd, g[i] - sa - x[i] * sx, r[i]));
-    }
-    if (tid == 0 && (!isfinite(sa) || !isfinite(sx))) raise_flag(p.status, HLQ_DEV_NONFINITE);
-  }
-  if (!p.part) return;
-  float* slab = p.part + (size_t)blockIdx.x * 2 * p.C;
-#pragma unroll
-  for (int k = 0; k < kTeams; ++k) {
-    if (kTeams > 1) __syncthreads();
-    if (team != k) continue;
-    float* to = k + 1 == kTeams ? slab : sum;
-#pragma unroll
-    for (int i = 0; i < kHeldElem; ++i) {
-      const int c = i * kTeam + tid;
-      if (c < C) {
-        to[c] = (k > 0 ? sum[c] : 0.f) + gw[i];
-        to[C + c] = (k > 0 ? sum[C + c] : 0.f) + gb[i];
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Backward, rows too long for these: g_x with one CTA per row, then the column
 // sums of slabs of rows.
 // ---------------------------------------------------------------------------
@@ -342,8 +232,8 @@ __global__ void __launch_bounds__(256) norm_bwd_join_kernel(NormBwd p, int slabs
   pdl_wait();
   float s = 0.f;
   if (c < n) {
-#pragma unroll 4
-    for (int k = warp; k < slabs; k += 8) s += ld_dep_f32(p.part + k * n + c);
+#pragma unroll 10
+    for (int k = warp; k < slabs; k += 8) s += p.part[k * n + c];
   }
   red[warp][lane] = s;
   __syncthreads();
@@ -370,9 +260,6 @@ cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
     if (p.C <= 128 * kHeldVec) return go(norm_fwd_kernel<kXBf16, 128, 8>, 128);
     if (p.C <= 512 * kHeldVec) return go(norm_fwd_kernel<kXBf16, 512, 8>, 512);
   } else {
-    if (p.C <= 32 * kHeldElem) return go(norm_fwd_kernel<kXBf16, 32, 1>, 32);
-    if (p.C <= 128 * kHeldElem) return go(norm_fwd_kernel<kXBf16, 128, 1>, 128);
-    if (p.C <= 512 * kHeldElem) return go(norm_fwd_kernel<kXBf16, 512, 1>, 512);
     if (p.C <= 1024 * kHeldElem) return go(norm_fwd_kernel<kXBf16, 1024, 1>, 1024);
   }
   return launch_pdl(norm_fwd_long_kernel, dim3((unsigned)(p.T < 65535 ? p.T : 65535)),
@@ -428,6 +315,8 @@ cudaError_t launch_norm_fwd(const NormFwd& p, cudaStream_t st) {
                      rows_of_eight(p.y, p.ldy, p.y_bf16, p.T, p.C) &&
                      rows_of_eight(p.weight, 0, p.w_bf16, 1, p.C) &&
                      rows_of_eight(p.bias, 0, p.w_bf16, 1, p.C);
+  RingPlan r;
+  if (!eight && norm_fwd_elem_plan(p, device_sm_count(), &r)) return launch_norm_fwd_elem(p, r, st);
   return p.x_bf16 ? launch_fwd<true>(p, eight, st) : launch_fwd<false>(p, eight, st);
 }
 
@@ -437,17 +326,9 @@ cudaError_t launch_norm_bwd(const NormBwd& p, int* slabs, cudaStream_t st) {
     *slabs = r.grid;
     return p.x_bf16 ? launch_norm_bwd_ring_bf16(p, r, st) : launch_norm_bwd_ring_f32(p, r, st);
   }
-  if (p.C <= 512 * kHeldElem) {
-    const int team = p.C <= 32 * kHeldElem ? 32 : p.C <= 128 * kHeldElem ? 128 : 512;
-    const int64_t ctas = (p.T * team + kElemThreads - 1) / kElemThreads;
-    int sms = device_sm_count();
-    if (sms > kMostSlabs) sms = kMostSlabs;
-    *slabs = (int)(ctas < sms ? ctas : sms);
-    const size_t smem = team < kElemThreads ? (size_t)p.C * 8 : 0;
-    return launch_pdl(team == 32    ? norm_bwd_elem_kernel<32>
-                      : team == 128 ? norm_bwd_elem_kernel<128>
-                                    : norm_bwd_elem_kernel<512>,
-                      dim3(*slabs), dim3(kElemThreads), smem, st, p);
+  if (norm_bwd_elem_plan(p, device_sm_count(), &r)) {
+    *slabs = r.grid;
+    return launch_norm_bwd_elem(p, r, st);
   }
   if (p.part) {
     *slabs = (int)(p.T < 128 ? p.T : 128);

@@ -25,4 +25,11 @@ bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out);
 cudaError_t launch_norm_bwd_ring_bf16(const NormBwd& p, const RingPlan& r, cudaStream_t st);
 cudaError_t launch_norm_bwd_ring_f32(const NormBwd& p, const RingPlan& r, cudaStream_t st);
 
+
+// Rows of any length and alignment (up to 8192 elements): hlq_norm_elem.cu.
+bool norm_fwd_elem_plan(const NormFwd& p, int sms, RingPlan* out);
+cudaError_t launch_norm_fwd_elem(const NormFwd& p, const RingPlan& r, cudaStream_t st);
+bool norm_bwd_elem_plan(const NormBwd& p, int sms, RingPlan* out);
+cudaError_t launch_norm_bwd_elem(const NormBwd& p, const RingPlan& r, cudaStream_t st);
+
 }  // namespace hlq

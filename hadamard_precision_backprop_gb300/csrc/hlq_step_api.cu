@@ -43,7 +43,7 @@ constexpr int64_t kClipParts = 4096;
 int64_t clip_launches(int64_t n) { return n > 0 ? (n + kClipTensors - 1) / kClipTensors : 1; }
 size_t clip_ws(int64_t n) {
   const int64_t parts = 1024 * clip_launches(n);
-  return (size_t)(parts < kClipParts ? parts : kClipParts) * sizeof(double);
+  return (size_t)(parts < kClipParts ? parts : kClipParts) * sizeof(float);
 }
 
 }  // namespace
@@ -234,8 +234,8 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
   const int sms = device_sm_count();
   if (!status || sms <= 0) return HLQ_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  double* part = static_cast<double*>(d_ws);
-  const int64_t parts_each = (int64_t)(clip_ws(n) / sizeof(double)) / clip_launches(n);
+  float* part = static_cast<float*>(d_ws);
+  const int64_t parts_each = (int64_t)(clip_ws(n) / sizeof(float)) / clip_launches(n);
   int n_part = 0;
   ClipTable tab;
   // the tensors from i0 on that fill one table; returns the next i0
