@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(kThreads)
     clip_norm_kernel(const __grid_constant__ ClipTable tab, float* part) {
   __shared__ double red[kThreads / 32];
   pdl_wait();
-  pdl_trigger();
   const int64_t k0 = tab.chunks * blockIdx.x / gridDim.x;
   const int64_t k1 = tab.chunks * (blockIdx.x + 1) / gridDim.x;
   int i = tensor_of(tab, k0);
@@ -200,7 +199,6 @@ __global__ void __launch_bounds__(kThreads)
                       int first) {
   __shared__ float shared_coef;
   pdl_wait();
-  pdl_trigger();
   if (threadIdx.x < 32) {
     const float c = clip_coef(q, first && blockIdx.x == 0);
     if (threadIdx.x == 0) shared_coef = c;
@@ -250,7 +248,10 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-// Four CTAs of 256 threads an SM: 128 KB of loads in flight.
+// Four CTAs of 256 threads an SM: 128 KB of loads in flight.  Neither pass
+// lets the next kernel start before its own CTAs are done: CTAs of the second
+// that came early would crowd on the SMs that the first left first, five on
+// some and three on others (376 us instead of 356 for 236 M fp32 gradients).
 int clip_grid(int64_t chunks, int sms) {
   const int64_t most = (int64_t)sms * 4;
   return (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);

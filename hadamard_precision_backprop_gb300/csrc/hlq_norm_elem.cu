@@ -105,7 +105,7 @@ template <int kTeam>
 __device__ __forceinline__ Ring ring_setup(unsigned char* smem, const RingPlan& plan, int team,
                                            int tid, int* abort_flag) {
   Ring r;
-  r.stages = smem + (size_t)team * plan.stages * plan.stage_bytes;
+  r.stages = smem + plan.before + (size_t)team * plan.stages * plan.stage_bytes;
   r.full = reinterpret_cast<uint64_t*>(smem + plan.smem - 8 * 8 * plan.teams) + team * 8;
   if (threadIdx.x == 0) *abort_flag = 0;
   if (tid == 0) {
@@ -153,17 +153,24 @@ constexpr int kCols = 16;  // columns a thread owns
 
 constexpr int elem_threads(int team) { return team > 32 ? team : 512; }
 
+// Twice as many threads an SM as in the backward pass: only the row is in
+// registers, weights and bias are in shared memory as fp32 (before the rings).
 template <bool kXBf16, int kTeam>
-__global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / kTeam)
+__global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 2 : 1024 / kTeam)
     norm_fwd_elem_kernel(const __grid_constant__ NormFwd p, const __grid_constant__ RingPlan plan) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float red[2][kTeam / 32];
   __shared__ int abort_flag;
   constexpr int kSize = kXBf16 ? 2 : 4;
   const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, C = (int)p.C;
+  float *w = reinterpret_cast<float*>(smem), *b = w + C;
   const Ring ring = ring_setup<kTeam>(smem, plan, team, tid, &abort_flag);
   pdl_wait();
   pdl_trigger();
+  for (int c = threadIdx.x; c < C; c += blockDim.x) {
+    w[c] = p.weight ? load_elem(p.weight, p.w_bf16, c) : 1.f;
+    b[c] = p.bias ? load_elem(p.bias, p.w_bf16, c) : 0.f;
+  }
   const Source src[2] = {
       {p.x, p.ldx * kSize, p.C * kSize, kSize, 0},
       {p.residual, p.ldr * kSize, p.C * kSize, kSize, slot_bytes(p.C * kSize)}};
@@ -176,14 +183,7 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
   };
   if (tid == 0)
     for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
-  __syncwarp();
-  float w[kCols], b[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) {
-    const int c = i * kTeam + tid;
-    w[i] = p.weight && c < C ? load_elem(p.weight, p.w_bf16, c) : 1.f;
-    b[i] = p.bias && c < C ? load_elem(p.bias, p.w_bf16, c) : 0.f;
-  }
+  __syncthreads();
   const float inv = 1.f / (float)C;
   int stage = 0;
   uint32_t parity = 0;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
         const int c = i * kTeam + tid;
-        if (c < C) store_elem(p.y, kOut, t * p.ldy + c, fmaf(v[i] * rstd, w[i], b[i]));
+        if (c < C) store_elem(p.y, kOut, t * p.ldy + c, fmaf(v[i] * rstd, w[c], b[c]));
       }
     };
     if (p.y_bf16)
@@ -348,13 +348,15 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
   }
 }
 
-// As norm_bwd_ring_plan, for rows of `stage` bytes in their slots.
-bool elem_plan(int64_t T, int64_t C, int64_t stage, bool sums, int sms, RingPlan* out) {
+// As norm_bwd_ring_plan, for rows of `stage` bytes in their slots; an SM holds
+// 512 x ctas_each threads, and a CTA has `before` bytes before its rings.
+bool elem_plan(int64_t T, int64_t C, int64_t stage, bool sums, int ctas_each, int64_t before,
+               int sms, RingPlan* out) {
   if (sms <= 0 || C > 512 * kCols) return false;
   RingPlan r{};
   r.team = C <= 32 * kCols ? 32 : C <= 128 * kCols ? 128 : 512;
-  const int per_sm = r.team == 32 ? 1 : 512 / r.team;
-  if (sms * per_sm > kMostSlabs) sms = kMostSlabs / per_sm;
+  const int per_sm = ctas_each * (r.team == 32 ? 1 : 512 / r.team);
+  if (sums && sms * per_sm > kMostSlabs) sms = kMostSlabs / per_sm;
   r.smem_most = (size_t)(228 / per_sm - 1) * 1024 - 512;
   r.stage_bytes = (int)stage;
   const int64_t ctas_most = (int64_t)sms * per_sm, rows_each = (T + ctas_most - 1) / ctas_most;
@@ -363,7 +365,9 @@ bool elem_plan(int64_t T, int64_t C, int64_t stage, bool sums, int sms, RingPlan
   const int64_t ctas = (T + r.teams - 1) / r.teams;
   r.grid = (int)(ctas < ctas_most ? ctas : ctas_most);
   const int64_t rows = (T + (int64_t)r.grid * r.teams - 1) / ((int64_t)r.grid * r.teams);
-  const size_t fixed = 8 * 8 * r.teams;
+  r.before = (int)((before + 15) / 16 * 16);
+  const size_t fixed = 8 * 8 * r.teams + r.before;
+  if (fixed > r.smem_most) return false;
   int64_t fit = (int64_t)(r.smem_most - fixed) / (stage * r.teams);
   if (fit > 8) fit = 8;
   r.stages = (int)(fit < rows ? fit : rows);
@@ -400,7 +404,7 @@ cudaError_t pick_bwd(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
 
 bool norm_fwd_elem_plan(const NormFwd& p, int sms, RingPlan* out) {
   const int64_t slot = slot_bytes(p.C * (p.x_bf16 ? 2 : 4));
-  return elem_plan(p.T, p.C, slot * (p.residual ? 2 : 1), false, sms, out);
+  return elem_plan(p.T, p.C, slot * (p.residual ? 2 : 1), false, 2, p.C * 8, sms, out);
 }
 cudaError_t launch_norm_fwd_elem(const NormFwd& p, const RingPlan& r, cudaStream_t st) {
   return p.x_bf16 ? pick_fwd<true>(p, r, st) : pick_fwd<false>(p, r, st);
@@ -409,7 +413,7 @@ cudaError_t launch_norm_fwd_elem(const NormFwd& p, const RingPlan& r, cudaStream
 bool norm_bwd_elem_plan(const NormBwd& p, int sms, RingPlan* out) {
   const int64_t stage = slot_bytes(p.C * (p.x_bf16 ? 2 : 4)) + slot_bytes(p.C * (p.gy_bf16 ? 2 : 4)) +
                         (p.gres ? slot_bytes(p.C * (p.gx_bf16 ? 2 : 4)) : 0);
-  return elem_plan(p.T, p.C, stage, p.part != nullptr, sms, out);
+  return elem_plan(p.T, p.C, stage, p.part != nullptr, 1, 0, sms, out);
 }
 cudaError_t launch_norm_bwd_elem(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
   return p.x_bf16 ? p.gy_bf16 ? pick_bwd<true, true>(p, r, st) : pick_bwd<true, false>(p, r, st)

@@ -19,6 +19,7 @@ constexpr int ring_threads(int team, int units) {
 struct RingPlan {
   int team, units;  // threads of a team, groups of four columns of each
   int teams, stages, stage_bytes, grid;
+  int before;       // bytes of a CTA's shared memory before its rings
   size_t smem, smem_most;
 };
 bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out);
