@@ -714,3 +714,42 @@ def test_rows_past_32_bit_offsets():
     nc = hlq.hlq_clip_grad_norm([x], 1.0, norm_only=True)
     norm, _ = clip64([f64(x[-3:])], 1.0)
     check(f64(nc)[:1], norm, 512 * U * norm, "norm")
+
+
+@pytest.mark.parametrize("T,C", [(2500, 768), (5000, 2048), (2000, 4096), (700, 8192), (500, 14336),
+                                 (4000, 24), (3000, 77), (2500, 1001), (900, 5663)])
+@pytest.mark.parametrize("x_dt,gy_dt", [(BF16, F32), (F32, BF16)])
+def test_layer_norm_backward_many_rows_a_cta(T, C, x_dt, gy_dt):
+    """More rows than fit a CTA's stages, several calls on their way at once:
+    every stage is filled and read many times over."""
+    r = rng(T, C, 5)
+    x, gr = dev(r.normal(size=(T, C)), x_dt), dev(r.normal(size=(T, C)), x_dt)
+    w, gy = dev(1 + 0.2 * r.normal(size=C)), dev(r.normal(size=(T, C)), gy_dt)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        y, mean, rstd = hlq.hlq_layer_norm(x, w)
+        got = [hlq.hlq_layer_norm_backward(gy, x, mean, rstd, w, g_residual=gr) for _ in range(3)]
+    check_norm((y, mean, rstd), f64(x), f64(w), 0.0, x_dt)
+    check_norm_bwd(got[0], gy, x, mean, rstd, w, gr)
+    for other in got[1:]:
+        for p, q in zip(other, got[0]):
+            assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("T,V,dt", [(700, 3000, BF16), (700, 40000, BF16), (500, 70001, F32)])
+def test_logprobs_do_not_depend_on_the_number_of_rows(T, V, dt):
+    """The same bits for a row alone, in a few rows, in many, and from the
+    policy loss: the ratio of an unchanged policy is exactly 1.  (Rows of one
+    tensor begin at different offsets from 16 bytes, so a row alone is compared
+    where it lies.)"""
+    z, a = logits_case(T, V, dt, rng(T, V, 6))
+    a = torch.from_numpy(a).cuda()
+    many, lse = hlq.hlq_token_logprobs(z, a)
+    for lo, hi in ((0, 1), (3, 4), (T - 5, T), (100, 300)):
+        few = hlq.hlq_token_logprobs(z[lo:hi], a[lo:hi])
+        assert torch.equal(few[0], many[lo:hi]) and torch.equal(few[1], lse[lo:hi])
+    ones = torch.ones(T, device="cuda")
+    stats, logp, _ = hlq.hlq_policy_loss(z, a, many, ones, ones / T, ref_logp=many, kl_coef=0.1)
+    assert torch.equal(logp, many)
+    assert float(stats[2]) == 0.0 and float(stats[3]) == 0.0
+    assert abs(float(stats[0]) + 1.0) <= 1e-5
