@@ -64,20 +64,20 @@ struct Slice {
   static constexpr int kSize = kBf16 ? 2 : 4, kVec = 16 / kSize;
   static constexpr int kGroup = 16 / kVec;  // vectors of a group
   const char* row;
-  int64_t e0, edge;  // edge: this thread's single element, -1: none
-  int n;
-  __device__ __forceinline__ Slice(const void* base, int64_t offset, int64_t V, int slice,
+  int e0, n;  // V is below 2^31
+  int edge;   // this thread's single element, -1: none
+  __device__ __forceinline__ Slice(const void* base, int64_t offset, int V, int slice,
                                    int log_slices) {
     row = static_cast<const char*>(base) + offset * kSize;
-    int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / kSize;
-    if (head > V) head = V;
-    const int64_t vecs = (V - head) / kVec, per = (vecs + (1 << log_slices) - 1) >> log_slices;
-    const int64_t v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
+    const int phase = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    const int head = min((16 - phase) % 16 / kSize, V);
+    const int vecs = (V - head) / kVec, per = (vecs + (1 << log_slices) - 1) >> log_slices;
+    const int v0 = min(slice * per, vecs);
+    n = min(per, vecs - v0);
     e0 = head + v0 * kVec;
-    n = (int)(v1 - v0);
     edge = -1;
     if (slice == 0 && threadIdx.x < 16) {
-      const int64_t j = threadIdx.x, after = head + vecs * kVec + j - 8;
+      const int j = threadIdx.x, after = head + vecs * kVec + j - 8;
       if (j < 8 ? j < head : after < V) edge = j < 8 ? j : after;
     }
   }
@@ -86,7 +86,7 @@ struct Slice {
   // groups' loads from going out together: 323 -> 352 us at 4096 x 128256.)
   static constexpr int kStep = kGroup * kThreads;  // vectors of a group of all threads
   __device__ __forceinline__ void load(int j, uint4 (&raw)[kGroup]) const {
-    const uint4* at = reinterpret_cast<const uint4*>(row + e0 * kSize) + (j + (int)threadIdx.x);
+    const uint4* at = reinterpret_cast<const uint4*>(row + (int64_t)e0 * kSize) + (j + (int)threadIdx.x);
     constexpr uint32_t none = kBf16 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
     for (int i = 0; i < kGroup; ++i)
@@ -159,6 +159,19 @@ struct Running {
   }
 };
 
+// The pairs of kLanes neighbouring lanes joined, the same in each: the maximum
+// first, then the sums relative to it.
+template <int kLanes>
+__device__ __forceinline__ MaxSum lanes_pair(MaxSum p, float c) {
+  float m = p.m;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = p.s * ex2((p.m - m) * c);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return {m, s};
+}
+
 // The CTA's pair, in its first warp; `warp_pair` may be written again after
 // the next __syncthreads but one.
 __device__ __forceinline__ MaxSum cta_pair(MaxSum p, bool has_edge, float edge, float c,
@@ -168,17 +181,10 @@ __device__ __forceinline__ MaxSum cta_pair(MaxSum p, bool has_edge, float edge, 
     const float m = fmaxf(edge, -FLT_MAX);
     p = join(p, {m, ex2((edge - m) * c)}, c);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    p = join(p, {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)}, c);
+  p = lanes_pair<32>(p, c);
   if (lane == 0) warp_pair[tid >> 5] = p;
   __syncthreads();
-  if (tid < 32) {
-    p = warp_pair[lane % kWarps];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1)
-      p = join(p, {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)}, c);
-  }
+  if (tid < 32) p = lanes_pair<kWarps>(warp_pair[lane % kWarps], c);
   return p;
 }
 
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_cluster_kernel(TokenLogprob
   pdl_wait();
   pdl_trigger();
   if (log_slices) cluster_started_arrive();
-  const S sl(p.logits, t * p.ld, p.V, slice, log_slices);
+  const S sl(p.logits, t * p.ld, (int)p.V, slice, log_slices);
   int64_t a = -1;
   float logit = 0.f;
   if (slice == 0 && threadIdx.x == 0) {
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
   int64_t t = blockIdx.x;
   if (t >= p.T) return;
   int slice = 0, flip = 0;
-  S sl(p.logits, t * p.ld, p.V, 0, log_slices);
+  S sl(p.logits, t * p.ld, (int)p.V, 0, log_slices);
   int b = 0;
   uint4 raw[kGroups][S::kGroup];
 #pragma unroll
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
     const int b_next = slice_ends ? 0 : b + kGroups * S::kStep;
     const bool more = t_next < p.T;
     S next = sl;
-    if (slice_ends && more) next = S(p.logits, t_next * p.ld, p.V, slice_next, log_slices);
+    if (slice_ends && more) next = S(p.logits, t_next * p.ld, (int)p.V, slice_next, log_slices);
     float edge_next = edge;
     if (slice_ends && more && next.edge >= 0) edge_next = next.elem(next.edge);
 #pragma unroll
@@ -353,12 +359,12 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
   pdl_wait();
   pdl_trigger();
   const float w = p.weight[t];
-  const S sl(p.logits, t * p.ld, p.V, slice, log_slices);
+  const S sl(p.logits, t * p.ld, (int)p.V, slice, log_slices);
   char* g = static_cast<char*>(p.g) + t * p.ldg * S::kSize;
   auto put = [&](int j, const F2* v) {
     const int64_t e = sl.e0 + (int64_t)j * S::kVec;
     if constexpr (kAligned) {
-      reinterpret_cast<uint4*>(g + sl.e0 * S::kSize)[j] = narrow<kBf16>(v);
+      reinterpret_cast<uint4*>(g + (int64_t)sl.e0 * S::kSize)[j] = narrow<kBf16>(v);
     } else {
 #pragma unroll
       for (int k = 0; k < S::kVec / 2; ++k) {
