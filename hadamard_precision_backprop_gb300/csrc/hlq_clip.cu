@@ -7,6 +7,13 @@
 // captured with.  The tensors are cut into chunks of 8192 elements; a CTA
 // takes a run of consecutive chunks, and each of its threads 32 elements of a
 // chunk, all loaded before the first is used.
+//
+// Bound by HBM: the gradients are read for the norm and again for the product,
+// because no chip holds them in between (what L2 still holds is read first).
+// 236 M fp32 gradients in 192 tensors, written as bf16 (2.36 GB in the two
+// passes): 350 us, 1.01 of the measured copy rate; the bytes read once and
+// written once would be 212 us.  A few small tensors take the time of two
+// launches (10 us with the host's work for 24 of them).
 #include "hlq_device.cuh"
 #include "hlq_kernels.h"
 #include "hlq_rows.cuh"

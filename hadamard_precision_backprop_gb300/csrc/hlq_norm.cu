@@ -44,6 +44,11 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
 // 16-byte accesses, 32 elements a thread at most.  kUnit = 1: single elements,
 // 16 a thread, for rows that are not made of aligned groups of eight and too
 // long for hlq_norm_elem.cu.
+//
+// Bound by HBM: 16384 x 4096 bf16 with a residual (537 MB) takes 84 us, 0.95 of
+// the measured copy rate; 12608 x 768 without one 15 us, 0.76 (launch and last
+// wave).  The team is the smallest of 8, 32, 128 and 512 threads that holds the
+// row: more rows per SM are then under way, and short rows need no barrier.
 // ---------------------------------------------------------------------------
 constexpr int kHeldVec = 32, kHeldElem = 16;
 
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kTeam < 128 ? 128 : kTeam) norm_fwd_kernel(Nor
   }
 }
 
-// Rows too long for registers: three passes,
+// Rows too long for registers (above 16384 elements): three passes,
 // the later ones from L2.
 constexpr int kLongThreads = 1024;
 
@@ -224,7 +229,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_cols_kernel(NormBwd p) {
 }
 
 // The slabs' partial sums joined: a CTA takes 32 of the 2 C sums, its eight
-// warps every eighth slab each.
+// warps every eighth slab each (16 warps: 12 instead of 8 us for 152 slabs of
+// 14336 columns).
 __global__ void __launch_bounds__(256) norm_bwd_join_kernel(NormBwd p, int slabs) {
   __shared__ float red[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -268,8 +274,14 @@ cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
 
 }  // namespace
 
-// The ring's shape: as many stages as fit (at most 8, and no more than a team
-// has rows).  False: the rows are not for the ring, or do not fit.
+// The ring's shape.  Teams: a warp up to 1024 columns (16 or 24 of them in the
+// SM's one CTA: 8 that kept the first pass's values took 28.6 us at 12608 x 768
+// where 16 take 24), CTAs of 128 threads, four an SM, up to 2048 (one of 256
+// threads, two an SM: 64 us at 16384 x 2048 where these take 60), of 256, two an
+// SM, up to 4096 (four teams of 128 threads in one CTA left one stage each: 138
+// us at 16384 x 4096 where these take 105), of 512 above.  As many stages as
+// fit, at most 8 and no more than a team has rows.  False: the rows are not for
+// the ring, or do not fit.
 bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out) {
   if (sms <= 0 || p.C > 512 * kMostUnits * 4 || !rows_of_eight(p.x, p.ldx, p.x_bf16, p.T, p.C) ||
       !rows_of_eight(p.gy, p.ldgy, p.gy_bf16, p.T, p.C) ||

@@ -9,6 +9,12 @@
 // and a thread moves the few elements around them.  From there on the work is
 // by single elements: a thread owns up to 16 columns that lie kTeam apart, so
 // that a warp's accesses are consecutive.
+//
+// Bound by instructions and by the barriers of its reductions, not by bytes
+// (two- and four-byte accesses, some 20 instructions an element): forward 4689 x
+// 5663 bf16 48 us (16 us of bytes), backward with fp32 g_y 81 us (32); with the
+// rows loaded into registers by single elements instead, without a ring, these
+// took 73 and 104 us.
 #include "hlq_device.cuh"
 #include "hlq_norm_ring.cuh"
 #include "hlq_rows.cuh"

@@ -2,12 +2,24 @@
 //
 // A team of kTeam threads takes every (number of teams)-th row: a warp, with
 // several in a CTA and one CTA per SM, or for longer rows the whole CTA, one
-// or two per SM.  The rows of x, g_y and the residual's gradient come into a ring of
-// shared-memory stages by bulk copies, several rows ahead; each thread owns up
-// to kUnits groups of four columns and keeps their weights, and their sums
-// for g_w and g_b over all its rows, in registers.  The CTA's teams add their
-// sums in shared memory and write one slab of partial sums, which
+// to four per SM.  The rows of x, g_y and the residual's gradient come into a
+// ring of shared-memory stages by bulk copies, several rows ahead; each thread
+// owns up to kUnits groups of four columns and keeps their weights, and their
+// sums for g_w and g_b over all its rows, in registers.  The CTA's teams add
+// their sums in shared memory and write one slab of partial sums, which
 // norm_bwd_join_kernel adds.
+//
+// Bound by HBM for long rows: 16384 x 14336 bf16 (1.41 GB) in 206 us, 1.02 of
+// the measured copy rate, 16384 x 4096 with fp32 g_y and a residual (671 MB) in
+// 104 us, 0.97.  At 12608 x 768 (97 MB, 25 us) each further row costs what its
+// bytes do (1.15 us for 1000), and the rest is about 10 us of launch, first
+// copies, the sums' joining and its launch.
+//
+// Groups of four: fp32 and bf16 columns both lie next to each other over a
+// warp, without bank conflicts; pairs of fp32 go through one instruction (26
+// instructions an element before that and before the output type was decided
+// outside the column loop: 264 us at 16384 x 14336).  Rows go to CTAs in turn,
+// not in runs: with a run of consecutive rows for each CTA that case took 246.
 #pragma once
 
 #include <type_traits>

@@ -540,8 +540,9 @@ size_t hlq_noalloc_scratch_bytes(void);
  *    rows that all begin on 16-byte boundaries are moved fastest;
  *  - an output may be exactly one of the call's inputs of the same type and
  *    stride (in place); other overlaps are not allowed;
- *  - all sums are taken in fp32 (the norm's in fp64 across threads) in an
- *    order fixed by the sizes and the GPU: equal calls give equal bits;
+ *  - all sums are taken in fp32 (the norm's in fp64 where fp32 would overflow
+ *    or lose small terms) in an order fixed by the sizes, the alignments and the
+ *    GPU: equal calls give equal bits;
  *  - device flags: HLQ_DEV_NONFINITE where a row's statistics, its loss
  *    coefficient or the norm is infinite or NaN (outputs follow the formulas),
  *    HLQ_DEV_BADCODE where a token is outside [0, V).
@@ -588,7 +589,9 @@ size_t hlq_layer_norm_backward_workspace_bytes(int64_t T, int64_t C);
  * a NaN and HLQ_DEV_BADCODE.  Logits of -inf are tokens of probability 0; a
  * row of nothing else has no distribution (NaN).  logp, lse fp32 [T]; d_lse
  * may be NULL.  Serves for the old and the reference log-probabilities of
- * hlq_policy_loss.
+ * hlq_policy_loss: a row gives the same bits in both, whatever the number of
+ * rows, so that the ratio of an unchanged policy is exactly 1.  T <= (2^31 - 1)
+ * / 8.
  */
 hlq_status hlq_token_logprobs(const void *d_logits, int64_t ld, int dt,
                               const int64_t *d_targets, int64_t T, int64_t V, float scale,
