@@ -12,9 +12,11 @@
 //
 // Bound by instructions and by the barriers of its reductions, not by bytes
 // (two- and four-byte accesses, some 20 instructions an element): forward 4689 x
-// 5663 bf16 48 us (16 us of bytes), backward with fp32 g_y 81 us (32); with the
+// 5663 bf16 49 us (16 us of bytes), backward with fp32 g_y 77 us (32); with the
 // rows loaded into registers by single elements instead, without a ring, these
-// took 73 and 104 us.
+// took 73 and 104 us.  A warp's lanes copy one matrix's row each: one lane for
+// all of them took longer than the rest of a short row's work (20000 x 77
+// backward 43 -> 22 us).
 #include "hlq_device.cuh"
 #include "hlq_norm_ring.cuh"
 #include "hlq_rows.cuh"
@@ -44,7 +46,7 @@ __device__ __forceinline__ Span span_of(const void* base, int64_t ld_bytes, int6
 }
 // A row's place in its slot.
 __device__ __forceinline__ int row_at(const void* base, int64_t ld_bytes, int64_t t) {
-  return (int)((reinterpret_cast<uint64_t>(base) + t * ld_bytes) & 15);
+  return ((uint32_t)reinterpret_cast<uint64_t>(base) + (uint32_t)t * (uint32_t)ld_bytes) & 15;
 }
 __host__ __device__ constexpr int slot_bytes(int64_t bytes) {
   return (int)((bytes + 15) / 16 * 16 + 16);
@@ -71,33 +73,58 @@ __device__ __forceinline__ void copy_edges(const Span& s, int64_t bytes, int siz
   }
 }
 
-// Up to three matrices whose rows are copied together.
+// The matrix that a lane copies the rows of.
 struct Source {
   const void* base;
   int64_t ld_bytes, bytes;
   int size, slot;  // element size; the slot's offset in a stage
 };
 
-// Rows t of `n` matrices into a stage, by one thread.
-template <int kMost>
-__device__ __forceinline__ void issue_rows(const Source (&src)[kMost], int n, int64_t rows,
-                                           int64_t t, unsigned char* stage, uint64_t* bar) {
+// Row t of the first `n` lanes' matrices into a stage, by one warp together.
+__device__ __forceinline__ void issue_rows(const Source& src, int n, int64_t rows, int64_t t,
+                                           unsigned char* stage, uint64_t* bar) {
+  const int lane = threadIdx.x & 31;
+  Span s = {};
+  if (lane < n) {
+    s = span_of(src.base, src.ld_bytes, src.bytes, rows, t);
+    if (s.from > s.row || s.to < s.row + src.bytes)
+      copy_edges(s, src.bytes, src.size, stage + src.slot);
+  }
+  const uint32_t bytes = (uint32_t)(s.to - s.from);
   uint32_t total = 0;
 #pragma unroll
-  for (int k = 0; k < kMost; ++k)
-    if (k < n) {
-      const Span s = span_of(src[k].base, src[k].ld_bytes, src[k].bytes, rows, t);
-      total += (uint32_t)(s.to - s.from);
-      if (s.from > s.row || s.to < s.row + src[k].bytes)
-        copy_edges(s, src[k].bytes, src[k].size, stage + src[k].slot);
-    }
-  mbar_expect_tx(bar, total);  // an arrival: releases the elements just copied
+  for (int k = 0; k < 3; ++k) total += __shfl_sync(0xffffffffu, bytes, k);  // 0 from lane n on
+  __syncwarp();
+  if (lane == 0) mbar_expect_tx(bar, total);  // an arrival: releases the elements just copied
+  __syncwarp();
+  if (bytes > 0)
+    bulk_load(saddr(stage + src.slot) + (uint32_t)(s.from - (s.row & ~15ull)),
+              reinterpret_cast<const void*>(s.from), bytes, bar);
+  __syncwarp();
+}
+
+// The same by one thread, after another (and then its warp together again).
+__device__ __forceinline__ void issue_rows_alone(const Source& a, const Source& b, int n,
+                                                 int64_t rows, int64_t t, unsigned char* stage,
+                                                 uint64_t* bar) {
+  uint32_t total = 0;
 #pragma unroll
-  for (int k = 0; k < kMost; ++k)
+  for (int k = 0; k < 2; ++k)
     if (k < n) {
-      const Span s = span_of(src[k].base, src[k].ld_bytes, src[k].bytes, rows, t);
+      const Source& src = k ? b : a;
+      const Span s = span_of(src.base, src.ld_bytes, src.bytes, rows, t);
+      total += (uint32_t)(s.to - s.from);
+      if (s.from > s.row || s.to < s.row + src.bytes)
+        copy_edges(s, src.bytes, src.size, stage + src.slot);
+    }
+  mbar_expect_tx(bar, total);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < n) {
+      const Source& src = k ? b : a;
+      const Span s = span_of(src.base, src.ld_bytes, src.bytes, rows, t);
       if (s.to > s.from)
-        bulk_load(saddr(stage + src[k].slot) + (uint32_t)(s.from - (s.row & ~15ull)),
+        bulk_load(saddr(stage + src.slot) + (uint32_t)(s.from - (s.row & ~15ull)),
                   reinterpret_cast<const void*>(s.from), (uint32_t)(s.to - s.from), bar);
     }
 }
@@ -177,18 +204,26 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 2 : 1024 / 
     w[c] = p.weight ? load_elem(p.weight, p.w_bf16, c) : 1.f;
     b[c] = p.bias ? load_elem(p.bias, p.w_bf16, c) : 0.f;
   }
-  const Source src[2] = {
-      {p.x, p.ldx * kSize, p.C * kSize, kSize, 0},
-      {p.residual, p.ldr * kSize, p.C * kSize, kSize, slot_bytes(p.C * kSize)}};
+  const int lane = threadIdx.x & 31;
+  const int64_t x_ld = p.ldx * kSize, r_ld = p.ldr * kSize;
+  const int r_slot = slot_bytes(p.C * kSize);
+  const Source x_src = {p.x, x_ld, p.C * kSize, kSize, 0};
+  const Source r_src = {p.residual, r_ld, p.C * kSize, kSize, r_slot};
   const int64_t step = (int64_t)gridDim.x * plan.teams;
-  const int64_t t0 = (int64_t)blockIdx.x * plan.teams + team;
+  const int64_t t0 = blockIdx.x + (int64_t)gridDim.x * team;
+  // a warp's short rows by its lanes together, the longer ones by one thread
+  // (49 against 60 us at 4689 x 5663)
   auto issue = [&](int64_t t, int s) {
-    if (t < p.T && !*(volatile int*)&abort_flag)
-      issue_rows(src, p.residual ? 2 : 1, p.T, t, ring.stages + (size_t)s * plan.stage_bytes,
-                 &ring.full[s]);
+    unsigned char* to = ring.stages + (size_t)s * plan.stage_bytes;
+    if constexpr (kTeam == 32) {
+      if (t < p.T && !__shfl_sync(0xffffffffu, *(volatile int*)&abort_flag, 0))
+        issue_rows(lane == 0 ? x_src : r_src, p.residual ? 2 : 1, p.T, t, to, &ring.full[s]);
+    } else {
+      if (tid == 0 && t < p.T && !*(volatile int*)&abort_flag)
+        issue_rows_alone(x_src, r_src, p.residual ? 2 : 1, p.T, t, to, &ring.full[s]);
+    }
   };
-  if (tid == 0)
-    for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
+  for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
   __syncthreads();
   const float inv = 1.f / (float)C;
   int stage = 0;
@@ -196,8 +231,8 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 2 : 1024 / 
   for (int64_t t = t0; t < p.T; t += step) {
     mbar_wait(&ring.full[stage], parity, &abort_flag, p.status);
     const unsigned char* at = ring.stages + (size_t)stage * plan.stage_bytes;
-    const unsigned char* xs = at + row_at(p.x, src[0].ld_bytes, t);
-    const unsigned char* rs = at + src[1].slot + row_at(p.residual, src[1].ld_bytes, t);
+    const unsigned char* xs = at + row_at(p.x, x_ld, t);
+    const unsigned char* rs = at + r_slot + row_at(p.residual, r_ld, t);
     float v[kCols], s = 0.f;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
@@ -243,7 +278,7 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 2 : 1024 / 
       if (!(fabsf(mean) < INFINITY && rstd < INFINITY)) raise_flag(p.status, HLQ_DEV_NONFINITE);
     }
     team_sync<kTeam>();  // the stage has been read by the whole team
-    if (tid == 0) issue(t + plan.stages * step, stage);
+    issue(t + plan.stages * step, stage);
     __syncwarp();
     if (++stage == plan.stages) stage = 0, parity ^= 1;
   }
@@ -262,19 +297,21 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
   pdl_wait();
   pdl_trigger();
   const int gy_slot = slot_bytes(p.C * kSx), r_slot = gy_slot + slot_bytes(p.C * kSg);
-  const Source src[3] = {{p.x, p.ldx * kSx, p.C * kSx, kSx, 0},
-                         {p.gy, p.ldgy * kSg, p.C * kSg, kSg, gy_slot},
-                         {p.gres, p.ldgr * sr, p.C * sr, sr, r_slot}};
+  const int lane = threadIdx.x & 31;
+  const int64_t x_ld = p.ldx * kSx, gy_ld = p.ldgy * kSg, r_ld = p.ldgr * sr;
+  const int size = lane == 0 ? kSx : lane == 1 ? kSg : sr;
+  const Source src = {lane == 0 ? p.x : lane == 1 ? p.gy : p.gres,
+                      lane == 0 ? x_ld : lane == 1 ? gy_ld : r_ld, p.C * size, size,
+                      lane == 0 ? 0 : lane == 1 ? gy_slot : r_slot};
   const int64_t step = (int64_t)gridDim.x * plan.teams;
-  const int64_t t0 = (int64_t)blockIdx.x * plan.teams + team;
+  const int64_t t0 = blockIdx.x + (int64_t)gridDim.x * team;
   auto issue = [&](int64_t t, int s) {
-    if (t < p.T && !*(volatile int*)&abort_flag)
+    if (t < p.T && !__shfl_sync(0xffffffffu, *(volatile int*)&abort_flag, 0))
       issue_rows(src, p.gres ? 3 : 2, p.T, t, ring.stages + (size_t)s * plan.stage_bytes,
                  &ring.full[s]);
   };
-  if (tid == 0)
+  if (tid < 32)
     for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
-  __syncwarp();
   float w[kCols], gw[kCols], gb[kCols];
 #pragma unroll
   for (int i = 0; i < kCols; ++i) {
@@ -292,9 +329,9 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
     if (t + step < p.T) mean_next = p.mean[t + step], rstd_next = p.rstd[t + step];
     mbar_wait(&ring.full[stage], parity, &abort_flag, p.status);
     const unsigned char* at = ring.stages + (size_t)stage * plan.stage_bytes;
-    const unsigned char* xs = at + row_at(p.x, src[0].ld_bytes, t);
-    const unsigned char* gs = at + gy_slot + row_at(p.gy, src[1].ld_bytes, t);
-    const unsigned char* rs = at + r_slot + row_at(p.gres, src[2].ld_bytes, t);
+    const unsigned char* xs = at + row_at(p.x, x_ld, t);
+    const unsigned char* gs = at + gy_slot + row_at(p.gy, gy_ld, t);
+    const unsigned char* rs = at + r_slot + row_at(p.gres, r_ld, t);
     float xhat[kCols], a[kCols], sa = 0.f, sx = 0.f;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
@@ -331,8 +368,7 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
     if (tid == 0 && !(fabsf(sa) < INFINITY && fabsf(sx) < INFINITY))
       raise_flag(p.status, HLQ_DEV_NONFINITE);
     team_sync<kTeam>();  // the stage has been read by the whole team
-    if (tid == 0) issue(t + plan.stages * step, stage);
-    __syncwarp();
+    if (tid < 32) issue(t + plan.stages * step, stage);
     if (++stage == plan.stages) stage = 0, parity ^= 1;
   }
   if (!p.part) return;

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
   pdl_trigger();
 
   const int64_t step = (int64_t)gridDim.x * plan.teams;
-  const int64_t t0 = (int64_t)blockIdx.x * plan.teams + team;
+  const int64_t t0 = blockIdx.x + (int64_t)gridDim.x * team;
   auto issue = [&](int64_t t, int s) {
     if (t >= p.T || *(volatile int*)&abort_flag) return;
     const uint32_t dst = saddr(ring + (size_t)s * plan.stage_bytes);
