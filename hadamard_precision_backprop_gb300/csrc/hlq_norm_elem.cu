@@ -213,14 +213,19 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 2 : 1024 / 
   const int64_t t0 = blockIdx.x + (int64_t)gridDim.x * team;
   // a warp's short rows by its lanes together, the longer ones by one thread
   // (49 against 60 us at 4689 x 5663)
+  int64_t issued = 0;
   auto issue = [&](int64_t t, int s) {
     unsigned char* to = ring.stages + (size_t)s * plan.stage_bytes;
     if constexpr (kTeam == 32) {
-      if (t < p.T && !__shfl_sync(0xffffffffu, *(volatile int*)&abort_flag, 0))
+      if (t < p.T && !__shfl_sync(0xffffffffu, *(volatile int*)&abort_flag, 0)) {
+        ++issued;
         issue_rows(lane == 0 ? x_src : r_src, p.residual ? 2 : 1, p.T, t, to, &ring.full[s]);
+      }
     } else {
-      if (tid == 0 && t < p.T && !*(volatile int*)&abort_flag)
+      if (tid == 0 && t < p.T && !*(volatile int*)&abort_flag) {
+        ++issued;
         issue_rows_alone(x_src, r_src, p.residual ? 2 : 1, p.T, t, to, &ring.full[s]);
+      }
     }
   };
   for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
@@ -282,6 +287,7 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 2 : 1024 / 
     __syncwarp();
     if (++stage == plan.stages) stage = 0, parity ^= 1;
   }
+  if (tid == 0 && *(volatile int*)&abort_flag) ring_drain(ring.full, plan.stages, issued);
 }
 
 template <bool kXBf16, bool kGyBf16, int kTeam>
@@ -305,10 +311,12 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
                       lane == 0 ? 0 : lane == 1 ? gy_slot : r_slot};
   const int64_t step = (int64_t)gridDim.x * plan.teams;
   const int64_t t0 = blockIdx.x + (int64_t)gridDim.x * team;
+  int64_t issued = 0;
   auto issue = [&](int64_t t, int s) {
-    if (t < p.T && !__shfl_sync(0xffffffffu, *(volatile int*)&abort_flag, 0))
-      issue_rows(src, p.gres ? 3 : 2, p.T, t, ring.stages + (size_t)s * plan.stage_bytes,
-                 &ring.full[s]);
+    if (t >= p.T || __shfl_sync(0xffffffffu, *(volatile int*)&abort_flag, 0)) return;
+    ++issued;
+    issue_rows(src, p.gres ? 3 : 2, p.T, t, ring.stages + (size_t)s * plan.stage_bytes,
+               &ring.full[s]);
   };
   if (tid < 32)
     for (int s = 0; s < plan.stages; ++s) issue(t0 + s * step, s);
@@ -371,6 +379,7 @@ __global__ void __launch_bounds__(elem_threads(kTeam), kTeam == 32 ? 1 : 512 / k
     if (tid < 32) issue(t + plan.stages * step, stage);
     if (++stage == plan.stages) stage = 0, parity ^= 1;
   }
+  if (tid == 0 && *(volatile int*)&abort_flag) ring_drain(ring.full, plan.stages, issued);
   if (!p.part) return;
   float* slab = p.part + (size_t)blockIdx.x * 2 * p.C;
   float* sums = plan.teams == 1 ? slab : reinterpret_cast<float*>(smem) + team * 2 * C;

@@ -78,8 +78,10 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
 
   const int64_t step = (int64_t)gridDim.x * plan.teams;
   const int64_t t0 = blockIdx.x + (int64_t)gridDim.x * team;
+  int64_t issued = 0;
   auto issue = [&](int64_t t, int s) {
     if (t >= p.T || *(volatile int*)&abort_flag) return;
+    ++issued;
     const uint32_t dst = saddr(ring + (size_t)s * plan.stage_bytes);
     mbar_expect_tx(&full[s], (uint32_t)plan.stage_bytes);
     bulk_load(dst, static_cast<const char*>(p.x) + t * p.ldx * kSx, C * kSx, &full[s]);
@@ -178,6 +180,7 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
     __syncwarp();
     if (++stage == plan.stages) stage = 0, parity ^= 1;
   }
+  if (tid == 0 && *(volatile int*)&abort_flag) ring_drain(full, plan.stages, issued);
   if (!p.part) return;
   float* slab = p.part + (size_t)blockIdx.x * 2 * p.C;
   if (plan.teams == 1) {

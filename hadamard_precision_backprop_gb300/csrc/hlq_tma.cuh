@@ -91,6 +91,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity,
   return mbar_wait_for(b, parity, abort_flag, status, kWaitNs, cluster_scope);
 }
 
+// After a wait on a ring of stages gave up: wait, each within the same limit,
+// for the copies that are still on their way into shared memory.  `issued`
+// rows have been copied so far, row r into stage r % stages.
+__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int64_t issued) {
+  for (int s = 0; s < stages && s < issued; ++s) {
+    const uint32_t parity = (uint32_t)((issued - 1 - s) / stages) & 1;
+    const unsigned long long t0 = now_ns();
+    while (!mbar_test(&full[s], parity) && now_ns() - t0 < kWaitNs) {
+    }
+  }
+}
+
 // Address of the same shared-memory object in CTA `rank` of the cluster
 // (a shared::cluster address).
 __device__ __forceinline__ uint32_t cluster_map(uint32_t local_saddr, uint32_t rank) {
