@@ -185,7 +185,8 @@ struct NormBwd {
   bool gy_bf16, x_bf16, w_bf16, gx_bf16;  // gres has the type of gx
   unsigned int* status;
 };
-// g_x, and (with part) *slabs slabs of partial column sums, which the join adds.
+// g_x, and (with part) *slabs slabs of partial column sums, which the join
+// adds; 0 slabs: the column sums are written.
 int norm_bwd_most_slabs(int64_t T);
 cudaError_t launch_norm_bwd(const NormBwd& p, int* slabs, cudaStream_t st);
 cudaError_t launch_norm_bwd_join(const NormBwd& p, int slabs, cudaStream_t st);

@@ -20,6 +20,8 @@ struct RingPlan {
   int team, units;  // threads of a team, groups of four columns of each
   int teams, stages, stage_bytes, grid;
   int before;       // bytes of a CTA's shared memory before its rings
+  int cluster;      // the CTAs (all of them) are one cluster and join the sums
+                    // themselves; 0: they write slabs
   size_t smem, smem_most;
 };
 bool norm_bwd_ring_plan(const NormBwd& p, int sms, RingPlan* out);

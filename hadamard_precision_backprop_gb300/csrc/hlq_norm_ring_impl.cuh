@@ -7,7 +7,8 @@
 // owns up to kUnits groups of four columns and keeps their weights, and their
 // sums for g_w and g_b over all its rows, in registers.  The CTA's teams add
 // their sums in shared memory and write one slab of partial sums, which
-// norm_bwd_join_kernel adds.
+// norm_bwd_join_kernel adds; few rows go to one cluster, whose CTAs add their
+// sums through distributed shared memory.
 //
 // Bound by HBM for long rows: 16384 x 14336 bf16 (1.41 GB) in 206 us, 1.02 of
 // the measured copy rate, 16384 x 4096 with fp32 g_y and a residual (671 MB) in
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
   if (tid == 0 && *(volatile int*)&abort_flag) ring_drain(full, plan.stages, issued);
   if (!p.part) return;
   float* slab = p.part + (size_t)blockIdx.x * 2 * p.C;
-  if (plan.teams == 1) {
+  if (plan.teams == 1 && !plan.cluster) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int c = (i * kTeam + tid) * 4;
@@ -207,22 +208,57 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
     }
   }
   __syncthreads();
+  float* cta_sums = plan.cluster ? sums : slab;
   for (int c = threadIdx.x * 4; c < 2 * C; c += blockDim.x * 4) {
     Quad q = load4<false>(sums, c);
     for (int k = 1; k < plan.teams; ++k) {
       const Quad r = load4<false>(sums + k * 2 * C, c);
       q.v[0] = q.v[0] + r.v[0], q.v[1] = q.v[1] + r.v[1];
     }
-    store4<false>(slab, c, q);
+    store4<false>(cta_sums, c, q);
   }
+  if (!plan.cluster) return;
+  // Few rows: the CTAs are one cluster, and each adds a part of the columns
+  // over all of them, from their shared memory.
+  __syncthreads();
+  cluster_sync();
+  for (int c = (blockIdx.x * blockDim.x + threadIdx.x) * 4; c < 2 * C;
+       c += plan.cluster * blockDim.x * 4) {
+    float4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < plan.cluster; ++k) {
+      const float4 a = load_cluster(cluster_map(saddr(sums + c), k));
+      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    }
+    // C is a multiple of four: the group lies in one of the two
+    const bool first = c < C;
+    float* to = first ? p.gweight : p.gbias;
+    if (to) {
+      to += first ? c : c - C;
+      to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;  // any alignment
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while its sums may be read
 }
 
 template <bool kXBf16, bool kGyBf16, int kTeam, int kUnits>
 cudaError_t launch_ring(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
   const cudaError_t e = allow_smem<norm_bwd_ring_kernel<kXBf16, kGyBf16, kTeam, kUnits>>(r.smem_most);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_bwd_ring_kernel<kXBf16, kGyBf16, kTeam, kUnits>, dim3(r.grid),
-                    dim3(kTeam * r.teams), r.smem, st, p, r);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(r.grid);
+  cfg.blockDim = dim3(kTeam * r.teams);
+  cfg.dynamicSmemBytes = r.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = r.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = r.cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, norm_bwd_ring_kernel<kXBf16, kGyBf16, kTeam, kUnits>, p, r);
 }
 
 template <bool kXBf16, bool kGyBf16>

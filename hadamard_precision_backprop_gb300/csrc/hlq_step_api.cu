@@ -130,7 +130,7 @@ hlq_status hlq_layer_norm_backward(const void* d_gy, int64_t ldgy, int gy_dt, co
   if (!p.status) return HLQ_ERR_CUDA;
   int slabs = 0;
   HLQ_LAUNCH("norm_bwd", s, launch_norm_bwd(p, &slabs, s));
-  if (cols) HLQ_LAUNCH("norm_bwd_join", s, launch_norm_bwd_join(p, slabs, s));
+  if (slabs > 0 && cols) HLQ_LAUNCH("norm_bwd_join", s, launch_norm_bwd_join(p, slabs, s));
   return HLQ_OK;
 }
 

@@ -91,6 +91,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity,
   return mbar_wait_for(b, parity, abort_flag, status, kWaitNs, cluster_scope);
 }
 
+// Four floats of another CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // After a wait on a ring of stages gave up: wait, each within the same limit,
 // for the copies that are still on their way into shared memory.  `issued`
 // rows have been copied so far, row r into stage r % stages.

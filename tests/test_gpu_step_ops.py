@@ -753,3 +753,41 @@ def test_logprobs_do_not_depend_on_the_number_of_rows(T, V, dt):
     assert torch.equal(logp, many)
     assert float(stats[2]) == 0.0 and float(stats[3]) == 0.0
     assert abs(float(stats[0]) + 1.0) <= 1e-5
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 16, 17, 128, 129, 255, 256, 257])
+@pytest.mark.parametrize("C", [8, 264, 768, 1024, 2048, 9000])
+def test_layer_norm_backward_few_rows(T, C):
+    """Where the column sums are joined by one cluster, and just beyond."""
+    if C > 1024 and T > 17:
+        T -= 100 if T > 100 else 0
+    r = rng(T, C, 8)
+    x, gy, w = dev(r.normal(size=(T, C)), BF16), dev(r.normal(size=(T, C))), dev(r.normal(size=C))
+    _, mean, rstd = hlq.hlq_layer_norm(x)
+    got = hlq.hlq_layer_norm_backward(gy, x, mean, rstd, w)
+    check_norm_bwd(got, gy, x, mean, rstd, w, None)
+
+
+def test_outputs_given_or_made_are_the_same_bits():
+    """A call that makes its outputs (in one step of the extension) and one that
+    is given them (through Python)."""
+    r = rng(41)
+    x, w, b = dev(r.normal(size=(50, 264)), BF16), dev(r.normal(size=264)), dev(r.normal(size=264))
+    made = hlq.hlq_layer_norm(x, w, b)
+    given = hlq.hlq_layer_norm(x, w, b, out=torch.empty_like(x))
+    gy = dev(r.normal(size=(50, 264)))
+    made += hlq.hlq_layer_norm_backward(gy, x, *made[1:3], w)
+    given += hlq.hlq_layer_norm_backward(gy, x, *given[1:3], w, out=torch.empty_like(x))
+    z, a, old, adv, wt, ref = policy_inputs(9, 700, BF16, r, 1.0, 0.2, 0.2)
+    made += hlq.hlq_token_logprobs(z, a)
+    given += hlq.hlq_token_logprobs(z, a, logp=torch.empty(9, device="cuda"))
+    made += hlq.hlq_policy_loss(z, a, old, adv, wt, ref_logp=ref, kl_coef=0.1)
+    given += hlq.hlq_policy_loss(z, a, old, adv, wt, ref_logp=ref, kl_coef=0.1,
+                                 out=torch.empty_like(z))
+    g = [dev(r.normal(size=n)) for n in (5, 9000)]
+    made += (hlq.hlq_clip_grad_norm(g, 1.0, norm_only=True),)
+    given += (hlq.hlq_clip_grad_norm(g, 1.0, norm_only=True,
+                                     norm_coef=torch.empty(2, device="cuda")),)
+    assert len(made) == len(given) == 12
+    for p, q in zip(made, given):
+        assert torch.equal(p, q)
