@@ -13,7 +13,9 @@
 // 236 M fp32 gradients in 192 tensors, written as bf16 (2.36 GB in the two
 // passes): 350 us, 1.01 of the measured copy rate; the bytes read once and
 // written once would be 212 us.  A few small tensors take the time of two
-// launches (10 us with the host's work for 24 of them).
+// launches (9 us with the host's work for 24 of them).  54 M gradients whose
+// outputs begin anywhere in a flat buffer: 118 us where 49 M aligned ones take
+// 80 (the ends of each warp's run are stored one by one).
 #include "hlq_device.cuh"
 #include "hlq_kernels.h"
 #include "hlq_rows.cuh"
@@ -38,45 +40,116 @@ __device__ __forceinline__ int tensor_of(const ClipTable& tab, int64_t k) {
   return lo;
 }
 
-// This thread's elements of a chunk of n elements that begins at `e0` of the
-// tensor, zeros past its end: groups of four where the tensor is aligned to
-// them, else single elements a CTA width apart.  Element (i, k) is number
-// (i * kThreads + threadIdx.x) * 4 + k of the chunk, or
-// (i * 4 + k) * kThreads + threadIdx.x.
-__device__ __forceinline__ int64_t place(bool four, int i, int k) {
-  return four ? ((int64_t)i * kThreads + threadIdx.x) * 4 + k
-              : ((int64_t)i * 4 + k) * kThreads + threadIdx.x;
+// A tensor's elements are taken in groups of four that are aligned in its
+// input: the up to three elements before the first group go one by one with
+// the tensor's first chunk, and chunk c holds the 8192 elements from
+// head + 8192 c on.  Group (i, thread) of a chunk begins at its element
+// place(i).
+__device__ __forceinline__ int head_of(const void* p, bool bf16) {
+  return (int)(4 - ((reinterpret_cast<uintptr_t>(p) >> (bf16 ? 1 : 2)) & 3)) & 3;
 }
-__device__ __forceinline__ void load_chunk(const void* in, bool bf16, bool four, int64_t e0,
-                                           int64_t n, float (&v)[kQuads * 4]) {
-  if (four && n == kClipChunk) {
+struct Chunk {
+  int head;    // single elements before the tensor's first group
+  int64_t e0;  // the chunk's first element
+  int n;       // its elements; none where the head is all there is
+};
+__device__ __forceinline__ Chunk chunk_of(const ClipTable& tab, int i, int64_t k, bool bf16) {
+  Chunk c;
+  c.head = head_of(tab.in[i], bf16);
+  c.e0 = c.head + (k - tab.first[i]) * kClipChunk;
+  c.n = (int)max((int64_t)0, min((int64_t)kClipChunk, tab.numel[i] - c.e0));
+  return c;
+}
+__device__ __forceinline__ int place(int i) { return (i * kThreads + (int)threadIdx.x) * 4; }
+
+__device__ __forceinline__ void load_four(const void* in, bool bf16, int64_t e, float* v) {
+  if (bf16) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(in) + e);
+    v[0] = bf16_lo(r.x), v[1] = bf16_hi(r.x), v[2] = bf16_lo(r.y), v[3] = bf16_hi(r.y);
+  } else {
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(in) + e);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  }
+}
+__device__ __forceinline__ void store_four(void* out, bool bf16, int64_t e, const float* v) {
+  if (bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + e) =
+        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + e) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// This thread's groups of a chunk, zeros past its end.
+__device__ __forceinline__ void load_chunk(const void* in, bool bf16, const Chunk& c,
+                                           float (&v)[kQuads * 4]) {
+  if (c.n == kClipChunk) {
     if (bf16) {
-      uint2 r[kQuads];
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i)
-        r[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(in) + e0 +
-                                               place(true, i, 0));
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        v[i * 4] = bf16_lo(r[i].x), v[i * 4 + 1] = bf16_hi(r[i].x);
-        v[i * 4 + 2] = bf16_lo(r[i].y), v[i * 4 + 3] = bf16_hi(r[i].y);
-      }
+      for (int i = 0; i < kQuads; ++i) load_four(in, true, c.e0 + place(i), v + i * 4);
     } else {
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const float4 f =
-            *reinterpret_cast<const float4*>(static_cast<const float*>(in) + e0 + place(true, i, 0));
-        v[i * 4] = f.x, v[i * 4 + 1] = f.y, v[i * 4 + 2] = f.z, v[i * 4 + 3] = f.w;
-      }
+      for (int i = 0; i < kQuads; ++i) load_four(in, false, c.e0 + place(i), v + i * 4);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i)
+    for (int i = 0; i < kQuads; ++i) {
+      if (place(i) + 4 <= c.n) {
+        load_four(in, bf16, c.e0 + place(i), v + i * 4);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t e = place(four, i, k);
-        v[i * 4 + k] = e < n ? load_elem(in, bf16, e0 + e) : 0.f;
+        for (int k = 0; k < 4; ++k)
+          v[i * 4 + k] = place(i) + k < c.n ? load_elem(in, bf16, c.e0 + place(i) + k) : 0.f;
       }
+    }
+  }
+}
+
+// The same out again.  Where the output's groups of four begin `shift` elements
+// after the input's, a warp's run of 128 elements is passed on by that many
+// lanes' worth of values, so that all but its ends are still stored by fours.
+__device__ __forceinline__ void store_chunk(void* out, bool bf16, const Chunk& c, int shift,
+                                            const float (&v)[kQuads * 4]) {
+  const int lane = threadIdx.x & 31;
+  auto singly = [&](int i, int from, int to) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k >= from && k < to && place(i) + k < c.n)
+        store_elem(out, bf16, c.e0 + place(i) + k, v[i * 4 + k]);
+  };
+  if (shift == 0 && c.n == kClipChunk) {
+    if (bf16) {
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) store_four(out, true, c.e0 + place(i), v + i * 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) store_four(out, false, c.e0 + place(i), v + i * 4);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    if (shift == 0) {
+      if (place(i) + 4 <= c.n)
+        store_four(out, bf16, c.e0 + place(i), v + i * 4);
+      else
+        singly(i, 0, 4);
+    } else if (place(i) - lane * 4 + 128 <= c.n) {  // the same for the whole warp
+      float next[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) next[k] = __shfl_down_sync(0xffffffffu, v[i * 4 + k], 1);
+      const float* a = v + i * 4;
+      const float g[4] = {shift == 1 ? a[1] : shift == 2 ? a[2] : a[3],
+                          shift == 1 ? a[2] : shift == 2 ? a[3] : next[0],
+                          shift == 1 ? a[3] : shift == 2 ? next[0] : next[1],
+                          shift == 1 ? next[0] : shift == 2 ? next[1] : next[2]};
+      if (lane < 31)
+        store_four(out, bf16, c.e0 + place(i) + shift, g);
+      else
+        singly(i, shift, 4);
+      if (lane == 0) singly(i, 0, shift);
+    } else {
+      singly(i, 0, 4);
+    }
   }
 }
 
@@ -126,11 +199,17 @@ __global__ void __launch_bounds__(kThreads)
   Squares sq;
   for (int64_t k = k0; k < k1; ++k) {
     if (i + 1 < tab.n && tab.first[i + 1] <= k) ++i;  // every tensor has a chunk
-    const int64_t e0 = (k - tab.first[i]) * kClipChunk;
+    const bool bf16 = tab.flags[i] & kClipInBf16;
+    const Chunk c = chunk_of(tab, i, k, bf16);
     float v[kQuads * 4];
-    load_chunk(tab.in[i], tab.flags[i] & kClipInBf16, tab.flags[i] & kClipInFour, e0,
-               min((int64_t)kClipChunk, tab.numel[i] - e0), v);
+    load_chunk(tab.in[i], bf16, c, v);
     sq.add(v);
+    if (c.head > 0 && k == tab.first[i]) {
+      float h[kQuads * 4] = {};
+      if ((int)threadIdx.x < c.head && threadIdx.x < tab.numel[i])
+        h[0] = load_elem(tab.in[i], bf16, threadIdx.x);
+      sq.add(h);
+    }
   }
   // the warps' sums in fp32 (2^100 times all elements of a run could overflow
   // there, so above 2^100 in fp64 as well)
@@ -222,34 +301,16 @@ __global__ void __launch_bounds__(kThreads)
     const bool in_bf16 = fl & kClipInBf16, out_bf16 = fl & kClipOutBf16;
     // in place, by a coefficient of 1: already there
     if (coef == 1.f && tab.in[i] == tab.out[i] && in_bf16 == out_bf16) continue;
-    const bool four = (fl & kClipInFour) && (fl & kClipOutFour);
-    const int64_t e0 = (k - tab.first[i]) * kClipChunk;
-    const int64_t n = min((int64_t)kClipChunk, tab.numel[i] - e0);
+    void* out = tab.out[i];
+    const Chunk c = chunk_of(tab, i, k, in_bf16);
     float v[kQuads * 4];
-    load_chunk(tab.in[i], in_bf16, four, e0, n, v);
+    load_chunk(tab.in[i], in_bf16, c, v);
 #pragma unroll
     for (int q = 0; q < kQuads * 4; ++q) v[q] *= coef;
-    void* out = tab.out[i];
-    if (four && n == kClipChunk) {
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q) {
-        const int64_t e = e0 + place(true, q, 0);
-        if (out_bf16)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + e) = make_uint2(
-              pack_bf16(v[q * 4], v[q * 4 + 1]), pack_bf16(v[q * 4 + 2], v[q * 4 + 3]));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(out) + e) =
-              make_float4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t e = place(four, q, j);
-          if (e < n) store_elem(out, out_bf16, e0 + e, v[q * 4 + j]);
-        }
-    }
+    const int shift = (head_of(out, out_bf16) - c.head) & 3;
+    store_chunk(out, out_bf16, c, shift, v);
+    if ((int)threadIdx.x < c.head && k == tab.first[i] && threadIdx.x < tab.numel[i])
+      store_elem(out, out_bf16, threadIdx.x, coef * load_elem(tab.in[i], in_bf16, threadIdx.x));
   }
 }
 

@@ -223,7 +223,6 @@ cudaError_t launch_policy_stats(const PolicyLoss& p, cudaStream_t st);
 constexpr int kClipTensors = 512;
 constexpr int kClipChunk = 8192;
 constexpr unsigned char kClipInBf16 = 1, kClipOutBf16 = 2;
-constexpr unsigned char kClipInFour = 4, kClipOutFour = 8;  // aligned to four elements
 struct ClipTable {
   const void* in[kClipTensors];
   void* out[kClipTensors];

@@ -250,11 +250,7 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void* const* h_grads, const int32
       tab.numel[tab.n] = h_numels[i];
       tab.first[tab.n] = tab.chunks;
       tab.flags[tab.n] = (unsigned char)((h_grad_dts[i] == HLQ_BF16 ? kClipInBf16 : 0) |
-                                         (h_outs && h_out_dts[i] == HLQ_BF16 ? kClipOutBf16 : 0) |
-                                         (aligned_to(h_grads[i], 4 * elem_bytes(h_grad_dts[i]))
-                                              ? kClipInFour : 0) |
-                                         (h_outs && aligned_to(h_outs[i], 4 * elem_bytes(h_out_dts[i]))
-                                              ? kClipOutFour : 0));
+                                         (h_outs && h_out_dts[i] == HLQ_BF16 ? kClipOutBf16 : 0));
       tab.chunks += (h_numels[i] + kClipChunk - 1) / kClipChunk;
       ++tab.n;
     }

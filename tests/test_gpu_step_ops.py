@@ -791,3 +791,22 @@ def test_outputs_given_or_made_are_the_same_bits():
     assert len(made) == len(given) == 12
     for p, q in zip(made, given):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("o_off", [0, 1, 2, 3])
+@pytest.mark.parametrize("g_off", [0, 1, 2, 3])
+@pytest.mark.parametrize("g_dt,o_dt", [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)])
+def test_clip_grad_norm_offsets(g_off, o_off, g_dt, o_dt):
+    """Every pair of offsets from a group of four, lengths around the ends of
+    groups, warps' runs and chunks; nothing beside the outputs is written."""
+    r = rng(51, g_off, o_off)
+    grads, outs, bufs = [], [], []
+    for n in (1, 2, 3, 4, 5, 127, 128, 131, 1023, 8191, 8192, 8195, 20000):
+        grads.append(dev(r.normal(size=n + g_off), g_dt)[g_off:])
+        bufs.append(torch.full((n + o_off + 4,), 7.0, dtype=o_dt, device="cuda"))
+        outs.append(bufs[-1][o_off:o_off + n])
+    g64 = [f64(g) for g in grads]
+    check_clip(g64, outs, hlq.hlq_clip_grad_norm(grads, 1.0, outs=outs), 1.0)
+    for b, o in zip(bufs, outs):
+        assert bool((b[:o_off] == 7).all()) and bool((b[o_off + o.numel():] == 7).all())
+    check_clip(g64, grads, hlq.hlq_clip_grad_norm(grads, 1.0), 1.0)
