@@ -8,6 +8,7 @@ written to ``hadamard_precision_backprop_gb300/_build/``.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -77,8 +78,10 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    # the library alone where torch is not there to be bound to
+    with_ext = importlib.util.find_spec("torch") is not None
     if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
-                         for f in (LIB, EXT)):
+                         for f in ((LIB, EXT) if with_ext else (LIB,))):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -94,7 +97,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         objs = [ex.submit(compile_one, src) for src in SOURCES]
         linked = cf.Future()
-        ext = ex.submit(_build_ext, linked.result)
+        ext = ex.submit(_build_ext, linked.result) if with_ext else None
         try:
             tmp = LIB + f".tmp{os.getpid()}"
             _run([nvcc] + ARCH + ["-shared", "-o", tmp] + [o.result() for o in objs], "link")
@@ -103,7 +106,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             linked.set_exception(e)
             raise
         linked.set_result(None)
-        ext.result()
+        if ext is not None:
+            ext.result()
     return LIB
 
 
