@@ -335,10 +335,10 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
 }
 
 // What the first warp hands to its CTA: the gradient -coef p_v is
-// exp2(fma(z, c, bias)) k except at the action.  bias = -(c m) is rounded; the
-// exact rest of that product is in k.
+// exp2((z - m) c) k except at the action.  The difference comes first, as in the
+// sum: the product m c of a huge logit has no place for what z c adds to it.
 struct RowGrad {
-  float bias, k, at_action;
+  float neg_m, k, at_action;
   int64_t action;
 };
 
@@ -425,8 +425,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
     }
     const float coef = w * dlp * p.grad_scale * p.scale;
     if (tid == 0) {
-      const float bias = -(pair.m * c), fix = ex2(-fmaf(pair.m, c, bias));
-      grad = {bias, -coef * (fix / pair.s), -coef * expm1f(lp), a};
+      grad = {-pair.m, -coef / pair.s, -coef * expm1f(lp), a};
       if (slice == 0) {
         p.part[t] = w * pg;
         p.part[p.T + t] = w * kl;
@@ -440,12 +439,12 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
   if (!p.g) return;
   __syncthreads();
   const RowGrad gr = grad;
-  const F2 c2 = f2(c), bias = f2(gr.bias), k2 = f2(gr.k);
+  const F2 c2 = f2(c), neg = f2(gr.neg_m), k2 = f2(gr.k);
   auto gradient = [&](uint4 r, F2* v) {
     widen<kBf16>(r, v);
 #pragma unroll
     for (int k = 0; k < S::kVec / 2; ++k) {
-      const float2 x = split(fma2(v[k], c2, bias));
+      const float2 x = split((v[k] + neg) * c2);
       v[k] = f2(ex2(x.x), ex2(x.y)) * k2;
     }
   };
@@ -464,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
       }
     }
   }
-  if (sl.edge >= 0) store_elem(g, kBf16, sl.edge, ex2(fmaf(edge, c, gr.bias)) * gr.k);
+  if (sl.edge >= 0) store_elem(g, kBf16, sl.edge, ex2((edge + gr.neg_m) * c) * gr.k);
   // the action's element, by the thread that has just written it
   const int64_t e = gr.action - sl.e0;
   const bool mine = e >= 0 && e < (int64_t)sl.n * S::kVec ? (int)(e / S::kVec) % kThreads == tid
