@@ -10,6 +10,7 @@
 #include "hlq_device.cuh"
 #include "hlq_host.h"
 #include "hlq_kernels.h"
+#include "hlq_norm_range.cuh"
 #include "hlq_norm_ring.cuh"
 #include "hlq_rows.cuh"
 
@@ -40,25 +41,26 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
 // ---------------------------------------------------------------------------
 // Forward.  A team of kTeam threads holds a row in registers, so that the row
 // is read once and the variance is taken from the differences to the mean; all
-// of a thread's loads are in flight before the first is used.  kUnit = 8:
-// 16-byte accesses, 32 elements a thread at most.  kUnit = 1: single elements,
-// 16 a thread, for rows that are not made of aligned groups of eight and too
-// long for hlq_norm_elem.cu.
+// of a thread's loads are in flight before the first is used.  16-byte
+// accesses, 32 elements a thread at most.
 //
-// Bound by HBM: 16384 x 4096 bf16 with a residual (537 MB) takes 84 us, 0.95 of
-// the measured copy rate; 12608 x 768 without one 15 us, 0.76 (launch and last
-// wave).  The team is the smallest of 8, 32, 128 and 512 threads that holds the
-// row: more rows per SM are then under way, and short rows need no barrier.
+// Bound by HBM: 16384 x 4096 bf16 with a residual (537 MB) takes 83 us, 0.97 of
+// the measured copy rate; 12608 x 768 fp32 without one (77 MB) 14 us, 0.83, and
+// bf16 10 us, 0.58 (launch and last wave).  The team is the smallest of 8, 32,
+// 128 and 512 threads that holds the row: more rows per SM are then under way,
+// and short rows need no barrier.  64 registers a thread: two CTAs of 512 fit an
+// SM (8192 x 14336 bf16 120 us where one took 178), and eight of 128.
 // ---------------------------------------------------------------------------
-constexpr int kHeldVec = 32, kHeldElem = 16;
+constexpr int kHeld = 32;
+constexpr int team_threads(int team) { return team < 128 ? 128 : team; }
 
-template <bool kXBf16, int kTeam, int kUnit>
-__global__ void __launch_bounds__(kTeam < 128 ? 128 : kTeam) norm_fwd_kernel(NormFwd p) {
-  constexpr int kHeld = kUnit == 8 ? kHeldVec : kHeldElem;
-  constexpr int kNum = kHeld / kUnit, kThreads = kTeam < 128 ? 128 : kTeam;
+template <bool kXBf16, int kTeam>
+__global__ void __launch_bounds__(team_threads(kTeam), 1024 / team_threads(kTeam))
+    norm_fwd_kernel(NormFwd p) {
+  constexpr int kNum = kHeld / 8, kRows = team_threads(kTeam) / kTeam;
   __shared__ float red[2][32];
   const int tid = threadIdx.x % kTeam;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
+  const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kTeam;
   const bool live = t < p.T;
   const int C = (int)p.C;
   pdl_wait();
@@ -66,28 +68,20 @@ __global__ void __launch_bounds__(kTeam < 128 ? 128 : kTeam) norm_fwd_kernel(Nor
   float v[kHeld];
 #pragma unroll
   for (int i = 0; i < kNum; ++i) {
-    const int c = (i * kTeam + tid) * kUnit;
-    if constexpr (kUnit == 8) {
-      F8 f = {};
-      if (live && c < C) f = load8(p.x, kXBf16, t * p.ldx + c);
+    const int c = (i * kTeam + tid) * 8;
+    F8 f = {};
+    if (live && c < C) f = load8(p.x, kXBf16, t * p.ldx + c);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i * 8 + k] = f.v[k];
-    } else {
-      v[i] = live && c < C ? load_elem(p.x, kXBf16, t * p.ldx + c) : 0.f;
-    }
+    for (int k = 0; k < 8; ++k) v[i * 8 + k] = f.v[k];
   }
   if (p.residual) {
 #pragma unroll
     for (int i = 0; i < kNum; ++i) {
-      const int c = (i * kTeam + tid) * kUnit;
-      if constexpr (kUnit == 8) {
-        F8 f = {};
-        if (live && c < C) f = load8(p.residual, kXBf16, t * p.ldr + c);
+      const int c = (i * kTeam + tid) * 8;
+      F8 f = {};
+      if (live && c < C) f = load8(p.residual, kXBf16, t * p.ldr + c);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i * 8 + k] += f.v[k];
-      } else {
-        v[i] += live && c < C ? load_elem(p.residual, kXBf16, t * p.ldr + c) : 0.f;
-      }
+      for (int k = 0; k < 8; ++k) v[i * 8 + k] += f.v[k];
     }
   }
   float s = 0.f;
@@ -97,57 +91,57 @@ __global__ void __launch_bounds__(kTeam < 128 ? 128 : kTeam) norm_fwd_kernel(Nor
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kNum; ++i) {
-    if ((i * kTeam + tid) * kUnit < C) {
+    if ((i * kTeam + tid) * 8 < C) {
 #pragma unroll
-      for (int k = 0; k < kUnit; ++k) {
-        const float d = v[i * kUnit + k] - mean;
+      for (int k = 0; k < 8; ++k) {
+        const float d = v[i * 8 + k] - mean;
         s = fmaf(d, d, s);
       }
     }
   }
-  const float rstd = 1.f / sqrtf(team_sum<kTeam>(s, red[1]) / (float)C + p.eps);
+  s = team_sum<kTeam>(s, red[1]);
+  const float rstd = 1.f / sqrtf(s / (float)C + p.eps);
   if (!live) return;
+  // a row beyond the squares' range writes nothing here
+  const bool in_range = norm_in_range(s, norm_least(p.eps));
+  const int limit = in_range ? C : 0;
 #pragma unroll
   for (int i = 0; i < kNum; ++i) {
-    const int c = (i * kTeam + tid) * kUnit;
-    if (c >= C) continue;
-    if constexpr (kUnit == 8) {
-      F8 h, w, b, y;
+    const int c = (i * kTeam + tid) * 8;
+    if (c >= limit) continue;
+    F8 h, w, b, y;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h.v[k] = v[i * 8 + k], w.v[k] = 1.f, b.v[k] = 0.f;
-      if (p.weight) w = load8(p.weight, p.w_bf16, c);
-      if (p.bias) b = load8(p.bias, p.w_bf16, c);
-      if (p.h) store8(p.h, kXBf16, t * p.ldh + c, h);
+    for (int k = 0; k < 8; ++k) h.v[k] = v[i * 8 + k], w.v[k] = 1.f, b.v[k] = 0.f;
+    if (p.weight) w = load8(p.weight, p.w_bf16, c);
+    if (p.bias) b = load8(p.bias, p.w_bf16, c);
+    if (p.h) store8(p.h, kXBf16, t * p.ldh + c, h);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y.v[k] = fmaf((h.v[k] - mean) * rstd, w.v[k], b.v[k]);
-      store8(p.y, p.y_bf16, t * p.ldy + c, y);
-    } else {
-      const float w = p.weight ? load_elem(p.weight, p.w_bf16, c) : 1.f;
-      const float b = p.bias ? load_elem(p.bias, p.w_bf16, c) : 0.f;
-      if (p.h) store_elem(p.h, kXBf16, t * p.ldh + c, v[i]);
-      store_elem(p.y, p.y_bf16, t * p.ldy + c, fmaf((v[i] - mean) * rstd, w, b));
-    }
+    for (int k = 0; k < 8; ++k) y.v[k] = fmaf((h.v[k] - mean) * rstd, w.v[k], b.v[k]);
+    store8(p.y, p.y_bf16, t * p.ldy + c, y);
   }
-  if (tid == 0) {
-    if (p.mean) {
-      p.mean[t] = mean;
-      p.rstd[t] = rstd;
-    }
-    if (!isfinite(mean) || !isfinite(rstd)) raise_flag(p.status, HLQ_DEV_NONFINITE);
+  if (__builtin_expect(in_range, 1)) {
+    if (tid == 0) write_stats(p, t, mean, rstd);
+  } else {
+    norm_row_again<kTeam>(p, t, mean, s);
   }
 }
 
-// Rows too long for registers (above 16384 elements): three passes,
-// the later ones from L2.
+// Rows too long for registers (above 16384 elements), or for the shared memory
+// of hlq_norm_elem.cu: three passes, the later ones from L2 or L1.  Two CTAs an
+// SM; bound by latency and instructions, not by bytes: 2000 x 20001 bf16 103 us
+// (24 us of bytes), 2000 x 9001 54 (11), 5000 x 2001 fp32 with a residual 80 (24).
+// Holding rows of up to 16384 elements in the registers of one CTA an SM took
+// 60 and 125 us for the last two.
 constexpr int kLongThreads = 1024;
 
+template <bool kXBf16>
 __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(NormFwd p) {
   __shared__ float red[2][32];
   pdl_wait();
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
     auto h_at = [&](int64_t c) {
-      float v = load_elem(p.x, p.x_bf16, t * p.ldx + c);
-      if (p.residual) v += load_elem(p.residual, p.x_bf16, t * p.ldr + c);
+      float v = load_elem(p.x, kXBf16, t * p.ldx + c);
+      if (p.residual) v += load_elem(p.residual, kXBf16, t * p.ldr + c);
       return v;
     };
     float s = 0.f;
@@ -158,22 +152,20 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(NormFwd p) 
       const float d = h_at(c) - mean;
       s = fmaf(d, d, s);
     }
-    const float rstd =
-        1.f / sqrtf(team_sum<kLongThreads>(s, red[1]) / (float)p.C + p.eps);
+    s = team_sum<kLongThreads>(s, red[1]);
+    if (!norm_in_range(s, norm_least(p.eps))) {  // the same in every thread
+      norm_row_again<kLongThreads>(p, t, mean, s);
+      continue;
+    }
+    const float rstd = 1.f / sqrtf(s / (float)p.C + p.eps);
     for (int64_t c = threadIdx.x; c < p.C; c += kLongThreads) {
       const float h = h_at(c);
       const float w = p.weight ? load_elem(p.weight, p.w_bf16, c) : 1.f;
       const float b = p.bias ? load_elem(p.bias, p.w_bf16, c) : 0.f;
-      if (p.h) store_elem(p.h, p.x_bf16, t * p.ldh + c, h);
+      if (p.h) store_elem(p.h, kXBf16, t * p.ldh + c, h);
       store_elem(p.y, p.y_bf16, t * p.ldy + c, fmaf((h - mean) * rstd, w, b));
     }
-    if (threadIdx.x == 0) {
-      if (p.mean) {
-        p.mean[t] = mean;
-        p.rstd[t] = rstd;
-      }
-      if (!isfinite(mean) || !isfinite(rstd)) raise_flag(p.status, HLQ_DEV_NONFINITE);
-    }
+    if (threadIdx.x == 0) write_stats(p, t, mean, rstd);
     __syncthreads();  // red[0] is written again in the next row
   }
 }
@@ -257,18 +249,16 @@ __global__ void __launch_bounds__(256) norm_bwd_join_kernel(NormBwd p, int slabs
 template <bool kXBf16>
 cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
   auto go = [&](auto kernel, int team) {
-    const int threads = team < 128 ? 128 : team, rows = threads / team;
+    const int threads = team_threads(team), rows = threads / team;
     return launch_pdl(kernel, dim3((unsigned)((p.T + rows - 1) / rows)), dim3(threads), 0, st, p);
   };
   if (eight) {
-    if (p.C <= 8 * kHeldVec) return go(norm_fwd_kernel<kXBf16, 8, 8>, 8);
-    if (p.C <= 32 * kHeldVec) return go(norm_fwd_kernel<kXBf16, 32, 8>, 32);
-    if (p.C <= 128 * kHeldVec) return go(norm_fwd_kernel<kXBf16, 128, 8>, 128);
-    if (p.C <= 512 * kHeldVec) return go(norm_fwd_kernel<kXBf16, 512, 8>, 512);
-  } else {
-    if (p.C <= 1024 * kHeldElem) return go(norm_fwd_kernel<kXBf16, 1024, 1>, 1024);
+    if (p.C <= 8 * kHeld) return go(norm_fwd_kernel<kXBf16, 8>, 8);
+    if (p.C <= 32 * kHeld) return go(norm_fwd_kernel<kXBf16, 32>, 32);
+    if (p.C <= 128 * kHeld) return go(norm_fwd_kernel<kXBf16, 128>, 128);
+    if (p.C <= 512 * kHeld) return go(norm_fwd_kernel<kXBf16, 512>, 512);
   }
-  return launch_pdl(norm_fwd_long_kernel, dim3((unsigned)(p.T < 65535 ? p.T : 65535)),
+  return launch_pdl(norm_fwd_long_kernel<kXBf16>, dim3((unsigned)(p.T < 65535 ? p.T : 65535)),
                     dim3(kLongThreads), 0, st, p);
 }
 

@@ -556,7 +556,9 @@ size_t hlq_noalloc_scratch_bytes(void);
  * x, residual, h [T, C] have dtype x_dt; y [T, C] dtype y_dt; weight, bias
  * [C] dtype w_dt, either may be NULL (1, 0).  d_residual and d_h go together:
  * both NULL, or h (rounded to x_dt) is written to d_h.  d_mean, d_rstd fp32
- * [T]: both NULL, or both written.
+ * [T]: both NULL, or both written.  Rows whose sum or squares leave fp32's range,
+ * above or (with an eps below 2^-90) below, are scaled by a power of two for
+ * them: finite rows have the formulas' results whatever their size.
  */
 hlq_status hlq_layer_norm(const void *d_x, int64_t ldx, const void *d_residual, int64_t ldr,
                           int x_dt, const void *d_weight, const void *d_bias, int w_dt,

@@ -43,3 +43,79 @@ def test_policy_gradient_of_huge_logits(V, dt, scale):
     got = hlq.hlq_policy_loss(z, a, old, adv, w, ref_logp=ref, kl_coef=0.05, clip_high=0.28,
                               scale=scale)
     check_policy(got, z, a, old, adv, w, ref, scale, 0.2, 0.28, 0.05, 1.0)
+
+
+# ---------------------------------------------------------------------------
+# layer norm where squares leave fp32's range
+# ---------------------------------------------------------------------------
+def check_norm_range(got, h, w, b, y_dt, eps):
+    """check_norm with everything in units of the row's deviation, and half an
+    ulp of a subnormal rstd (2^-150) more."""
+    C = h.shape[1]
+    n = (C / 32 + 32) * U
+    y, mean, rstd = norm64(h, w, b, eps)
+    unit = 1 / rstd
+    e_mean = (n + 2 * U) * np.abs(h).mean(1)
+    d = np.abs(h - mean[:, None])
+    e_d = U * d + e_mean[:, None] + U * np.abs(h)
+    e_var = 2 * (d * e_d).mean(1) + np.square(e_d).mean(1) + (n + 4 * U) * np.square(d).mean(1)
+    var = np.square(d).mean(1) + eps
+    r_rstd = e_var / (2 * var) * (1 + e_var / var) + 4 * U
+    check(f64(got[1]) / unit, mean / unit, e_mean / unit, "mean")
+    check(f64(got[2]) * unit, 1.0, r_rstd + 2.0 ** -150 * unit, "rstd")
+    e_y = (np.abs(w) * rstd[:, None] * (e_d + d * (r_rstd[:, None] + 4 * U))
+           + 2 * U * np.abs(b) + 2 * OUT_U[y_dt] * np.abs(y))
+    check(got[0], y, e_y, "y")
+
+
+# teams of 8, 32, 128 and 512 threads; the element ring's three; 1024 threads; long rows
+WIDTHS = [64, 768, 4096, 16384, 77, 1001, 5663, 9001, 16387, 40000]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_layer_norm_range(C, dt):
+    """Finite rows of any size, beside ordinary ones: no flag, right results."""
+    r = rng(C, 62)
+    T = 9
+    w, b = dev(1 + 0.2 * r.normal(size=C)), dev(r.normal(size=C))
+    x = r.normal(size=(T, C))
+    for t, s in enumerate((1.0, 1e17, 3e19, 1e25, 1e37, 1e-10)):
+        x[t] *= s
+    x[6] = r.uniform(-3.3e38, 3.3e38, C)
+    x[7] = 2e38 * (1 + 0.05 * r.normal(size=C))        # the sum itself leaves the range
+    x = dev(x, dt)
+    check_norm_range(hlq.hlq_layer_norm(x, w, b, eps=EPS), f64(x), f64(w), f64(b), dt, EPS)
+    res = dev(f64(x) * 0.25, dt)
+    x[6:8] *= 0.5
+    got = hlq.hlq_layer_norm(x, w, b, eps=EPS, residual=res, out_dtype=F32)
+    check_norm_range(got, f64(x) + f64(res), f64(w), f64(b), F32, EPS)
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_layer_norm_range_without_eps(C, dt):
+    """Small rows, nothing added to the variance."""
+    r = rng(C, 63)
+    x = r.normal(size=(6, C))
+    for t, s in enumerate((1e-18, 1e-22, 1e-30, 1e-37, 1.0, 1e30)):
+        x[t] *= s
+    x = dev(x, dt)
+    check_norm_range(hlq.hlq_layer_norm(x, eps=0.0), f64(x), 1.0, 0.0, dt, 0.0)
+
+
+def test_layer_norm_flags_rows_without_statistics():
+    """What is still reported: infinity, NaN, no variance at all with eps 0."""
+    for C in (64, 1001, 20000):
+        for bad in (float("inf"), -float("inf"), float("nan")):
+            x = torch.randn(4, C, device="cuda") * 1e30
+            x[2, C // 2] = bad
+            y, _, rstd = hlq.hlq_layer_norm(x)
+            assert hlq.hlq_read_device_status(clear=True) == hlq.DEV_NONFINITE
+            assert bool(torch.isnan(y[2]).any()) and bool(torch.isfinite(y[[0, 1, 3]]).all())
+        y, _, rstd = hlq.hlq_layer_norm(torch.zeros(4, C, device="cuda"), eps=0.0)
+        assert bool(torch.isinf(rstd).all())
+        assert hlq.hlq_read_device_status(clear=True) == hlq.DEV_NONFINITE
+        y, mean, rstd = hlq.hlq_layer_norm(torch.zeros(4, C, device="cuda"), eps=1e-30)
+        assert not y.any() and not mean.any()
+        check(rstd, 1e15, 8 * U * 1e15, "rstd of a zero row")
