@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
     }
     sa = __shfl_sync(0xffffffffu, sum, 0) * inv;
     sx = __shfl_sync(0xffffffffu, sum, 16) * inv;
-    // g_x = rstd a - rstd sa - (x - mean) rstd^2 sx (+ g_residual)
-    const F2 shift = f2(-rstd * sa), slope = f2(-rstd * rstd * sx);
+    // g_x = rstd (a - sa - (x - mean) (rstd sx)) (+ g_residual): no rstd^2, which
+    // leaves fp32's range long before these do
+    const F2 shift = f2(-sa), slope = f2(-rstd * sx);
     auto write = [&](auto out_bf16, auto with_residual) {
       constexpr bool kOut = decltype(out_bf16)::value;
       constexpr int kSr = kOut ? 2 : 4;
@@ -157,14 +158,16 @@ __global__ void __launch_bounds__(ring_threads(kTeam, kUnits), kTeam == 32 ? 1 :
       for (int i = 0; i < kUnits; ++i) {
         if ((i * kTeam + tid) * 4 < C) {
           const Quad x = load4<kXBf16>(xs, i * kTeam * 4), g = load4<kGyBf16>(gs, i * kTeam * 4);
-          Quad o = {{shift, shift}};
-          if constexpr (decltype(with_residual)::value) {
-            o = load4<kOut>(rs, i * kTeam * 4);
-            o.v[0] = o.v[0] + shift, o.v[1] = o.v[1] + shift;
-          }
+          Quad o;
+          if constexpr (decltype(with_residual)::value) o = load4<kOut>(rs, i * kTeam * 4);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            o.v[k] = fma2(x.v[k] + neg_mean, slope, fma2(g.v[k] * w[i * 2 + k], rstd2, o.v[k]));
+          for (int k = 0; k < 2; ++k) {
+            const F2 d = fma2(x.v[k] + neg_mean, slope, fma2(g.v[k], w[i * 2 + k], shift));
+            if constexpr (decltype(with_residual)::value)
+              o.v[k] = fma2(d, rstd2, o.v[k]);
+            else
+              o.v[k] = d * rstd2;
+          }
           store4<kOut>(to, i * kTeam * 4, o);
         }
       }

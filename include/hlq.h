@@ -573,7 +573,8 @@ hlq_status hlq_layer_norm(const void *d_x, int64_t ldx, const void *d_residual, 
  *   g_weight = sum_t g_y xhat,  g_bias = sum_t g_y   (fp32 [C]).
  * g_y may have another type than x (hlq_linear_backward gives fp32 g_x);
  * g_residual, the gradient that reached h by the residual path, has the type
- * of g_x.  d_weight, d_gres, d_gweight, d_gbias may be NULL; the workspace
+ * of g_x; x - mean and the two sums have to be fp32 numbers (else
+ * HLQ_DEV_NONFINITE).  d_weight, d_gres, d_gweight, d_gbias may be NULL; the workspace
  * (hlq_layer_norm_backward_workspace_bytes) is needed for g_weight or g_bias.
  */
 hlq_status hlq_layer_norm_backward(const void *d_gy, int64_t ldgy, int gy_dt, const void *d_x,

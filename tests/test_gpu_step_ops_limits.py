@@ -119,3 +119,25 @@ def test_layer_norm_flags_rows_without_statistics():
         y, mean, rstd = hlq.hlq_layer_norm(torch.zeros(4, C, device="cuda"), eps=1e-30)
         assert not y.any() and not mean.any()
         check(rstd, 1e15, 8 * U * 1e15, "rstd of a zero row")
+
+
+# ---------------------------------------------------------------------------
+# its backward pass there
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [6, 700])
+@pytest.mark.parametrize("C", [264, 768, 1024, 2048, 4096, 14336, 77, 1001, 5663, 20001])
+@pytest.mark.parametrize("x_dt,gy_dt", [(F32, F32), (BF16, BF16)])
+def test_layer_norm_backward_range(T, C, x_dt, gy_dt):
+    """rstd whose square leaves fp32's range (deviations of 1e20 and more, or
+    of 1e-20 and less): xhat, and with it g_x, is an ordinary number."""
+    r = rng(T, C, 64)
+    s = np.resize([1.0, 3e19, 1e30, 1e37, 1e-25, 1e-37], T)
+    x = r.normal(size=(T, C)) * s[:, None]
+    x[3] = r.uniform(-1.6e38, 1.6e38, C)       # differences up to the end of the range
+    x = dev(x, x_dt)
+    w = dev(1 + 0.2 * r.normal(size=C))
+    _, mean, rstd = norm64(f64(x), 1.0, 0.0, 0.0)
+    mean, rstd = dev(mean), dev(rstd)
+    gy = dev(r.normal(size=(T, C)) * np.resize([1.0, 1.0, 1.0, 1e6, 1.0, 1e-3], T)[:, None], gy_dt)
+    got = hlq.hlq_layer_norm_backward(gy, x, mean, rstd, w, out_dtype=F32)
+    check_norm_bwd(got, gy, x, mean, rstd, w, None)
