@@ -262,7 +262,8 @@ __device__ __forceinline__ float clip_coef(const ClipSums& q, bool write) {
     norm = ldexpf(sqrtf(s), e);
   }
   float coef = q.max_norm / (norm + 1e-6f);
-  coef = coef > 1.f ? 1.f : coef;  // a NaN stays
+  // a NaN stays; without a limit an infinite norm clips nothing either
+  coef = coef > 1.f || (q.max_norm == INFINITY && norm == INFINITY) ? 1.f : coef;
   if (write && lane == 0) {
     q.norm_coef[0] = norm;
     q.norm_coef[1] = coef;

@@ -636,7 +636,7 @@ size_t hlq_policy_loss_workspace_bytes(int64_t T, int64_t V);
  * the coefficient alone.  d_norm_coef fp32 [2]: norm, coef.  The squares
  * neither overflow nor vanish: the norm is right to fp32 rounding wherever it
  * is a finite fp32 number.  An infinite norm gives coef 0, a NaN coef NaN, and
- * HLQ_DEV_NONFINITE; max_norm +inf clips nothing.
+ * HLQ_DEV_NONFINITE; max_norm +inf clips nothing (coef 1 unless the norm is NaN).
  * Workspace: hlq_clip_grad_norm_workspace_bytes(n).
  */
 hlq_status hlq_clip_grad_norm(int64_t n, const void *const *h_grads, const int32_t *h_grad_dts,

@@ -141,3 +141,28 @@ def test_layer_norm_backward_range(T, C, x_dt, gy_dt):
     gy = dev(r.normal(size=(T, C)) * np.resize([1.0, 1.0, 1.0, 1e6, 1.0, 1e-3], T)[:, None], gy_dt)
     got = hlq.hlq_layer_norm_backward(gy, x, mean, rstd, w, out_dtype=F32)
     check_norm_bwd(got, gy, x, mean, rstd, w, None)
+
+
+# ---------------------------------------------------------------------------
+# clipping that is switched off
+# ---------------------------------------------------------------------------
+def test_clip_grad_norm_without_a_limit_keeps_gradients():
+    """max_norm = inf clips nothing, an infinite gradient beside it or not."""
+    for bad in (float("inf"), -float("inf")):
+        g = [torch.randn(300, device="cuda"), torch.randn(9000, device="cuda")]
+        g[0][7] = bad
+        want = [t.clone() for t in g]
+        outs = [torch.empty_like(t) for t in g]
+        nc = hlq.hlq_clip_grad_norm(g, float("inf"), outs=outs)
+        assert nc.tolist() == [float("inf"), 1.0]
+        for o, t in zip(outs, want):
+            assert torch.equal(o, t)
+        assert hlq.hlq_clip_grad_norm(g, float("inf")).tolist() == [float("inf"), 1.0]
+        for o, t in zip(g, want):
+            assert torch.equal(o, t)
+        only = hlq.hlq_clip_grad_norm(g, float("inf"), norm_only=True)
+        assert only.tolist() == [float("inf"), 1.0]
+        assert hlq.hlq_read_device_status(clear=True) == hlq.DEV_NONFINITE
+    g = [torch.full((300,), float("nan"), device="cuda")]
+    assert bool(torch.isnan(hlq.hlq_clip_grad_norm(g, float("inf"))).all())
+    assert hlq.hlq_read_device_status(clear=True) == hlq.DEV_NONFINITE
