@@ -250,7 +250,10 @@ __device__ __forceinline__ void write_logprob(const TokenLogprobs& p, int64_t t,
   if (!isfinite(lse)) raise_flag(p.status, HLQ_DEV_NONFINITE);
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+// exp(scale d) = exp2(c d); no infinity, which a difference of 0 would make NaN.
+__device__ __forceinline__ float log2_scale(float scale) {
+  return fminf(scale * 1.4426950408889634f, FLT_MAX);
+}
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads) logprobs_cluster_kernel(TokenLogprobs p,
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_cluster_kernel(TokenLogprob
   __shared__ MaxSum warp_pair[kWarps], slots[kMostSlices];
   const int slice = blockIdx.x & ((1 << log_slices) - 1);
   const int64_t t = blockIdx.x >> log_slices;
-  const float c = p.scale * kLog2e;
+  const float c = log2_scale(p.scale);
   pdl_wait();
   pdl_trigger();
   if (log_slices) cluster_started_arrive();
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 3 : 2)
     logprobs_stream_kernel(TokenLogprobs p, int log_slices) {
   using S = Slice<kBf16>;
   __shared__ MaxSum warp_pair[2][kWarps];
-  const float c = p.scale * kLog2e;
+  const float c = log2_scale(p.scale);
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
   const int slice = blockIdx.x & ((1 << log_slices) - 1);
   const int tid = threadIdx.x;
   const int64_t t = blockIdx.x >> log_slices;
-  const float c = p.scale * kLog2e;
+  const float c = log2_scale(p.scale);
   pdl_wait();
   pdl_trigger();
   const float w = p.weight[t];

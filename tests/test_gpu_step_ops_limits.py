@@ -144,6 +144,30 @@ def test_layer_norm_backward_range(T, C, x_dt, gy_dt):
 
 
 # ---------------------------------------------------------------------------
+# softmax temperatures at the end of the range
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("V", [50, 40000, 300007])
+@pytest.mark.parametrize("T", [3, 700])
+def test_vocabulary_rows_with_a_huge_scale(T, V):
+    """scale * log2(e) above fp32's range: equal logits still share the
+    probability, and the largest takes it from smaller ones."""
+    if T > 3 and V > 100000:
+        T = 500
+    z = torch.zeros((T, V), device="cuda")
+    z[1, 7] = 1e-3
+    a = torch.full((T,), 7, device="cuda")
+    want = np.full(T, -math.log(V))
+    want[1] = 0.0
+    tol = e_logp(np.zeros(1), want, V)
+    logp, _ = hlq.hlq_token_logprobs(z, a, scale=3e38)
+    check(logp, want, tol, "logp")
+    ones = torch.ones(T, device="cuda")
+    stats, logp, g = hlq.hlq_policy_loss(z, a, logp, ones, ones / T, scale=3e38, grad_scale=1e-38)
+    check(logp, want, tol, "logp")
+    assert bool(torch.isfinite(stats).all()) and bool(torch.isfinite(g).all())
+
+
+# ---------------------------------------------------------------------------
 # clipping that is switched off
 # ---------------------------------------------------------------------------
 def test_clip_grad_norm_without_a_limit_keeps_gradients():
