@@ -56,7 +56,8 @@ __device__ __forceinline__ float ex2(float x) {
 
 // sum_i exp2(c z_i) as exp2(c m) s with m the maximum (-FLT_MAX and 0 before
 // the first term: then no difference below is -inf + inf).
-struct MaxSum {
+// Eight-byte aligned: clusters store it as one pair.
+struct alignas(8) MaxSum {
   float m, s;
 };
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
@@ -205,6 +206,7 @@ __device__ __forceinline__ MaxSum cluster_pair(MaxSum p, float c, int slice, int
   if (log_slices == 0) return p;
   __syncwarp();
   cluster_started_wait();
+  static_assert(sizeof(MaxSum) == 8 && alignof(MaxSum) == 8, "one aligned 8-byte store");
   if ((int)threadIdx.x < (1 << log_slices)) {
     const uint32_t at = cluster_map(saddr(slots + slice), threadIdx.x);
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(p.m), "f"(p.s)
