@@ -34,6 +34,14 @@ int code_of(at::ScalarType t) {
   return t == at::kFloat ? HLQ_F32 : t == at::kBFloat16 ? HLQ_BF16 : -1;
 }
 
+// Lets other threads run: allocations may wait for the driver, and launches for
+// a stream whose queue is full.  The arguments have been read before; their
+// tensors are held by the entry point's frame.
+struct WithoutGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~WithoutGil() { PyEval_RestoreThread(state); }
+};
+
 // What the arguments of one call have in common.
 struct Call {
   bool ok = true;
@@ -176,14 +184,21 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool stats = c.flag(a[6]);
   if (!c.ok || (w && b && w_dt != b_dt)) return not_implemented();
   const int64_t T = c.rows, C = c.cols;
-  at::Tensor y = c.empty({T, C}, y_type), h, mean, rstd;
-  if (a[4] != Py_None) h = c.empty({T, C}, x.dt == HLQ_BF16 ? at::kBFloat16 : at::kFloat);
-  if (stats) mean = c.empty({T}, at::kFloat), rstd = c.empty({T}, at::kFloat);
-  const hlq_status st = hlq_layer_norm(
-      x.p, x.ld, r.p, r.ld, x.dt, w, b, w_dt >= 0 ? w_dt : b_dt >= 0 ? b_dt : HLQ_F32, T, C,
-      (float)eps, y.mutable_data_ptr(), C, code_of(y_type), h.defined() ? h.mutable_data_ptr() : nullptr, C,
-      stats ? mean.mutable_data_ptr<float>() : nullptr,
-      stats ? rstd.mutable_data_ptr<float>() : nullptr, c.stream());
+  const bool residual = a[4] != Py_None;
+  at::Tensor y, h, mean, rstd;
+  hlq_status st;
+  {
+    WithoutGil g;
+    y = c.empty({T, C}, y_type);
+    if (residual) h = c.empty({T, C}, x.dt == HLQ_BF16 ? at::kBFloat16 : at::kFloat);
+    if (stats) mean = c.empty({T}, at::kFloat), rstd = c.empty({T}, at::kFloat);
+    st = hlq_layer_norm(
+        x.p, x.ld, r.p, r.ld, x.dt, w, b, w_dt >= 0 ? w_dt : b_dt >= 0 ? b_dt : HLQ_F32, T, C,
+        (float)eps, y.mutable_data_ptr(), C, code_of(y_type),
+        residual ? h.mutable_data_ptr() : nullptr, C,
+        stats ? mean.mutable_data_ptr<float>() : nullptr,
+        stats ? rstd.mutable_data_ptr<float>() : nullptr, c.stream());
+  }
   if (st != HLQ_OK) return not_implemented();
   return h.defined() ? tuple_of({y, mean, rstd, h}) : tuple_of({y, mean, rstd});
   END_HANDLE_TH_ERRORS
@@ -205,18 +220,23 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Call::Rows r = c.matrix(a[5], code_of(gx_type));
   const bool sums = c.flag(a[7]);
   if (!c.ok) return not_implemented();
-  at::Tensor gx = c.empty({T, C}, gx_type), gw, gb, ws;
-  size_t ws_bytes = 0;
-  if (sums) {
-    gw = c.empty({C}, at::kFloat), gb = c.empty({C}, at::kFloat);
-    ws_bytes = hlq_layer_norm_backward_workspace_bytes(T, C);
-    ws = c.workspace(ws_bytes);
+  at::Tensor gx, gw, gb, ws;
+  hlq_status st;
+  {
+    WithoutGil no_gil;
+    gx = c.empty({T, C}, gx_type);
+    size_t ws_bytes = 0;
+    if (sums) {
+      gw = c.empty({C}, at::kFloat), gb = c.empty({C}, at::kFloat);
+      ws_bytes = hlq_layer_norm_backward_workspace_bytes(T, C);
+      ws = c.workspace(ws_bytes);
+    }
+    st = hlq_layer_norm_backward(
+        g.p, g.ld, g.dt, x.p, x.ld, x.dt, mean, rstd, w, w_dt, r.p, r.ld, T, C,
+        gx.mutable_data_ptr(), C, code_of(gx_type), sums ? gw.mutable_data_ptr<float>() : nullptr,
+        sums ? gb.mutable_data_ptr<float>() : nullptr, sums ? ws.mutable_data_ptr() : nullptr,
+        ws_bytes, c.stream());
   }
-  const hlq_status st = hlq_layer_norm_backward(
-      g.p, g.ld, g.dt, x.p, x.ld, x.dt, mean, rstd, w, w_dt, r.p, r.ld, T, C,
-      gx.mutable_data_ptr(), C, code_of(gx_type), sums ? gw.mutable_data_ptr<float>() : nullptr,
-      sums ? gb.mutable_data_ptr<float>() : nullptr, sums ? ws.mutable_data_ptr() : nullptr, ws_bytes,
-      c.stream());
   if (st != HLQ_OK) return not_implemented();
   return tuple_of({gx, gw, gb});
   END_HANDLE_TH_ERRORS
@@ -233,10 +253,15 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t* targets = static_cast<const int64_t*>(c.vector(a[1], T, at::kLong));
   const double scale = c.number(a[2]);
   if (!c.ok) return not_implemented();
-  at::Tensor logp = c.empty({T}, at::kFloat), lse = c.empty({T}, at::kFloat);
-  const hlq_status st = hlq_token_logprobs(x.p, x.ld, x.dt, targets, T, c.cols, (float)scale,
-                                           logp.mutable_data_ptr<float>(),
-                                           lse.mutable_data_ptr<float>(), c.stream());
+  at::Tensor logp, lse;
+  hlq_status st;
+  {
+    WithoutGil g;
+    logp = c.empty({T}, at::kFloat), lse = c.empty({T}, at::kFloat);
+    st = hlq_token_logprobs(x.p, x.ld, x.dt, targets, T, c.cols, (float)scale,
+                            logp.mutable_data_ptr<float>(), lse.mutable_data_ptr<float>(),
+                            c.stream());
+  }
   return st == HLQ_OK ? tuple_of({logp, lse}) : not_implemented();
   END_HANDLE_TH_ERRORS
 }
@@ -257,20 +282,26 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   for (int i = 0; i < 5; ++i) v[i] = c.number(a[6 + i]);
   const bool grad = c.flag(a[11]);
   if (!c.ok) return not_implemented();
-  const size_t ws_bytes = hlq_policy_loss_workspace_bytes(T, V);
-  at::Tensor stats = c.empty({4}, at::kFloat), logp = c.empty({T}, at::kFloat), g;
-  if (grad) g = c.empty({T, V}, x.dt == HLQ_BF16 ? at::kBFloat16 : at::kFloat);
-  at::Tensor ws = c.workspace(ws_bytes);
-  const hlq_status st = hlq_policy_loss(
-      x.p, x.ld, x.dt, actions, old, ref, adv, w, T, V, (float)v[3], (float)v[0], (float)v[1],
-      (float)v[2], (float)v[4], stats.mutable_data_ptr<float>(), logp.mutable_data_ptr<float>(),
-      grad ? g.mutable_data_ptr() : nullptr, V, ws.mutable_data_ptr(), ws_bytes, c.stream());
+  at::Tensor stats, logp, g, ws;
+  hlq_status st;
+  {
+    WithoutGil no_gil;
+    const size_t ws_bytes = hlq_policy_loss_workspace_bytes(T, V);
+    stats = c.empty({4}, at::kFloat), logp = c.empty({T}, at::kFloat);
+    if (grad) g = c.empty({T, V}, x.dt == HLQ_BF16 ? at::kBFloat16 : at::kFloat);
+    ws = c.workspace(ws_bytes);
+    st = hlq_policy_loss(
+        x.p, x.ld, x.dt, actions, old, ref, adv, w, T, V, (float)v[3], (float)v[0], (float)v[1],
+        (float)v[2], (float)v[4], stats.mutable_data_ptr<float>(), logp.mutable_data_ptr<float>(),
+        grad ? g.mutable_data_ptr() : nullptr, V, ws.mutable_data_ptr(), ws_bytes, c.stream());
+  }
   if (st != HLQ_OK) return not_implemented();
   return tuple_of({stats, logp, g});
   END_HANDLE_TH_ERRORS
 }
 
 struct Table {
+  std::vector<at::Tensor> held;  // whatever becomes of the caller's list
   std::vector<const void*> p;
   std::vector<int32_t> dt;
   std::vector<int64_t> n;
@@ -278,7 +309,7 @@ struct Table {
   // has none yet).
   bool fill(Call& c, PyObject* seq) {
     const Py_ssize_t len = PySequence_Fast_GET_SIZE(seq);
-    p.resize(len), dt.resize(len), n.resize(len);
+    held.reserve(len), p.resize(len), dt.resize(len), n.resize(len);
     PyObject** items = PySequence_Fast_ITEMS(seq);
     for (Py_ssize_t i = 0; i < len; ++i) {
       const at::Tensor* t = c.tensor(items[i]);
@@ -288,6 +319,7 @@ struct Table {
       if (dt[i] < 0) return false;
       p[i] = t->const_data_ptr();
       n[i] = t->numel();
+      held.push_back(*t);
     }
     return c.ok;
   }
@@ -309,13 +341,18 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return not_implemented();
   const Table& out = a[2] == Py_None ? g : o;
   const int64_t count = (int64_t)g.p.size();
-  const size_t ws_bytes = hlq_clip_grad_norm_workspace_bytes(count);
-  at::Tensor norm_coef = c.empty({2}, at::kFloat), ws = c.workspace(ws_bytes);
-  const hlq_status st = hlq_clip_grad_norm(
-      count, g.p.data(), g.dt.data(),
-      norm_only ? nullptr : reinterpret_cast<void* const*>(const_cast<void**>(out.p.data())),
-      norm_only ? nullptr : out.dt.data(), g.n.data(), (float)max_norm,
-      norm_coef.mutable_data_ptr<float>(), ws.mutable_data_ptr(), ws_bytes, c.stream());
+  at::Tensor norm_coef, ws;
+  hlq_status st;
+  {
+    WithoutGil no_gil;
+    const size_t ws_bytes = hlq_clip_grad_norm_workspace_bytes(count);
+    norm_coef = c.empty({2}, at::kFloat), ws = c.workspace(ws_bytes);
+    st = hlq_clip_grad_norm(
+        count, g.p.data(), g.dt.data(),
+        norm_only ? nullptr : reinterpret_cast<void* const*>(const_cast<void**>(out.p.data())),
+        norm_only ? nullptr : out.dt.data(), g.n.data(), (float)max_norm,
+        norm_coef.mutable_data_ptr<float>(), ws.mutable_data_ptr(), ws_bytes, c.stream());
+  }
   return st == HLQ_OK ? THPVariable_Wrap(norm_coef) : not_implemented();
   END_HANDLE_TH_ERRORS
 }

@@ -190,3 +190,44 @@ def test_clip_grad_norm_without_a_limit_keeps_gradients():
     g = [torch.full((300,), float("nan"), device="cuda")]
     assert bool(torch.isnan(hlq.hlq_clip_grad_norm(g, float("inf"))).all())
     assert hlq.hlq_read_device_status(clear=True) == hlq.DEV_NONFINITE
+
+
+# ---------------------------------------------------------------------------
+# other threads
+# ---------------------------------------------------------------------------
+def test_other_threads_run_while_a_call_waits():
+    """A call that waits (its stream's queue of launches is full behind work
+    that takes half a second) leaves the interpreter to other threads."""
+    import threading
+    import time
+
+    from tests.test_gpu_step_ops import _calls
+
+    for call in _calls():
+        call()
+        torch.cuda.synchronize()
+        longest_gap, stop = [0.0], threading.Event()
+
+        def tick():
+            last = time.perf_counter()
+            while not stop.is_set():
+                time.sleep(0.002)
+                now = time.perf_counter()
+                longest_gap[0] = max(longest_gap[0], now - last)
+                last = now
+
+        thread = threading.Thread(target=tick)
+        thread.start()
+        try:
+            torch.cuda._sleep(1_000_000_000)
+            longest_call, until = 0.0, time.perf_counter() + 0.7
+            while time.perf_counter() < until and longest_call < 0.2:
+                t0 = time.perf_counter()
+                call()
+                longest_call = max(longest_call, time.perf_counter() - t0)
+        finally:
+            stop.set()
+            thread.join()
+        torch.cuda.synchronize()
+        assert longest_call > 0.2, "no call waited: nothing was tested"
+        assert longest_gap[0] < 0.1
