@@ -620,13 +620,15 @@ def _load_ext():
     NotImplemented, and the entry point goes on in Python."""
     global _ext
     _torch()
-    path = os.path.join(os.path.dirname(LIB_PATH), "_hlq_torch.so")
+    from .build import ext_path
+    path = ext_path()
     if not os.path.exists(path):
-        raise RuntimeError(f"the binding's extension is not built ({path} missing); run "
-                           "`python -m hadamard_precision_backprop_gb300.build`")
+        raise RuntimeError(f"the binding's extension is not built for this torch ({path} missing); "
+                           "run `python -m hadamard_precision_backprop_gb300.build`")
     spec = importlib.util.spec_from_file_location("_hlq_torch", path)
-    _ext = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_ext)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _ext = module
     return _ext
 
 

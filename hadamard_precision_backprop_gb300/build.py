@@ -20,7 +20,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libhlq.so")
-EXT = os.path.join(OUT_DIR, "_hlq_torch.so")
 
 SOURCES = ["hlq_api.cu", "hlq_quant.cu", "hlq_gemm_simple.cu", "hlq_gemm_tc.cu",
            "hlq_step_api.cu", "hlq_norm.cu", "hlq_norm_ring_bf16.cu",
@@ -42,6 +41,21 @@ def _flags():
                    "--expt-relaxed-constexpr"]
 
 
+def ext_path() -> str:
+    """The binding's extension for this interpreter and this torch: it reads
+    torch's C++ objects, so each torch has a module of its own."""
+    import sysconfig
+    import torch
+    return os.path.join(OUT_DIR, f"_hlq_torch-{torch.__version__}"
+                                 f"{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
+
+
+def is_current(with_ext: bool) -> bool:
+    """Whether the built files are there and no older than their sources."""
+    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
+               for f in ([LIB, ext_path()] if with_ext else [LIB]))
+
+
 def _build_ext(link_after) -> None:
     """Compile the extension module; it is linked against libhlq.so (found
     beside it) once `link_after` has returned."""
@@ -50,7 +64,8 @@ def _build_ext(link_after) -> None:
     top = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     cxx = shutil.which("g++") or "g++"
-    obj, tmp = os.path.join(OUT_DIR, "hlq_torch.o"), EXT + f".tmp{os.getpid()}"
+    ext = ext_path()
+    obj, tmp = os.path.join(OUT_DIR, "hlq_torch.o"), ext + f".tmp{os.getpid()}"
     inc = [os.path.join(top, "include"), sysconfig.get_paths()["include"],
            os.path.join(cuda, "include"), INCLUDE]
     _run([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall",
@@ -62,7 +77,7 @@ def _build_ext(link_after) -> None:
     _run([cxx, "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lhlq", "-Wl,-rpath,$ORIGIN",
           "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
           "-ltorch", "-lc10_cuda", "-lc10"], "link of the extension")
-    os.replace(tmp, EXT)
+    os.replace(tmp, ext)
 
 
 def _run(cmd, what):
@@ -80,8 +95,7 @@ def _deps_mtime() -> float:
 def build(force: bool = False, verbose: bool = False) -> str:
     # the library alone where torch is not there to be bound to
     with_ext = importlib.util.find_spec("torch") is not None
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
-                         for f in ((LIB, EXT) if with_ext else (LIB,))):
+    if not force and is_current(with_ext):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
