@@ -8,7 +8,6 @@ written to ``hadamard_precision_backprop_gb300/_build/``.
 from __future__ import annotations
 
 import concurrent.futures as cf
-import importlib.util
 import os
 import shutil
 import subprocess
@@ -48,6 +47,16 @@ def ext_path() -> str:
     import torch
     return os.path.join(OUT_DIR, f"_hlq_torch-{torch.__version__}"
                                  f"{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
+
+
+def can_bind() -> bool:
+    """Whether there is a torch to bind to: one with CUDA.  The library alone is
+    built where there is none."""
+    try:
+        import torch
+    except ImportError:
+        return False
+    return torch.version.cuda is not None
 
 
 def is_current(with_ext: bool) -> bool:
@@ -93,8 +102,7 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    # the library alone where torch is not there to be bound to
-    with_ext = importlib.util.find_spec("torch") is not None
+    with_ext = can_bind()
     if not force and is_current(with_ext):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
