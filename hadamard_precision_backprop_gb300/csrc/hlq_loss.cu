@@ -14,7 +14,8 @@
 // maximum and the sum of exp(z - maximum).  These pairs are joined over the
 // warp, the slice's warps and the slices, always in the same order: a token's
 // log-probability has the same bits whatever the number of rows and in both
-// operators, so that the ratio of an unchanged policy is exactly 1.
+// operators, so that the ratio of an unchanged policy is exactly 1.  (The groups
+// are aligned in memory: a row at another offset from 16 bytes has others.)
 //   policy loss: a cluster of CTAs, one for a slice, joins the slices through
 //     distributed shared memory; the gradient is computed from the registers,
 //     so that the row is read once;

@@ -593,8 +593,11 @@ size_t hlq_layer_norm_backward_workspace_bytes(int64_t T, int64_t C);
  * row of nothing else has no distribution (NaN).  logp, lse fp32 [T]; d_lse
  * may be NULL.  Serves for the old and the reference log-probabilities of
  * hlq_policy_loss: a row gives the same bits in both, whatever the number of
- * rows, so that the ratio of an unchanged policy is exactly 1.  T <= (2^31 - 1)
- * / 8.
+ * rows, so that the ratio of an unchanged policy is exactly 1.  That holds for
+ * rows at the same offset from a 16-byte boundary (always so where the row
+ * stride is a multiple of 16 bytes): a row moved to another offset, as in
+ * shuffled batches of an odd V, is summed in another order and may differ in
+ * its last bits.  T <= (2^31 - 1) / 8.
  */
 hlq_status hlq_token_logprobs(const void *d_logits, int64_t ld, int dt,
                               const int64_t *d_targets, int64_t T, int64_t V, float scale,

@@ -231,3 +231,30 @@ def test_other_threads_run_while_a_call_waits():
         torch.cuda.synchronize()
         assert longest_call > 0.2, "no call waited: nothing was tested"
         assert longest_gap[0] < 0.1
+
+
+# ---------------------------------------------------------------------------
+# log-probabilities of rows that lie elsewhere
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("V", [1001, 32003, 151671])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_logprobs_of_moved_rows(V, dt):
+    """The same bits wherever a row lies at the same offset from a 16-byte
+    boundary; at another offset its terms are added in another order, and both
+    results stay within the bound of a log-probability."""
+    T, step = 7, 16 // torch.empty(0, dtype=dt).element_size()
+    z, a = logits_case(T, V, dt, rng(V, 67))
+    at = torch.from_numpy(a).cuda()
+    want = logsoftmax64(f64(z))[np.arange(T), a]
+    here = hlq.hlq_token_logprobs(z, at)
+    for off in range(step + 1):
+        for t in range(T):
+            buf = torch.zeros(off + V, dtype=dt, device="cuda")
+            row = buf[off:].view(1, V)
+            row.copy_(z[t:t + 1])
+            got = hlq.hlq_token_logprobs(row, at[t:t + 1])
+            if (t * V - off) % step == 0:
+                assert torch.equal(got[0], here[0][t:t + 1])
+                assert torch.equal(got[1], here[1][t:t + 1])
+            check(got[0], want[t:t + 1], e_logp(f64(z), want[t:t + 1], V), "logp")
+    check(here[0], want, e_logp(f64(z), want, V), "logp")
