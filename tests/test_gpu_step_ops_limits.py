@@ -234,6 +234,54 @@ def test_other_threads_run_while_a_call_waits():
 
 
 # ---------------------------------------------------------------------------
+# kernels that few sizes reach
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,C", [(3, 8193), (5, 9001), (2, 12345), (2, 16383), (400, 9001)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_layer_norm_of_odd_rows_above_8192(T, C, dt):
+    """One element at a time, 1024 threads a row."""
+    r = rng(T, C, 65)
+    x, res = (dev(r.normal(size=(T, C)) + 0.5, dt) for _ in range(2))
+    w, b = dev(r.normal(size=C), dt), dev(r.normal(size=C), dt)
+    check_norm(hlq.hlq_layer_norm(x, w, b, out_dtype=F32), f64(x), f64(w), f64(b), F32)
+    got = hlq.hlq_layer_norm(x, w, b, residual=res)
+    h = f64(x) + f64(res)
+    check(got[3], h, 2 * OUT_U[dt] * np.abs(h), "h")
+    check_norm(got, h, f64(w), f64(b), dt)
+
+
+@pytest.mark.parametrize("C", [1687, 1689, 2001, 2047, 2049, 7191, 7193, 8190, 8191])
+def test_layer_norm_of_odd_fp32_rows_with_a_residual(C):
+    """Around the widths whose two slots of a row do not fit a CTA's share of
+    shared memory; rows enough to fill every stage again."""
+    T = 5000 if C < 4000 else 1500
+    r = rng(C, 66)
+    x, res = dev(r.normal(size=(T, C))), dev(r.normal(size=(T, C)))
+    w, b = dev(r.normal(size=C)), dev(r.normal(size=C))
+    got = hlq.hlq_layer_norm(x, w, b, residual=res)
+    h = f64(x) + f64(res)
+    check(got[3], h, 2 * U * np.abs(h), "h")
+    check_norm(got, h, f64(w), f64(b), F32)
+
+
+@pytest.mark.parametrize("V,ld,off,ldg,offg", [(131073, 131073, 0, 131080, 3),
+                                               (151671, 151680, 8, 151671, 1),
+                                               (300007, 300010, 2, 300008, 0)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_policy_loss_of_long_rows_at_other_offsets(V, ld, off, ldg, offg, dt):
+    """Rows that are read twice, the gradient's at another offset from 16 bytes."""
+    T = 5
+    z, a, old, adv, w, ref = policy_inputs(T, V, dt, rng(V, ldg), 1.0, 0.2, 0.2, ld, off)
+    buf = torch.full((offg + T * ldg + 8,), 7.0, dtype=dt, device="cuda")
+    out = buf[offg:].as_strided((T, V), (ldg, 1))
+    got = hlq.hlq_policy_loss(z, a, old, adv, w, ref_logp=ref, kl_coef=0.1, out=out)
+    check_policy(got, z, a, old, adv, w, ref, 1.0, 0.2, 0.2, 0.1, 1.0)
+    touched = torch.zeros_like(buf, dtype=torch.bool)
+    touched[offg:].as_strided((T, V), (ldg, 1)).fill_(True)
+    assert bool((buf[~touched] == 7).all())
+
+
+# ---------------------------------------------------------------------------
 # log-probabilities of rows that lie elsewhere
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("V", [1001, 32003, 151671])
