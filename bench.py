@@ -9,10 +9,12 @@ One step = the whole hot path on one batch of synthetic input:
 Default workload: the largest single-GPU layer of the five, a Llama-3-8B
 MLP down_proj: T = 8 x 2048 = 16384 tokens, Cin = 14336, Cout = 4096, bf16
 inputs, per-token g_y quantizer.  The other layers (ViT-B qkv and fc2,
-ResNet-50 3x3 im2col, the small single linear) are timed the same way in the
-line's `per_workload` block.
+ResNet-50 3x3 im2col, the small single linear) are timed the same way; the
+line's `per_workload` block has their times.
 
-Prints one JSON line (rank 0).  `value` is microseconds per layer step
+Prints one JSON line (rank 0) of a few kilobytes, and before it on stderr another
+(`{"details": ...}`) with the tables that would make it tens of kilobytes: times
+by row and by kernel, the optional paths, every layer's own, each e2e step.  `value` is microseconds per layer step
 (lower is better), device-timed with CUDA events on the launching stream,
 inputs resident in HBM, L2 flushed (256 MiB write) before every timed step.
 `e2e` is the same step through libhlq's host-buffer entry
@@ -881,6 +883,19 @@ def run_profile(args, wl):
     return 0
 
 
+def split_line(full):
+    """The benchmark's line, short enough for a reader of a bounded tail of the
+    output, and the tables taken out of it."""
+    details = {k: full[k] for k in ("rows", "kernels", "variants", "per_workload")}
+    details["e2e_steps_us"] = full["e2e"]["steps_us"]
+    line = {k: v for k, v in full.items() if k not in details}
+    line["e2e"] = {k: v for k, v in full["e2e"].items() if k != "steps_us"}
+    line["per_workload"] = {
+        name: {"us_per_layer": w["us_per_layer"], "e2e_us": w["e2e"]["value"]}
+        for name, w in full["per_workload"].items()}
+    return line, details
+
+
 def run_ours(args, wl, rank, world, local_rank):
     import torch
     import hadamard_precision_backprop_gb300 as hlq
@@ -940,6 +955,8 @@ def run_ours(args, wl, rank, world, local_rank):
     if world == 1 and not args.no_cpu_baseline:
         line["cpu_baseline"] = cpu_baseline(wl, inp, min(args.cpu_sample_tokens, wl.T),
                                             args.cpu_sample_w_rows)
+    line, details = split_line(line)
+    print(json.dumps({"details": details}), file=sys.stderr, flush=True)
     print(json.dumps(line), flush=True)
     return 0
 
