@@ -13,9 +13,10 @@
 // 236 M fp32 gradients in 192 tensors, written as bf16 (2.36 GB in the two
 // passes): 350 us, 1.01 of the measured copy rate; the bytes read once and
 // written once would be 212 us.  A few small tensors take the time of two
-// launches (9 us with the host's work for 24 of them).  54 M gradients whose
-// outputs begin anywhere in a flat buffer: 118 us where 49 M aligned ones take
-// 80 (the ends of each warp's run are stored one by one).
+// launches (9 us with the host's work for 24 of them).  54 M gradients written
+// as bf16: 76 us, 89 where the outputs begin anywhere in a flat buffer (the ends
+// of each warp's run are stored one by one).  Without the bound on registers the
+// second pass takes 104 of them and two CTAs run on an SM: 81 and 111 us.
 #include "hlq_device.cuh"
 #include "hlq_kernels.h"
 #include "hlq_rows.cuh"
@@ -24,6 +25,7 @@ namespace hlq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;  // 64 registers a thread
 constexpr int kQuads = kClipChunk / kThreads / 4;  // groups of four a thread
 
 // The tensor that holds chunk `k` of the concatenation: the last one whose
@@ -189,7 +191,7 @@ struct Squares {
 
 // A CTA's partial result is the norm of its elements: an fp32 number wherever
 // the whole norm is one.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     clip_norm_kernel(const __grid_constant__ ClipTable tab, float* part) {
   __shared__ double red[kThreads / 32];
   pdl_wait();
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(32) clip_coef_kernel(ClipSums q) {
 // The runs and their chunks in the opposite order of the norm's pass: what
 // that pass read last is still in L2.  Each CTA adds the partial sums itself
 // (a few thousand at most, from L2), which costs less than a launch between.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     clip_scale_kernel(const __grid_constant__ ClipTable tab, const __grid_constant__ ClipSums q,
                       int first) {
   __shared__ float shared_coef;
@@ -317,12 +319,12 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-// Four CTAs of 256 threads an SM: 128 KB of loads in flight.  Neither pass
+// kCtasPerSm CTAs an SM: 128 KB of loads in flight.  Neither pass
 // lets the next kernel start before its own CTAs are done: CTAs of the second
 // that came early would crowd on the SMs that the first left first, five on
 // some and three on others (376 us instead of 356 for 236 M fp32 gradients).
 int clip_grid(int64_t chunks, int sms) {
-  const int64_t most = (int64_t)sms * 4;
+  const int64_t most = (int64_t)sms * kCtasPerSm;
   return (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);
 }
 
