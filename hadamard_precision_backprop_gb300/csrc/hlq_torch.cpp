@@ -11,6 +11,7 @@
 
 #include <array>
 #include <cstdint>
+#include <memory>
 #include <vector>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -301,7 +302,6 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 struct Table {
-  std::vector<at::Tensor> held;  // whatever becomes of the caller's list
   std::vector<const void*> p;
   std::vector<int32_t> dt;
   std::vector<int64_t> n;
@@ -309,7 +309,7 @@ struct Table {
   // has none yet).
   bool fill(Call& c, PyObject* seq) {
     const Py_ssize_t len = PySequence_Fast_GET_SIZE(seq);
-    held.reserve(len), p.resize(len), dt.resize(len), n.resize(len);
+    p.resize(len), dt.resize(len), n.resize(len);
     PyObject** items = PySequence_Fast_ITEMS(seq);
     for (Py_ssize_t i = 0; i < len; ++i) {
       const at::Tensor* t = c.tensor(items[i]);
@@ -319,7 +319,6 @@ struct Table {
       if (dt[i] < 0) return false;
       p[i] = t->const_data_ptr();
       n[i] = t->numel();
-      held.push_back(*t);
     }
     return c.ok;
   }
@@ -336,8 +335,12 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool norm_only = c.flag(a[3]);
   if (!c.ok) return not_implemented();
   Table g, o;
+  // whatever becomes of the caller's list of outputs (the gradients' is the
+  // entry point's own)
+  const std::unique_ptr<PyObject, void (*)(PyObject*)> outs(
+      is_seq(a[2]) ? PySequence_Tuple(a[2]) : nullptr, [](PyObject* t) { Py_XDECREF(t); });
   if (!g.fill(c, a[0]) || c.device != c10::cuda::current_device()) return not_implemented();
-  if (a[2] != Py_None && (norm_only || !is_seq(a[2]) || !o.fill(c, a[2]) || o.n != g.n))
+  if (a[2] != Py_None && (norm_only || !outs || !o.fill(c, outs.get()) || o.n != g.n))
     return not_implemented();
   const Table& out = a[2] == Py_None ? g : o;
   const int64_t count = (int64_t)g.p.size();
