@@ -1,4 +1,4 @@
-"""A policy trained by reward, every step of its backward pass in libhlq.
+"""A policy trained by reward: its backward pass in libhlq, down to the embedding.
 
 The policy reads one token and answers with another: embedding, layer norm,
 vocabulary projection.  It is rewarded for the answer `table[token]`.  Each

@@ -26,12 +26,15 @@
 // Bound by HBM, and next to that by latency: a CTA's loads, its sums, the
 // cluster's barrier, the row's few scalars (in one warp, 7 waiting) and its
 // stores follow one another, and only the other CTAs of the SM fill the gaps.
-// Policy loss 4096 x 128256 bf16 with a quarter of the rows masked (1.84 GB) 316
+// Policy loss 4096 x 128256 bf16 with a quarter of the rows masked (1.84 GB) 315
 // us, 0.87 of the measured copy rate; 1000 x 50021 (175 MB) 41 us, 0.64 (ramp
-// and tail, some 17 instructions an element).  Log-probabilities 2048 x 32003
-// fp32 (262 MB) 40 us, 0.98; 4096 x 128256 bf16 240 us, 0.66 (half as many bytes
-// a register in flight).  With one pass over 64 loaded elements for the maximum
-// and one for the sum, and clusters everywhere, these took 416, 54, 99 and 254.
+// and tail, some 17 instructions an element).  Every row counted: 2048 x 128256
+// fp32 (2.1 GB) 370 us, 0.85; 2048 x 151936 bf16, read twice (1.24 GB without
+// that), 246 us, 0.76; 4096 x 128256 bf16 without a gradient (1.05 GB) 255 us,
+// 0.62.  Log-probabilities 2048 x 32003 fp32 (262 MB) 40 us, 0.99; 4096 x 128256
+// bf16 239 us, 0.66 (half as many bytes a register in flight).  With one pass
+// over 64 loaded elements for the maximum and one for the sum, and clusters
+// everywhere, the two masked cases took 416 and 54, these 99 and 254.
 #include <cfloat>
 #include <type_traits>
 
@@ -360,9 +363,10 @@ __device__ __forceinline__ uint4 narrow(const F2* v) {
 }
 
 // kHeld: the slice is kept in registers between the two passes, else (rows of
-// more than 8 x 16384 elements) read again.  Five CTAs an SM for bf16: 320 us at
-// 4096 x 128256 where four took 325.  kAligned: g's rows begin at the same offset from a 16-byte boundary
-// as the logits'; else g is written element by element.
+// more than 8 x 16384 elements) read again.  Five CTAs an SM for bf16, in 48 registers
+// with 16 to 32 bytes spilled: 320 us at 4096 x 128256 where four took 325.
+// kAligned: g's rows begin at the same offset from a 16-byte boundary as the
+// logits'; else g is written element by element.
 template <bool kBf16, bool kHeld, bool kAligned>
 __global__ void __launch_bounds__(kThreads, kBf16 ? 5 : 2)
     policy_rows_kernel(const __grid_constant__ PolicyLoss p, int log_slices) {

@@ -266,9 +266,10 @@ cudaError_t launch_fwd(const NormFwd& p, bool eight, cudaStream_t st) {
 
 // The ring's shape.  Teams: a warp up to 1024 columns (16 or 24 of them in the
 // SM's one CTA: 8 that kept the first pass's values took 28.6 us at 12608 x 768
-// where 16 take 24), CTAs of 128 threads, four an SM, up to 2048 (one of 256
-// threads, two an SM: 64 us at 16384 x 2048 where these take 60), of 256, two an
-// SM, up to 4096 (four teams of 128 threads in one CTA left one stage each: 138
+// where 16 take 24; above 768 columns a thread spills some 80 bytes, but teams of
+// 128 threads take 36 us at 16384 x 1024 where a warp takes 34), CTAs of 128
+// threads, four an SM, up to 2048 (one of 256 threads, two an SM: 64 us at 16384
+// x 2048 where these take 60), of 256, two an SM, up to 4096 (four teams of 128 threads in one CTA left one stage each: 138
 // us at 16384 x 4096 where these take 105), of 512 above.  As many stages as
 // fit, at most 8 and no more than a team has rows.  False: the rows are not for
 // the ring, or do not fit.

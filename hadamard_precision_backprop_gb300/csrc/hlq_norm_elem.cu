@@ -12,11 +12,11 @@
 //
 // Bound by instructions and by the barriers of its reductions, not by bytes
 // (two- and four-byte accesses, some 20 instructions an element): forward 4689 x
-// 5663 bf16 49 us (16 us of bytes), backward with fp32 g_y 77 us (32); with the
+// 5663 bf16 47 us (16 us of bytes), backward with fp32 g_y 77 us (32); with the
 // rows loaded into registers by single elements instead, without a ring, these
 // took 73 and 104 us.  A warp's lanes copy one matrix's row each: one lane for
 // all of them took longer than the rest of a short row's work (20000 x 77
-// backward 43 -> 22 us).
+// backward 43 -> 22 us; its bytes take 2).
 #include "hlq_device.cuh"
 #include "hlq_norm_range.cuh"
 #include "hlq_norm_ring.cuh"

@@ -29,7 +29,9 @@ cudaError_t launch_norm_bwd_ring_bf16(const NormBwd& p, const RingPlan& r, cudaS
 cudaError_t launch_norm_bwd_ring_f32(const NormBwd& p, const RingPlan& r, cudaStream_t st);
 
 
-// Rows of any length and alignment (up to 8192 elements): hlq_norm_elem.cu.
+// Rows of any length and alignment, up to 8192 elements, whose stages fit a CTA's
+// share of shared memory (forward, fp32 with a residual: not those of 1689 to
+// 2048 and above 7192): hlq_norm_elem.cu.
 bool norm_fwd_elem_plan(const NormFwd& p, int sms, RingPlan* out);
 cudaError_t launch_norm_fwd_elem(const NormFwd& p, const RingPlan& r, cudaStream_t st);
 bool norm_bwd_elem_plan(const NormBwd& p, int sms, RingPlan* out);

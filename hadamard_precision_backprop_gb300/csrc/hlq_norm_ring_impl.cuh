@@ -10,9 +10,10 @@
 // norm_bwd_join_kernel adds; few rows go to one cluster, whose CTAs add their
 // sums through distributed shared memory.
 //
-// Bound by HBM for long rows: 16384 x 14336 bf16 (1.41 GB) in 206 us, 1.02 of
+// Bound by HBM for long rows: 16384 x 14336 bf16 (1.41 GB) in 213 us, 0.99 of
 // the measured copy rate, 16384 x 4096 with fp32 g_y and a residual (671 MB) in
-// 104 us, 0.97.  At 12608 x 768 (97 MB, 25 us) each further row costs what its
+// 105 us, 0.95.  16384 x 1024 with fp32 g_y (134 MB) takes 34 us, 0.60.  At 12608
+// x 768 (97 MB, 25 us) each further row costs what its
 // bytes do (1.15 us for 1000), and the rest is about 10 us of launch, first
 // copies, the sums' joining and its launch.
 //
@@ -266,6 +267,9 @@ cudaError_t launch_ring(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
 
 template <bool kXBf16, bool kGyBf16>
 cudaError_t pick_ring(const NormBwd& p, const RingPlan& r, cudaStream_t st) {
+// Few steps of kUnits for the compiler's sake.  Those of the longest rows pay for
+// themselves: with 8 in place of 6 and 7, 8192 x 12288 takes 143 us instead of 99
+// and 8192 x 14336 156 instead of 110.
 #define HLQ_RING(TEAM, UNITS) \
   if (r.team == TEAM && r.units <= UNITS) return launch_ring<kXBf16, kGyBf16, TEAM, UNITS>(p, r, st)
   HLQ_RING(32, 2);
