@@ -104,6 +104,27 @@ def test_layer_norm_range_without_eps(C, dt):
     check_norm_range(hlq.hlq_layer_norm(x, eps=0.0), f64(x), 1.0, 0.0, dt, 0.0)
 
 
+@pytest.mark.parametrize("C", [64, 768, 4096, 16384, 77, 1001, 5663, 9001, 40000])
+def test_layer_norm_range_in_place(C):
+    """Rows taken once more are read again: what is written over them comes last."""
+    r = rng(C, 68)
+    x, res = r.normal(size=(6, C)), r.normal(size=(6, C))
+    x[1:5] *= 3e30
+    res[2:4] *= 1e30
+    x, res = dev(x), dev(res)
+    want = hlq.hlq_layer_norm(x, residual=res)
+    a, c = x.clone(), res.clone()
+    got = hlq.hlq_layer_norm(a, residual=c, out=a, h=c)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    a, c = x.clone(), res.clone()
+    got = hlq.hlq_layer_norm(a, residual=c, out=c, h=a)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    a = x.clone()
+    assert torch.equal(hlq.hlq_layer_norm(a, out=a)[0], hlq.hlq_layer_norm(x)[0])
+
+
 def test_layer_norm_flags_rows_without_statistics():
     """What is still reported: infinity, NaN, no variance at all with eps 0."""
     for C in (64, 1001, 20000):
