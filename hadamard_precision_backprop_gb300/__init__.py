@@ -18,6 +18,9 @@ Entry points (same names as the C ABI):
   hlq_token_logprobs(logits, targets)         -> logp, lse fp32 [T]
   hlq_policy_loss(logits, actions, ...)       -> stats, logp, gradient of logits
   hlq_clip_grad_norm(grads, max_norm, ...)    -> norm and coefficient, grads clipped
+  hlq_attention(q, k, v, ...)                 -> out, lse
+  hlq_attention_backward(g_out, q, k, v, ...) -> g_q, g_k, g_v (or g_qkv)
+  hlq_dropout(x, p, seed, ...)                -> y (+ residual)
   hlq_debug_gx_parts / hlq_debug_gw_parts     -> intermediates for checks
   hlq_workspace_bytes, hlq_read_device_status, hlq_status_string
 """
@@ -64,6 +67,8 @@ EXPORTS = [
     "hlq_layer_norm", "hlq_layer_norm_backward", "hlq_layer_norm_backward_workspace_bytes",
     "hlq_token_logprobs", "hlq_policy_loss", "hlq_policy_loss_workspace_bytes",
     "hlq_clip_grad_norm", "hlq_clip_grad_norm_workspace_bytes",
+    "hlq_attention", "hlq_attention_backward", "hlq_attention_backward_workspace_bytes",
+    "hlq_dropout",
 ]
 
 _lock = threading.Lock()
@@ -156,6 +161,13 @@ def lib() -> ctypes.CDLL:
             "hlq_policy_loss_workspace_bytes": (sz, [i64, i64]),
             "hlq_clip_grad_norm": (i32, [i64, P, P, P, P, P, f32, P, P, sz, P]),
             "hlq_clip_grad_norm_workspace_bytes": (sz, [i64]),
+            "hlq_attention": (i32, [P, P, P, i32, i64, i64, i64, i64, i64, P, P, i64, i32, f32, P,
+                                    P, P]),
+            "hlq_attention_backward": (i32, [P, i32, P, P, P, P, i32, P, i64, i64, i64, i64, i64,
+                                             P, P, i64, i32, f32, P, P, P, i32, P, sz, P]),
+            "hlq_attention_backward_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+            "hlq_dropout": (i32, [P, i64, i32, P, i64, i64, i64, ctypes.c_double, u64, P, P, i64,
+                                  i32, P]),
             "hlq_status_string": (ctypes.c_char_p, [i32]),
             "hlq_version": (i32, []),
         }
@@ -963,6 +975,189 @@ def hlq_clip_grad_norm(grads, max_norm: float, outs=None, norm_only: bool = Fals
                                   max_norm, pn, pws, n_ws, _raw_stream(index))
     _check(rc, "hlq_clip_grad_norm")
     return norm_coef
+
+
+class _Heads(ctypes.Structure):
+    """hlq_heads: a [tokens, heads, D] tensor, its strides in elements."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+def _heads(t, what, index=None, shape=None, dtype=None):
+    """hlq_heads of a CUDA tensor [tokens, heads, D] whose heads are contiguous
+    (any strides of tokens and heads), on device `index`, of `shape` and of
+    `dtype` where these are given."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if shape is None:
+        if t.dim() != 3:
+            raise ValueError(f"{what} must have shape [tokens, heads, D], not {tuple(t.shape)}")
+    elif t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    token, head, step = t.stride()
+    if step != 1 and t.shape[2] > 1:
+        raise ValueError(f"the heads of {what} must be contiguous")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the inputs on cuda:{index}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be of dtype {dtype}, not {t.dtype}")
+    return ctypes.byref(_Heads(t.data_ptr(), token, head))
+
+
+def _sequences(seqs, seqs_k, batch, index):
+    """Addresses of the offsets and the number of sequences."""
+    if seqs is None:
+        if seqs_k is not None:
+            raise ValueError("seqs_k needs seqs")
+        return None, None, int(batch)
+    i32 = _torch().int32
+    n = seqs.shape[0] if seqs.dim() == 1 else 0
+    if n < 2:
+        raise ValueError(f"seqs must have shape (batch + 1,), not {tuple(seqs.shape)}")
+    if batch not in (1, n - 1):
+        raise ValueError(f"seqs holds {n - 1} sequences, batch is {batch}")
+    return (_vector(seqs, "seqs", n, index, i32), _vector(seqs_k, "seqs_k", n, index, i32), n - 1)
+
+
+def _qkv(q, k, v):
+    """What the attention calls have in common: the arguments, the device."""
+    pq = _heads(q, "q")
+    _code(q.dtype)
+    index = q.get_device()
+    _need_current(index)
+    pk = _heads(k, "k", index, dtype=q.dtype)
+    if k.shape[2] != q.shape[2]:
+        raise ValueError(f"q has heads of {q.shape[2]}, k of {k.shape[2]}")
+    if k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+        raise ValueError(f"the {k.shape[1]} heads of k must divide the {q.shape[1]} of q")
+    return pq, pk, _heads(v, "v", index, k.shape, q.dtype), index
+
+
+def hlq_attention(q, k, v, seqs=None, seqs_k=None, batch: int = 1, causal: bool = False,
+                  scale=None, out=None, lse=None, stream=None):
+    """Softmax attention over packed sequences: q [Tq, Hq, D], k and v [Tk, Hk,
+    D] (bf16 or fp32, any token and head strides: parts of a qkv layer's output
+    as they are; Hk divides Hq).  Returns (out [Tq, Hq, D], lse fp32 [Tq, Hq]).
+    `batch` sequences of one length, or `seqs` int32 [batch + 1]: offsets of the
+    sequences' queries (and keys; seqs_k where those have their own).  causal:
+    the last query sees all keys, each before it one fewer.  scale: 1/sqrt(D) by
+    default.  Rows of no sequence and queries that see nothing: 0, lse -inf."""
+    if stream is not None:
+        return _on_stream(hlq_attention, locals())
+    if out is None and lse is None:
+        got = (_ext or _load_ext()).attention(q, k, v, seqs, seqs_k, batch, causal, scale)
+        if got is not NotImplemented:
+            return got
+    torch = _torch()
+    pq, pk, pv, index = _qkv(q, k, v)
+    Tq, Hq, D = q.shape
+    ps, psk, batch = _sequences(seqs, seqs_k, batch, index)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    po = _heads(out, "out", index, q.shape, q.dtype)
+    if lse is None:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+    _need_buf(lse, (Tq, Hq), torch.float32, index, "lse")
+    rc = lib().hlq_attention(pq, pk, pv, _code(q.dtype), Tq, k.shape[0], Hq, k.shape[1], D, ps, psk,
+                             batch, 1 if causal else 0, D ** -0.5 if scale is None else scale, po,
+                             lse.data_ptr(), _raw_stream(index))
+    _check(rc, "hlq_attention")
+    return out, lse
+
+
+def hlq_attention_backward(g_out, q, k, v, out, lse, seqs=None, seqs_k=None, batch: int = 1,
+                           causal: bool = False, scale=None, out_dtype=None, packed: bool = False,
+                           g_q=None, g_k=None, g_v=None, ws=None, stream=None):
+    """Backward pass of hlq_attention, from its inputs and outputs and g_out [Tq,
+    Hq, D] (bf16 or fp32, whatever q's type): (g_q, g_k, g_v) of `out_dtype`
+    (default: q's), or with packed=True (as many keys as queries) one tensor
+    [T, Hq + 2 Hk, D] that holds them one after the other within each token: the
+    gradient of a qkv layer's output."""
+    if stream is not None:
+        return _on_stream(hlq_attention_backward, locals())
+    if g_q is None and g_k is None and g_v is None and ws is None:
+        got = (_ext or _load_ext()).attention_backward(g_out, q, k, v, out, lse, seqs, seqs_k,
+                                                       batch, causal, scale, out_dtype, packed)
+        if got is not NotImplemented:
+            return got
+    torch = _torch()
+    pq, pk, pv, index = _qkv(q, k, v)
+    Tq, Hq, D = q.shape
+    Tk, Hk, _ = k.shape
+    pg = _heads(g_out, "g_out", index, q.shape)
+    po = _heads(out, "out", index, q.shape, q.dtype)
+    _need_buf(lse, (Tq, Hq), torch.float32, index, "lse")
+    ps, psk, batch = _sequences(seqs, seqs_k, batch, index)
+    g_all = None
+    if packed:
+        if g_q is not None or g_k is not None or g_v is not None:
+            raise ValueError("packed allocates g_q, g_k and g_v itself")
+        if Tq != Tk:
+            raise ValueError(f"packed gradients need as many keys as queries, not {Tk} and {Tq}")
+        g_all = torch.empty((Tq, Hq + 2 * Hk, D), dtype=out_dtype or q.dtype, device=q.device)
+        g_q, g_k, g_v = g_all.split([Hq, Hk, Hk], 1)
+    given = [t for t in (g_q, g_k, g_v) if t is not None]
+    g_dtype = out_dtype or (given[0].dtype if given else q.dtype)
+    if g_q is None:
+        g_q = torch.empty(q.shape, dtype=g_dtype, device=q.device)
+    if g_k is None:
+        g_k = torch.empty(k.shape, dtype=g_dtype, device=q.device)
+    if g_v is None:
+        g_v = torch.empty(k.shape, dtype=g_dtype, device=q.device)
+    pgq = _heads(g_q, "g_q", index, q.shape, g_dtype)
+    pgk = _heads(g_k, "g_k", index, k.shape, g_dtype)
+    pgv = _heads(g_v, "g_v", index, k.shape, g_dtype)
+    dt, gout_dt = _code(q.dtype), _code(g_out.dtype)
+    n_ws = 0
+    if ws is None:
+        n_ws = lib().hlq_attention_backward_workspace_bytes(Tq, Hq, D, dt, gout_dt)
+    ws, pws, n_ws = _workspace(ws, n_ws, index, q.device)
+    rc = lib().hlq_attention_backward(
+        pg, gout_dt, pq, pk, pv, po, dt, lse.data_ptr(), Tq, Tk, Hq, Hk, D, ps, psk, batch,
+        1 if causal else 0, D ** -0.5 if scale is None else scale, pgq, pgk, pgv, _code(g_dtype),
+        pws, n_ws, _raw_stream(index))
+    _check(rc, "hlq_attention_backward")
+    return g_all if packed else (g_q, g_k, g_v)
+
+
+def hlq_dropout(x, p: float, seed, residual=None, out_dtype=None, out=None, stream=None):
+    """Dropout of x [T, C] with the residual added: each element kept with
+    probability 1 - p (in steps of 2^-16) and divided by it.  The mask is drawn
+    from `seed` (an int, or an int64 CUDA tensor of one element, which a
+    captured graph reads anew at each replay) and the element's place alone, and
+    is never stored: the backward pass is the same call on the gradient of y,
+    without the residual.  y has `out_dtype` (default: residual's, or x's) and
+    so has the residual."""
+    if stream is not None:
+        return _on_stream(hlq_dropout, locals())
+    if out is None:
+        got = (_ext or _load_ext()).dropout(x, p, seed, residual, out_dtype)
+        if got is not NotImplemented:
+            return got
+    torch = _torch()
+    ldx, x_dt, px = _rows(x, "x")
+    shape, index, device = x.shape, x.get_device(), x.device
+    _need_current(index)
+    T, C = shape
+    if out is None:
+        dtype = out_dtype or (x.dtype if residual is None else residual.dtype)
+        out = torch.empty(shape, dtype=dtype, device=device)
+        ldy, y_dt, py = _new_rows(out, C)
+    else:
+        ldy, y_dt, py = _rows(out, "out", index, shape, out_dtype)
+    ldr, pr = 0, None
+    if residual is not None:
+        ldr, _, pr = _rows(residual, "residual", index, shape, out.dtype)
+    pd = None
+    if isinstance(seed, torch.Tensor):
+        if not seed.is_cuda or seed.get_device() != index or seed.numel() != 1 \
+                or seed.dtype != torch.int64:
+            raise ValueError(f"seed must be an int or an int64 tensor of one element on cuda:{index}")
+        seed, pd = 0, seed.data_ptr()
+    rc = lib().hlq_dropout(px, ldx, x_dt, pr, ldr, T, C, p, int(seed) & (2 ** 64 - 1), pd, py, ldy,
+                           y_dt, _raw_stream(index))
+    _check(rc, "hlq_dropout")
+    return out
 
 
 def hlq_debug_gx_parts(g_y, w, gran_gy=PER_TOKEN, gran_w=PER_TENSOR, rnd=SR,

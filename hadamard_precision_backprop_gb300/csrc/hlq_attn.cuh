@@ -1,0 +1,116 @@
+// hlq_attn.cuh -- what the attention kernels share: one call's arguments, the
+// sequences and their tiles.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "hlq_device.cuh"
+#include "hlq_kernels.h"
+
+namespace hlq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Queries and keys of one sequence, and the tile of it that a CTA has.
+struct AttnTile {
+  int q0, nq, k0, nk;  // first row and number of rows
+  int row0;            // the tile's first row within the sequence
+};
+
+// Rows [lo, hi) of sequence b; `bad` where the offsets are not in order (the
+// rows are then cut to those that exist).
+__device__ __forceinline__ int2 seq_rows(const int32_t* seqs, int b, int T, bool& bad) {
+  const int a = (int)ld_dep_u32(reinterpret_cast<const unsigned int*>(seqs) + b);
+  const int e = (int)ld_dep_u32(reinterpret_cast<const unsigned int*>(seqs) + b + 1);
+  const int lo = min(max(a, 0), T), hi = min(max(e, lo), T);
+  bad |= a != lo || e != hi;
+  return make_int2(lo, hi);
+}
+
+// Tile t of `rows` queries (keys with kKeys) among the tiles of all sequences,
+// the last tile of a sequence first (with a causal mask it is the longest, if
+// they go by queries).  Returns -1, or where the tiles are used up the number
+// of tiles past the last one.  A whole warp calls it.
+//
+// With sequences of one length the tiles of all sequences that have the same
+// rank follow each other; else each lane looks at a sequence of its own and
+// the warp adds up their tiles, 32 sequences at a time.
+template <bool kKeys>
+__device__ __forceinline__ int find_tile(const Attn& p, int rows, int t, AttnTile& o) {
+  const int T = kKeys ? p.Tk : p.Tq;
+  if (!p.seqs_q) {
+    const int Lq = p.Tq / p.batch, Lk = p.Tk / p.batch, L = kKeys ? Lk : Lq;
+    const int per = (L + rows - 1) / rows;
+    const int rank = t / p.batch, b = t - rank * p.batch;
+    if (rank >= per) return t - per * p.batch;
+    o = {b * Lq, Lq, b * Lk, Lk, (kKeys ? rank : per - 1 - rank) * rows};
+    return -1;
+  }
+  const int32_t* seqs = kKeys ? p.seqs_k : p.seqs_q;
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0, sum;
+    if (b < p.batch) {
+      const int2 r = seq_rows(seqs, b, T, bad);
+      n = (r.y - r.x + rows - 1) / rows;
+    }
+    sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, sum > t);
+    if (past) {
+      const int first = __ffs(past) - 1;
+      const int tile = __shfl_sync(0xffffffffu, sum - 1 - t, first);  // from the last one back
+      const int tiles = __shfl_sync(0xffffffffu, n, first);
+      const int2 q = seq_rows(p.seqs_q, b0 + first, p.Tq, bad);
+      const int2 k = seq_rows(p.seqs_k, b0 + first, p.Tk, bad);
+      if (bad) raise_flag(p.status, HLQ_DEV_BADCODE);
+      o = {q.x, q.y - q.x, k.x, k.y - k.x, (kKeys ? tiles - 1 - tile : tile) * rows};
+      return -1;
+    }
+    t -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (bad) raise_flag(p.status, HLQ_DEV_BADCODE);
+  return t;
+}
+
+// Tiles of all sequences, at most, and one or more for the rows outside them:
+// sequence i has at most n_i / rows + (rows - 1) / rows tiles, and the n rows
+// outside take at most n / rows + 1.
+inline int64_t most_tiles(const Attn& p, bool keys, int rows) {
+  const int64_t T = keys ? p.Tk : p.Tq;
+  if (!p.seqs_q) return (T / p.batch + rows - 1) / rows * p.batch;
+  return (T + rows - 1) / rows + p.batch + 1;
+}
+
+// Rows of chunk `chunk` of the rows that belong to no sequence (before the
+// first and behind the last): calls f(row) for this thread's.
+template <bool kKeys, typename F>
+__device__ __forceinline__ void outside_rows(const Attn& p, int rows, int chunk, int thread,
+                                             int threads, F&& f) {
+  if (!p.seqs_q) return;
+  const int32_t* seqs = kKeys ? p.seqs_k : p.seqs_q;
+  const int T = kKeys ? p.Tk : p.Tq;
+  bool bad = false;
+  const int front = seq_rows(seqs, 0, T, bad).x;
+  const int back = max(front, seq_rows(seqs, p.batch - 1, T, bad).y);
+  const int64_t n = (int64_t)front + (T - back);
+  const int64_t first = (int64_t)chunk * rows;
+  for (int64_t i = first + thread; i < first + rows && i < n; i += threads)
+    f((int)(i < front ? i : back + (i - front)));
+}
+
+// Keys that query i of a tile's sequence sees: the last query sees all of
+// them, each one before it one fewer.
+__device__ __forceinline__ int keys_of(const Attn& p, const AttnTile& t, int i) {
+  return p.causal ? max(0, min(t.nk, i + 1 + t.nk - t.nq)) : t.nk;
+}
+
+}  // namespace hlq

@@ -1,0 +1,420 @@
+// hlq_attn_simt.cu -- attention and its backward pass on CUDA cores, in fp32:
+// every type, head size up to 256, stride and alignment.  The tensor-core
+// kernels take bf16 heads that TMA can read; the rest comes here.
+//
+//   s_ij = scale q_i . k_j          lse_i = log sum_j exp(s_ij)
+//   out_i = sum_j exp(s_ij - lse_i) v_j
+//   p_ij = exp(s_ij - lse_i)        delta_i = g_out_i . out_i
+//   ds_ij = p_ij (g_out_i . v_j - delta_i)
+//   g_q_i = scale sum_j ds_ij k_j,  g_k_j = scale sum_i ds_ij q_i,
+//   g_v_j = sum_i p_ij g_out_i
+//
+// One CTA of 16 x 16 threads has a tile of rows (queries; keys in the keys'
+// pass) in shared memory and goes over tiles of the other side.  Thread
+// (ty, tx) has rows ty RM .., columns tx, tx + 16, .. of a tile of scores and
+// columns 4 tx + 64 c .. of a row of results, so that a row belongs to half a
+// warp: maxima and sums are shuffles, and the probabilities go through shared
+// memory without a barrier.  The backward pass goes over the keys' tiles (g_k,
+// g_v) and over the queries' tiles (g_q) in kernels of their own: two products
+// more than one pass with atomics would take, and equal calls give equal bits.
+#include <cmath>
+
+#include "hlq_attn.cuh"
+#include "hlq_rows.cuh"
+
+namespace hlq {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Tile sizes by head size: rows of the CTA's own side and of the other side.
+// 79 KB (D <= 128) and 108 KB (D <= 256) of shared memory forward, 120 and
+// 142 KB backward.
+template <int DP>
+struct Cfg {
+  static constexpr int kLd = DP + 4;  // floats: rows 4 banks apart
+  static constexpr int kBM = DP <= 128 ? 64 : 32;
+  static constexpr int kBN = DP <= 64 ? 64 : 32;
+  static constexpr int kRM = kBM / 16, kRN = kBN / 16, kRD = DP / 16;
+  static constexpr int kLdP = kBN + 4;
+  static constexpr size_t kFwd = 4 * (size_t)(kBM * kLd + 2 * kBN * kLd + kBM * kLdP);
+  static constexpr size_t kBwd = 4 * (size_t)(2 * kBM * kLd + 2 * kBN * kLd + 2 * kBM * kLdP);
+};
+
+// Rows row0 .. row0 + n of head h as fp32, zeros in the rest of the tile.
+template <int DP>
+__device__ __forceinline__ void load_tile(float* dst, const Heads& x, bool bf16, int64_t row0,
+                                          int n, int rows, int h, int D) {
+  const int64_t at = row0 * x.token + (int64_t)h * x.head;
+  for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
+    const int r = i / DP, d = i % DP;
+    dst[r * Cfg<DP>::kLd + d] =
+        r < n && d < D ? load_elem(x.p, bf16, at + r * x.token + d) : 0.f;
+  }
+}
+
+// acc[i][j] = A[row i] . B[row j], rows as in the note at the top.
+template <int DP, int RM, int RN>
+__device__ __forceinline__ void rows_by_rows(const float* a, const float* b, int ty, int tx,
+                                             float (&acc)[RM][RN]) {
+  constexpr int kLd = Cfg<DP>::kLd;
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 u[RM], w[RN];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+      u[i] = *reinterpret_cast<const float4*>(a + (ty * RM + i) * kLd + d);
+#pragma unroll
+    for (int j = 0; j < RN; ++j)
+      w[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * kLd + d);
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < RN; ++j)
+        acc[i][j] = fmaf(u[i].w, w[j].w,
+                         fmaf(u[i].z, w[j].z, fmaf(u[i].y, w[j].y, fmaf(u[i].x, w[j].x, acc[i][j]))));
+  }
+}
+
+// acc[i][4 c + e] += sum_j P[row i][j] B[j][64 c + 4 tx + e].
+template <int DP, int RM, int BN>
+__device__ __forceinline__ void rows_by_columns(const float* P, const float* b, int ty, int tx,
+                                                float (&acc)[RM][Cfg<DP>::kRD]) {
+  constexpr int kLd = Cfg<DP>::kLd, kLdP = BN + 4;
+#pragma unroll 2
+  for (int j = 0; j < BN; j += 4) {
+    float p[RM][4];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(P + (ty * RM + i) * kLdP + j);
+      p[i][0] = v.x, p[i][1] = v.y, p[i][2] = v.z, p[i][3] = v.w;
+    }
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(b + (j + jj) * kLd + 64 * c + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+          acc[i][4 * c + 0] = fmaf(p[i][jj], v.x, acc[i][4 * c + 0]);
+          acc[i][4 * c + 1] = fmaf(p[i][jj], v.y, acc[i][4 * c + 1]);
+          acc[i][4 * c + 2] = fmaf(p[i][jj], v.z, acc[i][4 * c + 2]);
+          acc[i][4 * c + 3] = fmaf(p[i][jj], v.w, acc[i][4 * c + 3]);
+        }
+      }
+  }
+}
+
+template <int DP, int RM>
+__device__ __forceinline__ void store_rows(const Heads& x, bool bf16, int64_t row0, int n, int h,
+                                           int D, int ty, int tx, float factor,
+                                           const float (&acc)[RM][Cfg<DP>::kRD]) {
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int r = ty * RM + i;
+    if (r >= n) continue;
+    const int64_t at = (row0 + r) * x.token + (int64_t)h * x.head;
+#pragma unroll
+    for (int c = 0; c < Cfg<DP>::kRD; ++c) {
+      const int d = 64 * (c / 4) + 4 * tx + c % 4;
+      if (d < D) store_elem(x.p, bf16, at + d, factor * acc[i][c]);
+    }
+  }
+}
+
+template <int DP, int RM>
+__device__ __forceinline__ void clear(float (&acc)[RM][Cfg<DP>::kRD]) {
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int c = 0; c < Cfg<DP>::kRD; ++c) acc[i][c] = 0.f;
+}
+
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const Attn p) {
+  using C = Cfg<DP>;
+  constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
+  extern __shared__ float smem[];
+  float *sq = smem, *sk = sq + BM * C::kLd, *sv = sk + BN * C::kLd, *sp = sv + BN * C::kLd;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  pdl_wait();
+  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  AttnTile t;
+  const int past = find_tile<false>(p, BM, blockIdx.x / p.Hq, t);
+  if (past >= 0) {  // rows of no sequence
+    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
+      p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
+      for (int d = 0; d < p.D; ++d)
+        store_elem(p.out.p, p.bf16, row * p.out.token + h * p.out.head + d, 0.f);
+    });
+    return;
+  }
+  const int n = min(BM, t.nq - t.row0);
+  const int keys = keys_of(p, t, t.row0 + n - 1);  // the last row sees the most
+  load_tile<DP>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
+  float m[RM], l[RM], acc[RM][C::kRD];
+  clear<DP, RM>(acc);
+#pragma unroll
+  for (int i = 0; i < RM; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  const float c2 = p.scale * kLog2e;
+  for (int j0 = 0; j0 < keys; j0 += BN) {
+    __syncthreads();  // the tiles before have been read
+    const int nk = min(BN, keys - j0);
+    load_tile<DP>(sk, p.k, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    load_tile<DP>(sv, p.v, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    __syncthreads();
+    float s[RM][RN];
+    rows_by_rows<DP, RM, RN>(sq, sk, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const int sees = keys_of(p, t, t.row0 + ty * RM + i) - j0;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < RN; ++j) {
+        s[i][j] = tx + 16 * j < sees ? s[i][j] * c2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+      top = fmaxf(m[i], half_warp_max(top));
+      const float base = top == -INFINITY ? 0.f : top;  // nothing seen so far
+      const float keep = exp2f(m[i] - base);
+      m[i] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < RN; ++j) {
+        const float e = exp2f(s[i][j] - base);
+        sum += e;
+        sp[(ty * RM + i) * C::kLdP + tx + 16 * j] = e;
+      }
+      l[i] = l[i] * keep + half_warp_sum(sum);
+#pragma unroll
+      for (int c = 0; c < C::kRD; ++c) acc[i][c] *= keep;
+    }
+    __syncwarp();
+    rows_by_columns<DP, RM, BN>(sp, sv, ty, tx, acc);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // an empty row is zeros
+#pragma unroll
+    for (int c = 0; c < C::kRD; ++c) acc[i][c] *= inv;
+    const int r = ty * RM + i;
+    if (tx == 0 && r < n)
+      p.lse[(int64_t)(t.q0 + t.row0 + r) * p.Hq + h] =
+          l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+  }
+  store_rows<DP, RM>(p.out, p.bf16, t.q0 + t.row0, n, h, p.D, ty, tx, 1.f, acc);
+}
+
+// delta = g_out . out, and lse in units of log 2, both [Hq, Tq] (a tile's
+// values are together); +infinity for a row that sees nothing, so that all its
+// probabilities are 0.  With kCopy g_out rounded to bf16 as well.  A warp has
+// four rows, eight lanes each.  What rows of no sequence give is used nowhere.
+template <bool kCopy>
+__global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const Attn p) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 8;
+  const int part = threadIdx.x & 7;
+  const bool there = i < (int64_t)p.Tq * p.Hq;
+  const int64_t t = there ? i / p.Hq : 0;
+  const int h = there ? (int)(i - t * p.Hq) : 0;
+  const int64_t go = t * p.gout.token + h * p.gout.head, oo = t * p.out.token + h * p.out.head;
+  float sum = 0.f;
+  if (there)
+    for (int d = part; d < p.D; d += 8) {
+      const float g = load_elem(p.gout.p, p.gout_bf16, go + d);
+      sum = fmaf(g, load_elem(p.out.p, p.bf16, oo + d), sum);
+      if (kCopy) store_elem(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + d, g);
+    }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (there && part == 0) {
+    const float lse = p.lse[i];
+    p.delta[(int64_t)h * p.Tq + t] = sum;
+    p.lse2[(int64_t)h * p.Tq + t] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  }
+}
+
+// g_k and g_v of a tile of keys: over the query heads that share the key head
+// and the tiles of queries that see it.  Rows are keys, columns queries.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) attn_bwd_keys_simt_kernel(const Attn p) {
+  using C = Cfg<DP>;
+  constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
+  extern __shared__ float smem[];
+  float *sk = smem, *sv = sk + BM * C::kLd, *sq = sv + BM * C::kLd, *sg = sq + BN * C::kLd,
+        *sp = sg + BN * C::kLd, *sd = sp + BM * C::kLdP;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  pdl_wait();
+  const int hk = blockIdx.x % p.Hk, group = p.Hq / p.Hk;
+  AttnTile t;
+  const int past = find_tile<true>(p, BM, blockIdx.x / p.Hk, t);
+  if (past >= 0) {
+    outside_rows<true>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
+      for (int d = 0; d < p.D; ++d) {
+        store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
+        store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
+      }
+    });
+    return;
+  }
+  const int n = min(BM, t.nk - t.row0);
+  load_tile<DP>(sk, p.k, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
+  load_tile<DP>(sv, p.v, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
+  float gk[RM][C::kRD], gv[RM][C::kRD];
+  clear<DP, RM>(gk);
+  clear<DP, RM>(gv);
+  // the first query that sees the tile's first key
+  const int first = p.causal ? max(0, t.row0 + t.nq - t.nk) / BN * BN : 0;
+  const float c2 = p.scale * kLog2e;
+  for (int h = hk * group; h < (hk + 1) * group; ++h)
+    for (int i0 = first; i0 < t.nq; i0 += BN) {
+      __syncthreads();
+      const int nq = min(BN, t.nq - i0);
+      load_tile<DP>(sq, p.q, p.bf16, t.q0 + i0, nq, BN, h, p.D);
+      load_tile<DP>(sg, p.gout, p.gout_bf16, t.q0 + i0, nq, BN, h, p.D);
+      __syncthreads();
+      float s[RM][RN], dp[RM][RN];
+      rows_by_rows<DP, RM, RN>(sk, sq, ty, tx, s);
+      rows_by_rows<DP, RM, RN>(sv, sg, ty, tx, dp);
+#pragma unroll
+      for (int j = 0; j < RN; ++j) {
+        const int i = i0 + tx + 16 * j;  // the query
+        const bool there = i < t.nq;
+        const int64_t at = (int64_t)h * p.Tq + t.q0 + i;
+        const float lse2 = there ? ld_dep_f32(p.lse2 + at) : INFINITY;
+        const float delta = there ? ld_dep_f32(p.delta + at) : 0.f;
+        const int sees = there ? keys_of(p, t, i) - t.row0 : 0;
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+          const float e = ty * RM + r < sees ? exp2f(s[r][j] * c2 - lse2) : 0.f;
+          sp[(ty * RM + r) * C::kLdP + tx + 16 * j] = e;
+          sd[(ty * RM + r) * C::kLdP + tx + 16 * j] =
+              ty * RM + r < sees ? e * (dp[r][j] - delta) : 0.f;
+        }
+      }
+      __syncwarp();
+      rows_by_columns<DP, RM, BN>(sp, sg, ty, tx, gv);
+      rows_by_columns<DP, RM, BN>(sd, sq, ty, tx, gk);
+      __syncwarp();
+    }
+  store_rows<DP, RM>(p.gk, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, p.scale, gk);
+  store_rows<DP, RM>(p.gv, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, 1.f, gv);
+}
+
+// g_q of a tile of queries.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) attn_bwd_queries_simt_kernel(const Attn p) {
+  using C = Cfg<DP>;
+  constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
+  extern __shared__ float smem[];
+  float *sq = smem, *sg = sq + BM * C::kLd, *sk = sg + BM * C::kLd, *sv = sk + BN * C::kLd,
+        *sd = sv + BN * C::kLd;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  pdl_wait();
+  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  AttnTile t;
+  const int past = find_tile<false>(p, BM, blockIdx.x / p.Hq, t);
+  if (past >= 0) {
+    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
+      for (int d = 0; d < p.D; ++d)
+        store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
+    });
+    return;
+  }
+  const int n = min(BM, t.nq - t.row0);
+  const int keys = keys_of(p, t, t.row0 + n - 1);
+  load_tile<DP>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
+  load_tile<DP>(sg, p.gout, p.gout_bf16, t.q0 + t.row0, n, BM, h, p.D);
+  float gq[RM][C::kRD], lse2[RM], delta[RM];
+  clear<DP, RM>(gq);
+#pragma unroll
+  for (int r = 0; r < RM; ++r) {
+    const bool there = ty * RM + r < n;
+    const int64_t at = (int64_t)h * p.Tq + t.q0 + t.row0 + ty * RM + r;
+    lse2[r] = there ? ld_dep_f32(p.lse2 + at) : INFINITY;
+    delta[r] = there ? ld_dep_f32(p.delta + at) : 0.f;
+  }
+  const float c2 = p.scale * kLog2e;
+  for (int j0 = 0; j0 < keys; j0 += BN) {
+    __syncthreads();
+    const int nk = min(BN, keys - j0);
+    load_tile<DP>(sk, p.k, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    load_tile<DP>(sv, p.v, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    __syncthreads();
+    float s[RM][RN], dp[RM][RN];
+    rows_by_rows<DP, RM, RN>(sq, sk, ty, tx, s);
+    rows_by_rows<DP, RM, RN>(sg, sv, ty, tx, dp);
+#pragma unroll
+    for (int r = 0; r < RM; ++r) {
+      const int sees = keys_of(p, t, t.row0 + ty * RM + r) - j0;
+#pragma unroll
+      for (int j = 0; j < RN; ++j)
+        sd[(ty * RM + r) * C::kLdP + tx + 16 * j] =
+            tx + 16 * j < sees ? exp2f(s[r][j] * c2 - lse2[r]) * (dp[r][j] - delta[r]) : 0.f;
+    }
+    __syncwarp();
+    rows_by_columns<DP, RM, BN>(sd, sk, ty, tx, gq);
+    __syncwarp();
+  }
+  store_rows<DP, RM>(p.gq, p.g_bf16, t.q0 + t.row0, n, h, p.D, ty, tx, p.scale, gq);
+}
+
+template <auto kKernel>
+cudaError_t launch(const Attn& p, bool keys, int rows, size_t smem, cudaStream_t st) {
+  const int64_t grid = most_tiles(p, keys, rows) * (keys ? p.Hk : p.Hq);
+  if (grid == 0) return cudaSuccess;
+  cudaError_t e = allow_smem<kKernel>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kKernel, dim3((unsigned)grid), dim3(kThreads), smem, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st) {
+  if (p.D <= 64) return launch<attn_fwd_simt_kernel<64>>(p, false, Cfg<64>::kBM, Cfg<64>::kFwd, st);
+  if (p.D <= 128)
+    return launch<attn_fwd_simt_kernel<128>>(p, false, Cfg<128>::kBM, Cfg<128>::kFwd, st);
+  return launch<attn_fwd_simt_kernel<256>>(p, false, Cfg<256>::kBM, Cfg<256>::kFwd, st);
+}
+
+cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st) {
+  const int64_t grid = ((int64_t)p.Tq * p.Hq * 8 + 255) / 256;
+  if (grid == 0) return cudaSuccess;
+  return launch_pdl(p.gout16.p ? attn_bwd_rows_kernel<true> : attn_bwd_rows_kernel<false>,
+                    dim3((unsigned)grid), dim3(256), 0, st, p);
+}
+
+cudaError_t launch_attn_bwd_keys_simt(const Attn& p, cudaStream_t st) {
+  if (p.D <= 64)
+    return launch<attn_bwd_keys_simt_kernel<64>>(p, true, Cfg<64>::kBM, Cfg<64>::kBwd, st);
+  if (p.D <= 128)
+    return launch<attn_bwd_keys_simt_kernel<128>>(p, true, Cfg<128>::kBM, Cfg<128>::kBwd, st);
+  return launch<attn_bwd_keys_simt_kernel<256>>(p, true, Cfg<256>::kBM, Cfg<256>::kBwd, st);
+}
+
+cudaError_t launch_attn_bwd_queries_simt(const Attn& p, cudaStream_t st) {
+  if (p.D <= 64)
+    return launch<attn_bwd_queries_simt_kernel<64>>(p, false, Cfg<64>::kBM, Cfg<64>::kBwd, st);
+  if (p.D <= 128)
+    return launch<attn_bwd_queries_simt_kernel<128>>(p, false, Cfg<128>::kBM, Cfg<128>::kBwd, st);
+  return launch<attn_bwd_queries_simt_kernel<256>>(p, false, Cfg<256>::kBM, Cfg<256>::kBwd, st);
+}
+
+}  // namespace hlq

@@ -246,4 +246,44 @@ cudaError_t launch_clip_coef(const ClipSums& q, cudaStream_t st);
 cudaError_t launch_clip_scale(const ClipTable& tab, const ClipSums& q, bool first, int grid,
                               cudaStream_t st);
 
+// ---------------------------------------------------------------------------
+// Between a block's linear layers.
+// ---------------------------------------------------------------------------
+// [tokens, heads, D]: strides in elements.
+struct Heads {
+  void* p;
+  int64_t token, head;
+};
+// One call of attention or of its backward pass.
+struct Attn {
+  Heads q, k, v, out;         // out: written forward, read backward
+  float* lse;                 // [Tq, Hq], likewise
+  Heads gout, gq, gk, gv;     // backward
+  float *delta, *lse2;        // backward, workspace: [Hq, Tq] each
+  Heads gout16;               // backward, workspace: g_out as bf16; p null where g_out itself is
+  const int32_t *seqs_q, *seqs_k;  // both null: sequences of one length
+  int batch, Tq, Tk, Hq, Hk, D;
+  int causal;
+  float scale;
+  bool bf16, gout_bf16, g_bf16;
+  unsigned int* status;
+};
+cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st);
+// delta, lse2 and g_out as bf16 (where p.gout16 has room for it)
+cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st);
+cudaError_t launch_attn_bwd_keys_simt(const Attn& p, cudaStream_t st);
+cudaError_t launch_attn_bwd_queries_simt(const Attn& p, cudaStream_t st);
+
+struct Dropout {
+  const void *x, *residual;  // residual may be null; it has y's type
+  void* y;
+  const uint64_t* d_seed;    // added to seed; may be null
+  int64_t ldx, ldr, ldy, T, C;
+  uint64_t seed;
+  uint32_t drop;             // of 65536
+  float scale;
+  bool x_bf16, y_bf16;
+};
+cudaError_t launch_dropout(const Dropout& p, cudaStream_t st);
+
 }  // namespace hlq

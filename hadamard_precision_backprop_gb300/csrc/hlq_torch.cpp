@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <array>
+#include <cmath>
 #include <cstdint>
 #include <memory>
 #include <vector>
@@ -360,10 +361,187 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A [tokens, heads, D] tensor whose heads are contiguous; `shape` [3] sets its
+// shape where it is not yet set (negative), else asks for it.
+struct HeadsArg {
+  hlq_heads h{};
+  int dt = -1;
+};
+HeadsArg heads_arg(Call& c, PyObject* o, int64_t (&shape)[3], int dt) {
+  const at::Tensor* t = c.tensor(o);
+  HeadsArg r;
+  if (!t || t->dim() != 3 || (t->stride(2) != 1 && t->size(2) > 1)) {
+    c.ok = false;
+    return r;
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (shape[i] < 0) shape[i] = t->size(i);
+    if (shape[i] != t->size(i)) c.ok = false;
+  }
+  r.dt = code_of(t->scalar_type());
+  if (r.dt < 0 || (dt >= 0 && r.dt != dt)) c.ok = false;
+  r.h = {const_cast<void*>(t->const_data_ptr()), t->stride(0), t->stride(1)};
+  return r;
+}
+
+hlq_heads heads_out(const at::Tensor& t, int64_t head0 = 0) {
+  char* p = static_cast<char*>(t.mutable_data_ptr());
+  return {p + head0 * t.stride(1) * (int64_t)t.element_size(), t.stride(0), t.stride(1)};
+}
+
+// What the attention calls have in common.
+struct AttnArgs {
+  HeadsArg q, k, v;
+  int64_t sq[3] = {-1, -1, -1}, sk[3] = {-1, -1, -1};
+  const int32_t *seqs = nullptr, *seqs_k = nullptr;
+  int64_t batch = 1;
+  bool causal = false;
+  double scale = 1;
+
+  void read(Call& c, PyObject* const* qkv, PyObject* const* rest) {
+    const at::Tensor* t = c.tensor(qkv[0]);
+    if (!t || t->get_device() != c10::cuda::current_device()) {
+      c.ok = false;
+      return;
+    }
+    c.device = t->get_device();
+    q = heads_arg(c, qkv[0], sq, -1);
+    k = heads_arg(c, qkv[1], sk, q.dt);
+    v = heads_arg(c, qkv[2], sk, q.dt);
+    if (sq[2] != sk[2]) c.ok = false;
+    if (rest[0] != Py_None) {
+      const at::Tensor* s = c.tensor(rest[0]);
+      if (!s || s->dim() != 1 || s->size(0) < 2) {
+        c.ok = false;
+        return;
+      }
+      seqs = static_cast<const int32_t*>(c.vector(rest[0], s->size(0), at::kInt));
+      seqs_k = static_cast<const int32_t*>(c.vector(rest[1], s->size(0), at::kInt));
+      batch = s->size(0) - 1;
+    } else if (rest[1] != Py_None) {
+      c.ok = false;
+    }
+    if (!PyLong_CheckExact(rest[2])) {
+      c.ok = false;
+      return;
+    }
+    const int64_t b = PyLong_AsLongLong(rest[2]);
+    if (b == -1 && PyErr_Occurred()) PyErr_Clear(), c.ok = false;
+    if (!seqs)
+      batch = b;
+    else if (b != 1 && b != batch)
+      c.ok = false;
+    causal = c.flag(rest[3]);
+    scale = rest[4] == Py_None ? 1 / std::sqrt((double)sq[2]) : c.number(rest[4]);
+  }
+};
+
+// (q, k, v, seqs, seqs_k, batch, causal, scale)
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 8) return not_implemented();
+  Call c;
+  AttnArgs x;
+  x.read(c, a, a + 3);
+  if (!c.ok) return not_implemented();
+  at::Tensor out, lse;
+  hlq_status st;
+  {
+    WithoutGil g;
+    out = c.empty({x.sq[0], x.sq[1], x.sq[2]}, x.q.dt == HLQ_BF16 ? at::kBFloat16 : at::kFloat);
+    lse = c.empty({x.sq[0], x.sq[1]}, at::kFloat);
+    const hlq_heads o = heads_out(out);
+    st = hlq_attention(&x.q.h, &x.k.h, &x.v.h, x.q.dt, x.sq[0], x.sk[0], x.sq[1], x.sk[1], x.sq[2],
+                       x.seqs, x.seqs_k, x.batch, x.causal, (float)x.scale, &o,
+                       lse.mutable_data_ptr<float>(), c.stream());
+  }
+  return st == HLQ_OK ? tuple_of({out, lse}) : not_implemented();
+  END_HANDLE_TH_ERRORS
+}
+
+// (g_out, q, k, v, out, lse, seqs, seqs_k, batch, causal, scale, out_dtype, packed)
+PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 13) return not_implemented();
+  Call c;
+  AttnArgs x;
+  x.read(c, a + 1, a + 6);
+  if (!c.ok) return not_implemented();
+  const HeadsArg g = heads_arg(c, a[0], x.sq, -1), o = heads_arg(c, a[4], x.sq, x.q.dt);
+  const int64_t Tq = x.sq[0], Hq = x.sq[1], D = x.sq[2], Tk = x.sk[0], Hk = x.sk[1];
+  const at::Tensor* l = c.tensor(a[5]);
+  if (!l || l->dim() != 2 || l->size(0) != Tq || l->size(1) != Hq || !l->is_contiguous() ||
+      l->scalar_type() != at::kFloat)
+    return not_implemented();
+  const float* lse = l->const_data_ptr<float>();
+  const at::ScalarType type = c.dtype(a[11], x.q.dt);
+  const bool packed = c.flag(a[12]);
+  if (!c.ok || (packed && Tq != Tk)) return not_implemented();
+  at::Tensor gq, gk, gv, ws;
+  hlq_status st;
+  {
+    WithoutGil no_gil;
+    const size_t ws_bytes = hlq_attention_backward_workspace_bytes(Tq, Hq, D, x.q.dt, g.dt);
+    hlq_heads pq, pk, pv;
+    if (packed) {
+      gq = c.empty({Tq, Hq + 2 * Hk, D}, type);
+      pq = heads_out(gq), pk = heads_out(gq, Hq), pv = heads_out(gq, Hq + Hk);
+    } else {
+      gq = c.empty({Tq, Hq, D}, type), gk = c.empty({Tk, Hk, D}, type);
+      gv = c.empty({Tk, Hk, D}, type);
+      pq = heads_out(gq), pk = heads_out(gk), pv = heads_out(gv);
+    }
+    ws = c.workspace(ws_bytes);
+    st = hlq_attention_backward(&g.h, g.dt, &x.q.h, &x.k.h, &x.v.h, &o.h, x.q.dt, lse, Tq, Tk, Hq,
+                                Hk, D, x.seqs, x.seqs_k, x.batch, x.causal, (float)x.scale, &pq,
+                                &pk, &pv, code_of(type), ws.mutable_data_ptr(), ws_bytes,
+                                c.stream());
+  }
+  if (st != HLQ_OK) return not_implemented();
+  return packed ? THPVariable_Wrap(gq) : tuple_of({gq, gk, gv});
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, p, seed, residual, out_dtype)
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5) return not_implemented();
+  Call c;
+  const Call::Rows x = c.first(a[0]);
+  if (!c.ok) return not_implemented();
+  const double p = c.number(a[1]);
+  uint64_t seed = 0;
+  const uint64_t* d_seed = nullptr;
+  if (PyLong_CheckExact(a[2])) {
+    seed = PyLong_AsUnsignedLongLongMask(a[2]);
+    if (PyErr_Occurred()) PyErr_Clear(), c.ok = false;
+  } else {
+    const at::Tensor* t = c.tensor(a[2]);
+    if (!t || t->numel() != 1 || t->scalar_type() != at::kLong) return not_implemented();
+    d_seed = static_cast<const uint64_t*>(t->const_data_ptr());
+  }
+  const Call::Rows r = c.matrix(a[3], -1);
+  const bool residual = a[3] != Py_None;
+  const at::ScalarType type = c.dtype(a[4], residual ? r.dt : x.dt);
+  if (!c.ok || (residual && code_of(type) != r.dt)) return not_implemented();
+  at::Tensor y;
+  hlq_status st;
+  {
+    WithoutGil g;
+    y = c.empty({c.rows, c.cols}, type);
+    st = hlq_dropout(x.p, x.ld, x.dt, r.p, r.ld, c.rows, c.cols, p, seed, d_seed,
+                     y.mutable_data_ptr(), c.cols, code_of(type), c.stream());
+  }
+  return st == HLQ_OK ? THPVariable_Wrap(y) : not_implemented();
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(layer_norm),  METHOD(layer_norm_backward), METHOD(token_logprobs),
-                         METHOD(policy_loss), METHOD(clip_grad_norm),      {nullptr, nullptr, 0, nullptr}};
+                         METHOD(policy_loss), METHOD(clip_grad_norm),      METHOD(attention),
+                         METHOD(attention_backward), METHOD(dropout),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hlq_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -648,6 +648,102 @@ hlq_status hlq_clip_grad_norm(int64_t n, const void *const *h_grads, const int32
                               void *d_ws, size_t ws_bytes, void *stream);
 size_t hlq_clip_grad_norm_workspace_bytes(int64_t n);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Between a block's linear layers in a training step: softmax attention, whose
+ * inputs are parts of the qkv layer's output and whose gradients are that
+ * layer's g_y; its output goes to the projection, whose fp32 g_x is its g_out;
+ * and dropout of what comes back to the residual stream.  The conventions of
+ * the operators around the layer hold (any sizes, alignment of the element
+ * type, equal calls give equal bits).
+ * ---------------------------------------------------------------------------
+ */
+
+/* [tokens, heads, D]: elements of one head of one token are contiguous, tokens
+ * and heads are these strides (in elements) apart, each >= 0 and at most 2^40.
+ * An output's elements must not overlap: its heads follow each other within a
+ * token, or its tokens within a head.  Strides of a dimension of at most one
+ * are not read. */
+typedef struct {
+    void *ptr;
+    int64_t token_stride;
+    int64_t head_stride;
+} hlq_heads;
+
+/*
+ * Softmax attention over packed sequences.  q [Tq, Hq, D], k and v [Tk, Hk, D]
+ * of dtype dt; Hk divides Hq, and query head h takes key head h / (Hq / Hk).
+ * For each query i and key j of the same sequence
+ *   s_ij = scale q_i . k_j,   lse_i = log sum_j exp(s_ij),
+ *   out_i = sum_j exp(s_ij - lse_i) v_j,
+ * out [Tq, Hq, D] of dtype dt, lse fp32 [Tq, Hq] (contiguous).  With `causal`
+ * the last query of a sequence sees all its keys and each one before it one
+ * fewer: j <= i + Lk - Lq.  A query that sees nothing has out 0 and lse -inf.
+ * Sequences: d_seqs NULL: `batch` of them, all of one length (batch divides Tq
+ * and Tk).  Otherwise d_seqs int32 [batch + 1] on the device: sequence b has
+ * the queries d_seqs[b] .. d_seqs[b + 1] - 1, and the keys of d_seqs_k likewise
+ * (NULL: the same offsets; Tk == Tq).  Lengths may be 0.  Rows in front of the
+ * first sequence and behind the last take no part: out 0, lse -inf.  Offsets
+ * that decrease or leave [0, T] raise HLQ_DEV_BADCODE; the outputs are then
+ * unspecified, but nothing outside the tensors is read or written.
+ * Infinities and NaN in a sequence's keys and values may reach every row of that
+ * sequence, masked or not, and no other sequence.
+ * fp32: products and sums in fp32.  bf16: products on the tensor cores where
+ * D <= 128 and q, k and v begin on 16-byte boundaries with strides of whole 16
+ * bytes; the probabilities are then rounded to bf16 for their product with v.
+ * Maxima, sums and out are held in fp32 and out is rounded once.
+ * Any other alignment or D: products in fp32, slower.
+ * D <= 256; Tq Hq, Tk Hk < 2^31; (batch + 1) Hq < 2^30; scale > 0.
+ */
+hlq_status hlq_attention(const hlq_heads *q, const hlq_heads *k, const hlq_heads *v, int dt,
+                         int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D,
+                         const int32_t *d_seqs, const int32_t *d_seqs_k, int64_t batch,
+                         int causal, float scale, const hlq_heads *out, float *d_lse,
+                         void *stream);
+
+/*
+ * Its backward pass; the probabilities are computed again from lse:
+ *   p_ij = exp(s_ij - lse_i),  delta_i = g_out_i . out_i,
+ *   g_v_j = sum_i p_ij g_out_i,  ds_ij = p_ij (g_out_i . v_j - delta_i),
+ *   g_q_i = scale sum_j ds_ij k_j,  g_k_j = scale sum_i ds_ij q_i,
+ * the sums of g_k and g_v also over the query heads that share the key head.
+ * g_out [Tq, Hq, D] of either dtype (gout_dt); q, k, v, out of dtype dt; g_q, g_k,
+ * g_v of either dtype (g_dt); they may be parts of one [T, (Hq + 2 Hk) D] tensor.
+ * Rows of no sequence have gradients of 0, and so have queries that see nothing.
+ * bf16 on the tensor cores as above: g_out, p and ds are rounded to bf16 for
+ * their products (also where the gradients are fp32); all sums are fp32.
+ * Infinities and NaN in a sequence may reach all its gradients, and no others.
+ * Workspace: hlq_attention_backward_workspace_bytes.
+ */
+hlq_status hlq_attention_backward(const hlq_heads *g_out, int gout_dt, const hlq_heads *q,
+                                  const hlq_heads *k, const hlq_heads *v, const hlq_heads *out,
+                                  int dt, const float *d_lse, int64_t Tq, int64_t Tk, int64_t Hq,
+                                  int64_t Hk, int64_t D, const int32_t *d_seqs,
+                                  const int32_t *d_seqs_k, int64_t batch, int causal, float scale,
+                                  const hlq_heads *g_q, const hlq_heads *g_k,
+                                  const hlq_heads *g_v, int g_dt, void *d_ws, size_t ws_bytes,
+                                  void *stream);
+size_t hlq_attention_backward_workspace_bytes(int64_t Tq, int64_t Hq, int64_t D, int dt,
+                                              int gout_dt);
+
+/*
+ * Dropout, with the residual added: for element e = t C + c
+ *   y[t, c] = kept(e) ? x[t, c] 65536 / (65536 - drop) : 0   (+ residual[t, c]),
+ *   drop = p 65536 rounded to nearest even,  kept(e): u(e) >= drop,
+ * u(e) half e % 2 (low first) of word (e % 8) / 2 of Philox4x32-10 with key (seed
+ * lo, seed hi) and counter (e/8 lo, e/8 hi, 4, 0).  The mask is never stored:
+ * the backward pass is the same call on the gradient of y (without residual).
+ * The probability is exact in steps of 2^-16, and the factor is that of the
+ * rounded one.  What is dropped is not read as a number: NaN becomes 0.
+ * x [T, C] of dtype x_dt; residual (may be NULL) and y of dtype y_dt; row
+ * strides, alignments and in place as for the layer norm.  p in [0, 1]; d_seed:
+ * a device word that is added to seed (may be NULL): a captured graph draws a
+ * new mask where that word has changed.
+ */
+hlq_status hlq_dropout(const void *d_x, int64_t ldx, int x_dt, const void *d_residual,
+                       int64_t ldr, int64_t T, int64_t C, double p, uint64_t seed,
+                       const uint64_t *d_seed, void *d_y, int64_t ldy, int y_dt, void *stream);
+
 /* Static text for a status code. */
 const char *hlq_status_string(int status);
 
