@@ -1,0 +1,376 @@
+// hlq_attn_fwd_tc.cu -- attention's forward pass in bf16 on the tensor cores
+// (tcgen05, TMEM, TMA), heads up to 128.
+//
+// A CTA has two tiles of 128 queries of one head and goes over the keys' tiles
+// of 128.  Per tile of keys and of queries:
+//   S = Q K^T (TMEM, fp32)  ->  P = exp2(c S - c m), bf16, in the place of S
+//   O += P V (TMEM, fp32)
+// warp 0 loads (TMA), warp 1 issues the products, warp 2 clears V's rows behind
+// the sequence's end, warps 4-7 and 8-11 are the softmax of the first and of
+// the second tile of queries, a thread to a row: maximum and sum need no
+// shuffles.  While one tile's softmax runs, the products of the other one do.
+//
+// m is the maximum of the tiles so far when it was last taken over; it is taken
+// over again only where the row's maximum has risen by more than 8 in units of
+// log 2 (P then stays below 2^8, which costs bf16 nothing), so that O is
+// rescaled rarely.  Sums are those of the unrounded probabilities, in fp32.
+#include <cmath>
+#include <cstring>
+
+#include "hlq_attn_tc.cuh"
+#include "hlq_rows.cuh"
+
+namespace hlq {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr float kRise = 8.f;
+
+template <int DP>
+struct FwdCfg {
+  static constexpr int kChunks = DP / kChunk;
+  static constexpr uint32_t kTile = kChunks * kChunkBytes;
+  static constexpr int kStages = DP == 64 ? 4 : 2;  // of K and of V each
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * kStages) * kTile + 256;
+  static constexpr uint32_t kO = 256, kColumns = 512;
+};
+
+struct FwdBars {
+  uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_empty[4], v_last, v_clear, s_full[2],
+      p_full[2], o_full[2], drained;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(FwdBars) <= 256, "barriers fit their 256 bytes");
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_fwd_tc_kernel(const Attn p, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, int wide_out) {
+  using C = FwdCfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t *sq = smem, *sk = sq + 2 * C::kTile, *sv = sk + C::kStages * C::kTile;
+  FwdBars& bar = *reinterpret_cast<FwdBars*>(sv + C::kStages * C::kTile);
+  volatile int* abort_flag = &bar.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bar.q_full[g], 1);
+      mbar_init(&bar.s_full[g], 1);
+      mbar_init(&bar.p_full[g], 4);
+      mbar_init(&bar.o_full[g], 1);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
+      mbar_init(&bar.v_full[s], 1);
+      mbar_init(&bar.v_empty[s], 1);
+    }
+    mbar_init(&bar.v_last, 1);
+    mbar_init(&bar.v_clear, 1);
+    mbar_init(&bar.drained, 1);
+    bar.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) alloc(&bar.tmem, C::kColumns);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bar.tmem;
+  pdl_trigger();
+  pdl_wait();
+
+  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  AttnTile t;
+  const int past = find_tile<false>(p, 2 * kRows, blockIdx.x / p.Hq, t);
+  const auto wait = [&](uint64_t* b, uint32_t phase) {
+    return mbar_wait(b, phase & 1, abort_flag, p.status);
+  };
+  // tiles of keys that the two tiles of queries see
+  int tiles[2] = {0, 0};
+  if (past < 0)
+    for (int g = 0; g < 2; ++g) {
+      const int last = min(t.row0 + (g + 1) * kRows, t.nq) - 1;
+      if (last >= t.row0 + g * kRows) tiles[g] = (keys_of(p, t, last) + kRows - 1) / kRows;
+    }
+  const int n = max(tiles[0], tiles[1]);
+  // rows of the sequence's last tile of keys, if this CTA goes as far and it is not full
+  const int rest = n > 0 && t.nk < n * kRows ? t.nk - (n - 1) * kRows : 0;
+
+  if (past >= 0) {
+    outside_rows<false>(p, 2 * kRows, past, threadIdx.x, kThreads, [&](int row) {
+      p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
+      for (int d = 0; d < p.D; ++d)
+        store_elem(p.out.p, true, row * p.out.token + h * p.out.head + d, 0.f);
+    });
+  } else if (warp < 4) {
+   fewer_registers<72>();
+   if (warp == 0) {
+    if (lane == 0 && n > 0) {
+      int k_done = 0, v_done = 0, q_done = 0, last_done = 0;
+      const auto load_q = [&](int g) {
+        mbar_expect_tx(&bar.q_full[g], C::kTile);
+        load_tile<C::kChunks>(sq + g * C::kTile, &mq, &bar.q_full[g], h, t.q0 + t.row0 + g * kRows);
+        ++q_done;
+      };
+      const auto load_k = [&](int j) {
+        const int s = j % C::kStages;
+        if (j >= C::kStages && !wait(&bar.k_empty[s], j / C::kStages - 1)) return false;
+        mbar_expect_tx(&bar.k_full[s], C::kTile);
+        load_tile<C::kChunks>(sk + s * C::kTile, &mk, &bar.k_full[s], hk, t.k0 + j * kRows);
+        ++k_done;
+        return true;
+      };
+      const auto load_v = [&](int j) {
+        const int s = j % C::kStages;
+        if (j >= C::kStages && !wait(&bar.v_empty[s], j / C::kStages - 1)) return false;
+        uint64_t* full = rest && j == n - 1 ? &bar.v_last : &bar.v_full[s];
+        mbar_expect_tx(full, C::kTile);
+        load_tile<C::kChunks>(sv + s * C::kTile, &mv, full, hk, t.k0 + j * kRows);
+        ++(full == &bar.v_last ? last_done : v_done);
+        return true;
+      };
+      load_q(0);
+      load_k(0);
+      if (tiles[1] > 0) load_q(1);
+      for (int j = 0; j < n; ++j)
+        if ((j > 0 && !load_k(j)) || !load_v(j)) break;
+      if (*abort_flag) {  // let the copies under way land
+        ring_drain(bar.q_full, 2, q_done);
+        ring_drain(bar.k_full, C::kStages, k_done);
+        ring_drain(bar.v_full, C::kStages, v_done);
+        ring_drain(&bar.v_last, 1, last_done);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {
+      const int steps = (p.D + 15) / 16;
+      const uint32_t aq = saddr(sq), ak = saddr(sk), av = saddr(sv);
+      bool ok = true;
+      const auto scores = [&](int g, int j) {
+        if (g >= 0 && j < tiles[g]) {
+          fence_after();
+          product_of_rows(tmem + g * kRows, aq + g * C::kTile, ak + (j % C::kStages) * C::kTile, steps);
+          commit(&bar.s_full[g]);
+        }
+      };
+      ok = wait(&bar.q_full[0], 0) && wait(&bar.k_full[0], 0);
+      if (ok) scores(0, 0);
+      if (ok && tiles[1] > 0) ok = wait(&bar.q_full[1], 0);
+      if (ok) scores(1, 0);
+      if (C::kStages < n) commit(&bar.k_empty[0]);
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j % C::kStages;
+        ok = rest && j == n - 1 ? wait(&bar.v_clear, 0) : wait(&bar.v_full[s], j / C::kStages);
+        if (ok && j + 1 < n) ok = wait(&bar.k_full[(j + 1) % C::kStages], (j + 1) / C::kStages);
+        for (int g = 0; g < 2 && ok; ++g) {
+          if (j < tiles[g]) {
+            ok = wait(&bar.p_full[g], j);
+            if (!ok) break;
+            fence_after();
+            product_of_p(tmem + C::kO + g * DP, tmem + g * kRows, av + s * C::kTile, 16 * steps, j > 0);
+            if (j == tiles[g] - 1) commit(&bar.o_full[g]);
+          }
+          scores(g, j + 1);
+        }
+        // what is loaded after these waits for them
+        if (ok && j + C::kStages < n) commit(&bar.v_empty[s]);
+        if (ok && j + 1 + C::kStages < n) commit(&bar.k_empty[(j + 1) % C::kStages]);
+      }
+      if (!ok) drain(&bar.drained);
+    }
+  } else if (warp == 2) {
+    if (rest) {
+      const int s = (n - 1) % C::kStages;
+      if (wait(&bar.v_last, 0)) {
+        clear_rows<C::kChunks>(sv + s * C::kTile, rest);
+        if (lane == 0) mbar_arrive(&bar.v_clear);
+      }
+    }
+   }
+  } else {
+    more_registers<216>();
+    const int g = (warp - 4) >> 2;
+    const int row = t.row0 + g * kRows + (warp & 3) * 32 + lane;  // of the sequence
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // 32 lanes a warp, in bits 16-31
+    const uint32_t ts = tmem + g * kRows + lanes, to = tmem + C::kO + g * DP + lanes;
+    const int sees = keys_of(p, t, row);
+    // the tile's first row sees the fewest
+    const int full = keys_of(p, t, t.row0 + g * kRows) / kRows;
+    const float c2 = p.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < tiles[g] && ok; ++j) {
+      ok = wait(&bar.s_full[g], j);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ld_wait(s[c]);
+      if (j >= full) {
+        const int limit = sees - j * kRows;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i >= limit) s[c][i] = 0xff800000u;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[c][i]));
+      top = fmaxf(top, m);
+      // a row that has seen nothing takes over what it sees
+      const bool rises = top > m && !((top - m) * c2 <= kRise);
+      if (__any_sync(0xffffffffu, rises)) {
+        const float keep = rises ? exp2_fast((m - top) * c2) : 1.f;
+        if (rises) m = top;
+        l *= keep;
+        if (j > 0) {
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            ld32(to + 32 * c, o);
+            ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+            st32(to + 32 * c, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m * c2;
+      const F2 c22 = f2(c2), base2 = f2(base);
+      F2 sum = f2(0.f);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t e[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t(&r)[32] = s[2 * half + i / 16];
+          const int k = 2 * (i % 16);
+          const float2 x = split(fma2(f2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c22, base2));
+          const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+          sum = sum + f2(a, b);
+          e[i] = bf16x2(a, b);
+        }
+        st32(ts + 32 * half, e);
+      }
+      const float2 both = split(sum);
+      l += both.x + both.y;
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[g]);
+    }
+    if (tiles[g] > 0 && ok) ok = __all_sync(0xffffffffu, wait(&bar.o_full[g], 0));
+    const bool there = past < 0 && row < t.nq;
+    if (ok) {
+      fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zeros
+      const int64_t at = (int64_t)(t.q0 + row) * p.out.token + (int64_t)h * p.out.head;
+      if (there)
+        p.lse[(int64_t)(t.q0 + row) * p.Hq + h] =
+            l == 0.f ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c) {
+        uint32_t o[32];
+        if (tiles[g] > 0) {
+          ld32(to + 32 * c, o);
+          ld_wait(o);
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
+        if (there) {
+          if (wide_out) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (32 * c + i < p.D)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.p) + at + 32 * c + i) =
+                    make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]),
+                               bf16x2(v[i + 4], v[i + 5]), bf16x2(v[i + 6], v[i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i < p.D) store_elem(p.out.p, true, at + 32 * c + i, v[i]);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    dealloc(tmem, C::kColumns);
+  }
+}
+
+template <int DP>
+cudaError_t launch(const Attn& p, cudaStream_t st) {
+  using C = FwdCfg<DP>;
+  const int64_t grid = most_tiles(p, false, 2 * kRows) * p.Hq;
+  if (grid == 0) return cudaSuccess;
+  CUtensorMap mq, mk, mv;
+  if (!heads_map(&mq, p.q, p.Tq, p.Hq, p.D) || !heads_map(&mk, p.k, p.Tk, p.Hk, p.D) ||
+      !heads_map(&mv, p.v, p.Tk, p.Hk, p.D))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem<attn_fwd_tc_kernel<DP>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int wide_out = p.D % 8 == 0 && tma_heads(p.out, p.Tq, p.Hq);
+  return launch_pdl(attn_fwd_tc_kernel<DP>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, p,
+                    mq, mk, mv, wide_out);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D) {
+  const auto fn = encode();
+  if (!fn) return false;
+  // a dimension of one element: any stride does
+  const cuuint64_t token = T > 1 ? (cuuint64_t)x.token * 2 : 16;
+  const cuuint64_t head = H > 1 ? (cuuint64_t)x.head * 2 : 16;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {head, token};
+  const cuuint32_t box[3] = {tc::kChunk, 1, tc::kRows}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool attn_tc(const Attn& p) {
+  return p.bf16 && p.D <= 128 && p.Tq > 0 && p.Tk > 0 && tma_heads(p.q, p.Tq, p.Hq) &&
+         tma_heads(p.k, p.Tk, p.Hk) && tma_heads(p.v, p.Tk, p.Hk);
+}
+
+cudaError_t launch_attn_tc(const Attn& p, cudaStream_t st) {
+  return p.D <= 64 ? launch<64>(p, st) : launch<128>(p, st);
+}
+
+}  // namespace hlq

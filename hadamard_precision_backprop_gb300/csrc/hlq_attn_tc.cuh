@@ -1,0 +1,216 @@
+// hlq_attn_tc.cuh -- tensor-core pieces of the attention kernels (tcgen05, TMEM,
+// TMA tiles of heads).
+//
+// A tile of R rows of a head lies in shared memory as TMA writes it with the
+// 128-byte swizzle: chunk c (columns 64 c .. 64 c + 63) is R rows of 128 bytes,
+// chunks R x 128 bytes apart.  The same tile serves as an operand whose rows
+// are the product's rows and whose columns are summed over (K-major, eight rows
+// 1024 bytes apart) or the other way round (MN-major: eight rows are again
+// 1024 bytes apart, and the chunks are the leading dimension's step).
+// Probabilities and their gradients never leave TMEM: the warps that compute
+// them write them back as bf16 pairs, lane = row, and the next product takes
+// them from there as its first operand.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "hlq_attn.cuh"
+#include "hlq_tma.cuh"
+
+namespace hlq {
+namespace tc {
+
+constexpr int kRows = 128;        // rows of a tile
+constexpr int kChunk = 64;        // columns of a chunk
+constexpr uint32_t kChunkBytes = kRows * 128;
+
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// Columns summed over.  `col16`: the first of 16 columns, in steps of 16.
+__device__ __forceinline__ uint64_t by_columns(uint32_t tile, int col16) {
+  const uint32_t at = tile + (uint32_t)(col16 >> 2) * kChunkBytes + (uint32_t)(col16 & 3) * 32;
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Rows summed over.  `row16`: the first of 16 rows, in steps of 16.
+__device__ __forceinline__ uint64_t by_rows(uint32_t tile, int row16) {
+  const uint32_t at = tile + (uint32_t)row16 * 16 * 128;
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(kChunkBytes >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// bf16 x bf16 -> fp32, 128 x n; b_by_rows: the second operand's rows are summed over.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_by_rows) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (b_by_rows ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(kRows >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
+      : "memory");
+}
+// The first operand from TMEM: lane = row, a column holds two of the 16 summed over.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          saddr(bar))
+      : "memory");
+}
+
+// d [128 x 128] = A B^T over `steps` x 16 columns of both tiles.
+__device__ __forceinline__ void product_of_rows(uint32_t d, uint32_t a, uint32_t b, int steps) {
+  constexpr uint32_t id = idesc(kRows, false);
+  for (int k = 0; k < steps; ++k) mma_ss(d, by_columns(a, k), by_columns(b, k), id, k > 0);
+}
+// d [128 x n] (+)= P B over the 128 rows of B; P is in TMEM.
+__device__ __forceinline__ void product_of_p(uint32_t d, uint32_t p, uint32_t b, int n, bool add) {
+  const uint32_t id = idesc(n, true);
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)
+    mma_ts(d, p + 8 * k, by_rows(b, k), id, add || k > 0);
+}
+
+// 32 columns of this thread's TMEM lane; the values are there after ld_wait.
+__device__ __forceinline__ void ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+// The registers pass through the wait, so that nothing that reads them can go
+// before it.
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void alloc(uint32_t* holder, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   saddr(holder)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc(uint32_t base, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns)
+               : "memory");
+}
+
+// After a wait gave up: lets the products issued so far come to their end (for
+// two seconds at most), before shared memory and TMEM go.
+__device__ __forceinline__ void drain(uint64_t* bar) {
+  commit(bar);
+  const unsigned long long t0 = now_ns();
+  while (!mbar_test(bar, 0) && now_ns() - t0 < kWaitNs) {
+  }
+}
+
+// Registers of the calling warpgroup (of the launch's 168 a thread and three
+// warpgroups: 72 + 2 x 216).
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 2^x, 0 for -infinity.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Tile of 128 rows of head h, chunk by chunk; `bar` expects its bytes.
+template <int kChunks>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
+                                          int h, int row) {
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst) + c * kChunkBytes),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c * kChunk), "r"(h), "r"(row), "r"(saddr(bar))
+        : "memory");
+}
+
+// Zeros in rows `first` .. 127 of a tile, by one warp: rows behind a sequence's
+// last hold another sequence's values, and 0 times those need not be 0.
+template <int kChunks>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int first) {
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < (kRows - first) * kChunks * 8; i += 32) {
+    const int piece = i & 7, rest = i >> 3, c = rest % kChunks, r = first + rest / kChunks;
+    *reinterpret_cast<uint4*>(tile + c * kChunkBytes + r * 128 + piece * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+}  // namespace tc
+
+// Whether TMA can read x [T, H, D] of bf16 (a stride of 0 repeats rows, which
+// a tensor map does not).
+inline bool tma_heads(const Heads& x, int64_t T, int64_t H) {
+  const auto stride = [](int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 39); };
+  return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && stride(x.token, T) && stride(x.head, H);
+}
+// Map of x with boxes of 128 tokens x 1 head x 64 columns, zeros outside.
+bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D);
+
+}  // namespace hlq

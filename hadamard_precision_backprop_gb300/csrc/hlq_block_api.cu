@@ -125,7 +125,10 @@ hlq_status hlq_attention(const hlq_heads* q, const hlq_heads* k, const hlq_heads
   p.status = device_status_ptr();
   if (!p.status) return HLQ_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  HLQ_LAUNCH("attn_fwd", s, launch_attn_simt(p, s));
+  if (attn_tc(p))
+    HLQ_LAUNCH("attn_fwd_tc", s, launch_attn_tc(p, s));
+  else
+    HLQ_LAUNCH("attn_fwd", s, launch_attn_simt(p, s));
   return HLQ_OK;
 }
 

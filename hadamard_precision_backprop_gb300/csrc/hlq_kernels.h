@@ -268,6 +268,8 @@ struct Attn {
   bool bf16, gout_bf16, g_bf16;
   unsigned int* status;
 };
+bool attn_tc(const Attn& p);  // whether the tensor-core kernels take q, k and v
+cudaError_t launch_attn_tc(const Attn& p, cudaStream_t st);
 cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st);
 // delta, lse2 and g_out as bf16 (where p.gout16 has room for it)
 cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st);
