@@ -24,7 +24,7 @@ SOURCES = ["hlq_api.cu", "hlq_quant.cu", "hlq_gemm_simple.cu", "hlq_gemm_tc.cu",
            "hlq_step_api.cu", "hlq_norm.cu", "hlq_norm_ring_bf16.cu",
            "hlq_norm_ring_f32.cu", "hlq_norm_elem.cu", "hlq_loss.cu", "hlq_clip.cu",
            "hlq_block_api.cu", "hlq_attn_simt.cu", "hlq_attn_fwd_tc.cu",
-           "hlq_dropout.cu", "hlq_noalloc.cu"]
+           "hlq_attn_bwd_tc.cu", "hlq_dropout.cu", "hlq_noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

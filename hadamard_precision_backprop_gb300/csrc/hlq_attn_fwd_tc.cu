@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < DP / 32; ++c) {
         uint32_t o[32];
         if (tiles[g] > 0) {
+          __syncwarp();
           ld32(to + 32 * c, o);
           ld_wait(o);
         }
