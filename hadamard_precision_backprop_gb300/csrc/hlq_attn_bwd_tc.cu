@@ -30,17 +30,6 @@ using namespace tc;
 
 constexpr int kThreads = 384;
 
-// P or dS as the first operand: 16 columns summed over at a time, the first 64
-// from column 0 on, the others from 64 on (each half lies in the place of the
-// half of the fp32 tile that it was computed from).
-__device__ __forceinline__ void product_of_halves(uint32_t d, uint32_t p, uint32_t b, int n,
-                                                  bool add) {
-  const uint32_t id = idesc(n, true);
-#pragma unroll
-  for (int k = 0; k < kRows / 16; ++k)
-    mma_ts(d, p + (k >> 2) * 64 + (k & 3) * 8, by_rows(b, k), id, add || k > 0);
-}
-
 // 64 columns of this thread's row.
 __device__ __forceinline__ void ld64(uint32_t at, uint32_t (&r)[2][32]) {
   ld32(at, r[0]);
@@ -151,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   pdl_trigger();
   pdl_wait();
 
@@ -159,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   AttnTile t;
   const int past = find_tile<true>(p, kRows, blockIdx.x / p.Hk, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
-    return mbar_wait(b, phase & 1, abort_flag, p.status);
+    return wait_for(b, phase, abort_flag, p.status);
   };
   // tiles of queries of a head: from the one with the first query that sees the
   // tile's first key
@@ -207,49 +196,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring_drain(bar.g_full, C::kStages, g_done);
         }
       }
-    } else if (warp == 1) {
-      if (lane == 0 && n > 0) {
-        const int steps = (p.D + 15) / 16;
-        const uint32_t ak = saddr(sk), av = saddr(sv), aq = saddr(sq), ag = saddr(sg);
-        bool ok = wait(&bar.kv_full, 0);
-        const auto scores = [&](int it) {
-          const int s = it % C::kStages;
-          ok = wait(&bar.q_ready[s], it / C::kStages);
-          if (!ok) return;
-          fence_after();
-          product_of_rows(tmem + C::kS, ak, aq + s * C::kTile, steps);
+    } else if (warp == 1) {  // the whole warp, of which one thread issues
+      const int steps = (p.D + 15) / 16;
+      const uint32_t id = idesc(16 * steps, true);
+      const uint32_t ak = by_columns(saddr(sk)), av = by_columns(saddr(sv));
+      const uint32_t aq = by_columns(saddr(sq)), ag = by_columns(saddr(sg));
+      const uint32_t rq = by_rows(saddr(sq)), rg = by_rows(saddr(sg));
+      constexpr uint32_t kStep = C::kTile >> 4;
+      bool ok = n > 0 && wait(&bar.kv_full, 0);
+      const auto scores = [&](int it) {
+        const int s = it % C::kStages;
+        ok = wait(&bar.q_ready[s], it / C::kStages);
+        if (!ok) return;
+        fence_after();
+        if (elect_one()) {
+          product_of_rows<DP / 16>(tmem + C::kS, ak, aq + s * kStep, steps);
           commit(&bar.s_full);
-        };
-        const auto gradients = [&](int it) {
-          const int s = it % C::kStages;
-          ok = wait(&bar.g_ready[s], it / C::kStages);
-          if (!ok) return;
-          fence_after();
-          product_of_rows(tmem + C::kD, av, ag + s * C::kTile, steps);
-          commit(&bar.d_full);
-        };
-        if (ok) scores(0);
-        if (ok) gradients(0);
-        for (int it = 0; it < n && ok; ++it) {
-          const int s = it % C::kStages;
-          ok = wait(&bar.p_full, it);
-          if (!ok) break;
-          fence_after();
-          product_of_halves(tmem + C::kV, tmem + C::kS, ag + s * C::kTile, 16 * steps, it > 0);
-          if (it + C::kStages < n) commit(&bar.g_empty[s]);
-          if (it + 1 < n) scores(it + 1);
-          if (ok) ok = wait(&bar.ds_full, it);
-          if (!ok) break;
-          fence_after();
-          product_of_halves(tmem + C::kK, tmem + C::kD, aq + s * C::kTile, 16 * steps, it > 0);
-          if (it + C::kStages < n) commit(&bar.q_empty[s]);
-          if (it + 1 < n) gradients(it + 1);
         }
+        __syncwarp();
+      };
+      const auto gradients = [&](int it) {
+        const int s = it % C::kStages;
+        ok = wait(&bar.g_ready[s], it / C::kStages);
+        if (!ok) return;
+        fence_after();
+        if (elect_one()) {
+          product_of_rows<DP / 16>(tmem + C::kD, av, ag + s * kStep, steps);
+          commit(&bar.d_full);
+        }
+        __syncwarp();
+      };
+      if (ok) scores(0);
+      if (ok) gradients(0);
+      for (int it = 0; it < n && ok; ++it) {
+        const int s = it % C::kStages;
+        const bool reused = it + C::kStages < n;
+        ok = wait(&bar.p_full, it);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          product_of_p<64>(tmem + C::kV, tmem + C::kS, rg + s * kStep, id, it > 0);
+          if (reused) commit(&bar.g_empty[s]);
+        }
+        __syncwarp();
+        if (it + 1 < n) scores(it + 1);
+        if (ok) ok = wait(&bar.ds_full, it);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          product_of_p<64>(tmem + C::kK, tmem + C::kD, rq + s * kStep, id, it > 0);
+          if (reused) commit(&bar.q_empty[s]);
+        }
+        __syncwarp();
+        if (it + 1 < n) gradients(it + 1);
+      }
+      if (n > 0 && elect_one()) {
         if (ok)
           commit(&bar.acc_full);
         else
           drain(&bar.drained);
       }
+      __syncwarp();
     } else if (warp == 2) {  // clears the rows behind the sequence's end
       for (int it = 0; it < n; ++it) {
         const int s = it % C::kStages, use = it / C::kStages;
@@ -268,11 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i0 = tile_of(it) * kRows;
         const int64_t at = (int64_t)head_of(it) * p.Tq + t.q0 + i0;
         float* to = stats + s * 2 * kRows;
+        float v[2][kRows / 32];  // all on their way before the first is stored
 #pragma unroll
-        for (int i = lane; i < kRows; i += 32) {
-          const bool there = i0 + i < t.nq;
-          to[i] = there ? ld_dep_f32(p.lse2 + at + i) : INFINITY;
-          to[kRows + i] = there ? ld_dep_f32(p.delta + at + i) : 0.f;
+        for (int i = 0; i < kRows / 32; ++i) {
+          const bool there = i0 + 32 * i + lane < t.nq;
+          v[0][i] = there ? ld_dep_f32(p.lse2 + at + 32 * i + lane) : INFINITY;
+          v[1][i] = there ? ld_dep_f32(p.delta + at + 32 * i + lane) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows / 32; ++i) {
+          to[32 * i + lane] = v[0][i];
+          to[kRows + 32 * i + lane] = v[1][i];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.stat_full[s]);
@@ -435,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   pdl_trigger();
   pdl_wait();
 
@@ -443,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   AttnTile t;
   const int past = find_tile<false>(p, kRows, blockIdx.x / p.Hq, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
-    return mbar_wait(b, phase & 1, abort_flag, p.status);
+    return wait_for(b, phase, abort_flag, p.status);
   };
   const int keys = past < 0 ? keys_of(p, t, min(t.row0 + kRows, t.nq) - 1) : 0;
   const int n = (keys + kRows - 1) / kRows;
@@ -483,45 +496,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      if (lane == 0 && n > 0) {
-        const int steps = (p.D + 15) / 16;
-        const uint32_t aq = saddr(sq), ag = saddr(sg), ak = saddr(sk), av = saddr(sv);
-        bool ok = wait(&bar.qg_full, 0);
-        const auto scores = [&](int j) {
-          const int s = j % C::kStagesK;
-          ok = rest && j == n - 1 ? wait(&bar.k_clear, 0) : wait(&bar.k_full[s], j / C::kStagesK);
-          if (!ok) return;
-          fence_after();
-          product_of_rows(tmem + C::kS + 128 * (j & 1), aq, ak + s * C::kTile, steps);
+      const int steps = (p.D + 15) / 16;
+      const uint32_t id = idesc(16 * steps, true);
+      const uint32_t aq = by_columns(saddr(sq)), ag = by_columns(saddr(sg));
+      const uint32_t ak = by_columns(saddr(sk)), av = by_columns(saddr(sv)), rk = by_rows(saddr(sk));
+      constexpr uint32_t kStep = C::kTile >> 4;
+      bool ok = n > 0 && wait(&bar.qg_full, 0);
+      const auto scores = [&](int j) {
+        const int s = j % C::kStagesK;
+        ok = rest && j == n - 1 ? wait(&bar.k_clear, 0) : wait(&bar.k_full[s], j / C::kStagesK);
+        if (!ok) return;
+        fence_after();
+        if (elect_one()) {
+          product_of_rows<DP / 16>(tmem + C::kS + 128 * (j & 1), aq, ak + s * kStep, steps);
           commit(&bar.s_full[j & 1]);
-        };
-        const auto gradients = [&](int j) {
-          const int u = j % C::kStagesV;
-          ok = wait(&bar.v_full[u], j / C::kStagesV);
-          if (!ok) return;
-          fence_after();
-          product_of_rows(tmem + C::kD, ag, av + u * C::kTile, steps);
+        }
+        __syncwarp();
+      };
+      const auto gradients = [&](int j) {
+        const int u = j % C::kStagesV;
+        ok = wait(&bar.v_full[u], j / C::kStagesV);
+        if (!ok) return;
+        fence_after();
+        if (elect_one()) {
+          product_of_rows<DP / 16>(tmem + C::kD, ag, av + u * kStep, steps);
           commit(&bar.d_full);
           if (j + C::kStagesV < n) commit(&bar.v_empty[u]);
-        };
-        if (ok) scores(0);
-        if (ok) gradients(0);
-        if (ok && n > 1) scores(1);
-        for (int j = 0; j < n && ok; ++j) {
-          const int s = j % C::kStagesK;
-          ok = wait(&bar.ds_full, j);
-          if (!ok) break;
-          fence_after();
-          product_of_halves(tmem + C::kQ, tmem + C::kD, ak + s * C::kTile, 16 * steps, j > 0);
-          if (j + C::kStagesK < n) commit(&bar.k_empty[s]);
-          if (j + 1 < n) gradients(j + 1);
-          if (ok && j + 2 < n) scores(j + 2);
         }
+        __syncwarp();
+      };
+      if (ok) scores(0);
+      if (ok) gradients(0);
+      if (ok && n > 1) scores(1);
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j % C::kStagesK;
+        ok = wait(&bar.ds_full, j);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          product_of_p<64>(tmem + C::kQ, tmem + C::kD, rk + s * kStep, id, j > 0);
+          if (j + C::kStagesK < n) commit(&bar.k_empty[s]);
+        }
+        __syncwarp();
+        if (j + 1 < n) gradients(j + 1);
+        if (ok && j + 2 < n) scores(j + 2);
+      }
+      if (n > 0 && elect_one()) {
         if (ok)
           commit(&bar.acc_full);
         else
           drain(&bar.drained);
       }
+      __syncwarp();
     } else if (warp == 2) {
       if (rest) {
         if (__all_sync(0xffffffffu, wait(&bar.k_last, 0))) {

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   pdl_trigger();
   pdl_wait();
 
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   AttnTile t;
   const int past = find_tile<false>(p, 2 * kRows, blockIdx.x / p.Hq, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
-    return mbar_wait(b, phase & 1, abort_flag, p.status);
+    return wait_for(b, phase, abort_flag, p.status);
   };
   // tiles of keys that the two tiles of queries see
   int tiles[2] = {0, 0};
@@ -149,23 +149,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_drain(&bar.v_last, 1, last_done);
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+   } else if (warp == 1) {  // the whole warp, of which one thread issues
       const int steps = (p.D + 15) / 16;
-      const uint32_t aq = saddr(sq), ak = saddr(sk), av = saddr(sv);
-      bool ok = true;
+      const uint32_t id = idesc(16 * steps, true);
+      const uint32_t aq = by_columns(saddr(sq)), ak = by_columns(saddr(sk)), av = by_rows(saddr(sv));
+      constexpr uint32_t kStep = C::kTile >> 4;
+      bool ok = n > 0;
       const auto scores = [&](int g, int j) {
-        if (g >= 0 && j < tiles[g]) {
-          fence_after();
-          product_of_rows(tmem + g * kRows, aq + g * C::kTile, ak + (j % C::kStages) * C::kTile, steps);
+        if (j >= tiles[g]) return;
+        fence_after();
+        if (elect_one()) {
+          product_of_rows<DP / 16>(tmem + g * kRows, aq + g * kStep, ak + (j % C::kStages) * kStep, steps);
           commit(&bar.s_full[g]);
         }
+        __syncwarp();
       };
-      ok = wait(&bar.q_full[0], 0) && wait(&bar.k_full[0], 0);
+      const auto give_back = [&](uint64_t* b) {
+        if (elect_one()) commit(b);
+        __syncwarp();
+      };
+      ok = ok && wait(&bar.q_full[0], 0) && wait(&bar.k_full[0], 0);
       if (ok) scores(0, 0);
       if (ok && tiles[1] > 0) ok = wait(&bar.q_full[1], 0);
       if (ok) scores(1, 0);
-      if (C::kStages < n) commit(&bar.k_empty[0]);
+      if (ok && C::kStages < n) give_back(&bar.k_empty[0]);
       for (int j = 0; j < n && ok; ++j) {
         const int s = j % C::kStages;
         ok = rest && j == n - 1 ? wait(&bar.v_clear, 0) : wait(&bar.v_full[s], j / C::kStages);
@@ -175,18 +182,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(&bar.p_full[g], j);
             if (!ok) break;
             fence_after();
-            product_of_p(tmem + C::kO + g * DP, tmem + g * kRows, av + s * C::kTile, 16 * steps, j > 0);
-            if (j == tiles[g] - 1) commit(&bar.o_full[g]);
+            if (elect_one()) {
+              product_of_p<32>(tmem + C::kO + g * DP, tmem + g * kRows, av + s * kStep, id, j > 0);
+              if (j == tiles[g] - 1) commit(&bar.o_full[g]);
+            }
+            __syncwarp();
           }
           scores(g, j + 1);
         }
         // what is loaded after these waits for them
-        if (ok && j + C::kStages < n) commit(&bar.v_empty[s]);
-        if (ok && j + 1 + C::kStages < n) commit(&bar.k_empty[(j + 1) % C::kStages]);
+        if (ok && j + C::kStages < n) give_back(&bar.v_empty[s]);
+        if (ok && j + 1 + C::kStages < n) give_back(&bar.k_empty[(j + 1) % C::kStages]);
       }
-      if (!ok) drain(&bar.drained);
-    }
-  } else if (warp == 2) {
+      if (!ok && n > 0 && elect_one()) drain(&bar.drained);
+      __syncwarp();
+   } else if (warp == 2) {
     if (rest) {
       const int s = (n - 1) % C::kStages;
       if (wait(&bar.v_last, 0)) {

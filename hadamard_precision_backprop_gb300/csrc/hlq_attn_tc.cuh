@@ -33,17 +33,52 @@ __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// Columns summed over.  `col16`: the first of 16 columns, in steps of 16.
-__device__ __forceinline__ uint64_t by_columns(uint32_t tile, int col16) {
-  const uint32_t at = tile + (uint32_t)(col16 >> 2) * kChunkBytes + (uint32_t)(col16 & 3) * 32;
-  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Matrix descriptors: the low word holds the tile's address and the leading
+// step, the high word is the same for all.  Operands are taken in steps of 16
+// columns (rows), which are constants added to the low word: a product of 128 x
+// 128 x 16 takes 64 clocks, and the one thread that issues them has no time for
+// more (descriptors put together for each of them: 110 to 130 clocks).
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint64_t desc(uint32_t low) { return (uint64_t)kDescHigh << 32 | low; }
+// Columns summed over (the leading step is not used), or rows.
+__device__ __forceinline__ uint32_t by_columns(uint32_t tile) { return tile >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t by_rows(uint32_t tile) {
+  return tile >> 4 | kChunkBytes >> 4 << 16;
 }
-// Rows summed over.  `row16`: the first of 16 rows, in steps of 16.
-__device__ __forceinline__ uint64_t by_rows(uint32_t tile, int row16) {
-  const uint32_t at = tile + (uint32_t)row16 * 16 * 128;
-  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(kChunkBytes >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+__host__ __device__ constexpr uint32_t column_step(int k) {
+  return ((uint32_t)(k >> 2) * kChunkBytes + (uint32_t)(k & 3) * 32) >> 4;
+}
+__host__ __device__ constexpr uint32_t row_step(int k) { return (uint32_t)k * 16 * 128 >> 4; }
+
+// One thread of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+
+// Bounded wait, as mbar_wait, for waits that a product or a softmax hangs on: the
+// time and the abort flag are looked at every 64th try only (reading the timer
+// takes long enough to be missed on every wait).
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t phase, volatile int* abort_flag,
+                                         unsigned int* status) {
+  const uint32_t parity = phase & 1;
+  unsigned long long t0 = 0;
+  for (int i = 1; !mbar_test(b, parity); ++i) {
+    if (i % 64 != 0) continue;
+    if (*abort_flag) return false;
+    const unsigned long long t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitNs) {
+      if (atomicExch((int*)abort_flag, 1) == 0) atomicOr(status, HLQ_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
 // bf16 x bf16 -> fp32, 128 x n; b_by_rows: the second operand's rows are summed over.
@@ -74,17 +109,23 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
-// d [128 x 128] = A B^T over `steps` x 16 columns of both tiles.
+// d [128 x 128] = A B^T over the first `steps` x 16 columns of both tiles (of
+// kSteps at most).
+template <int kSteps>
 __device__ __forceinline__ void product_of_rows(uint32_t d, uint32_t a, uint32_t b, int steps) {
   constexpr uint32_t id = idesc(kRows, false);
-  for (int k = 0; k < steps; ++k) mma_ss(d, by_columns(a, k), by_columns(b, k), id, k > 0);
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k)
+    if (k < steps) mma_ss(d, desc(a + column_step(k)), desc(b + column_step(k)), id, k > 0);
 }
-// d [128 x n] (+)= P B over the 128 rows of B; P is in TMEM.
-__device__ __forceinline__ void product_of_p(uint32_t d, uint32_t p, uint32_t b, int n, bool add) {
-  const uint32_t id = idesc(n, true);
+// d [128 x n] (+)= P B over the 128 rows of B; P is in TMEM, its columns from 64
+// on kSecond columns behind the first.
+template <int kSecond>
+__device__ __forceinline__ void product_of_p(uint32_t d, uint32_t p, uint32_t b, uint32_t id,
+                                             bool add) {
 #pragma unroll
   for (int k = 0; k < kRows / 16; ++k)
-    mma_ts(d, p + 8 * k, by_rows(b, k), id, add || k > 0);
+    mma_ts(d, p + (k >> 2) * kSecond + (k & 3) * 8, desc(b + row_step(k)), id, add || k > 0);
 }
 
 // 32 columns of this thread's TMEM lane; the values are there after ld_wait.
