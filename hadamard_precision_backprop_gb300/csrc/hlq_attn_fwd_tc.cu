@@ -5,10 +5,11 @@
 // of 128.  Per tile of keys and of queries:
 //   S = Q K^T (TMEM, fp32)  ->  P = exp2(c S - c m), bf16, in the place of S
 //   O += P V (TMEM, fp32)
-// warp 0 loads (TMA), warp 1 issues the products, warp 2 clears V's rows behind
-// the sequence's end, warps 4-7 and 8-11 are the softmax of the first and of
-// the second tile of queries, a thread to a row: maximum and sum need no
-// shuffles.  While one tile's softmax runs, the products of the other one do.
+// warp 0 loads (TMA), warps 1 and 3 issue the products of the first and of the
+// second tile of queries, warp 2 clears V's rows behind the sequence's end,
+// warps 4-7 and 8-11 are the softmax of the two tiles, a thread to a row: maximum
+// and sum need no shuffles.  While one tile's softmax runs, the products of the
+// other one do; the product with V begins when half of P is there.
 //
 // m is the maximum of the tiles so far when it was last taken over; it is taken
 // over again only where the row's maximum has risen by more than 8 in units of
@@ -39,7 +40,7 @@ struct FwdCfg {
 
 struct FwdBars {
   uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_empty[4], v_last, v_clear, s_full[2],
-      p_full[2], o_full[2], drained;
+      p_full[2][2], o_full[2], drained[2];
   uint32_t tmem;
   int abort;
 };
@@ -63,18 +64,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bar.q_full[g], 1);
       mbar_init(&bar.s_full[g], 1);
-      mbar_init(&bar.p_full[g], 4);
+      mbar_init(&bar.p_full[g][0], 4);
+      mbar_init(&bar.p_full[g][1], 4);
       mbar_init(&bar.o_full[g], 1);
+      mbar_init(&bar.drained[g], 1);
     }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bar.k_full[s], 1);
-      mbar_init(&bar.k_empty[s], 1);
+      mbar_init(&bar.k_empty[s], 2);
       mbar_init(&bar.v_full[s], 1);
-      mbar_init(&bar.v_empty[s], 1);
+      mbar_init(&bar.v_empty[s], 2);
     }
     mbar_init(&bar.v_last, 1);
     mbar_init(&bar.v_clear, 1);
-    mbar_init(&bar.drained, 1);
     bar.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -149,52 +151,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_drain(&bar.v_last, 1, last_done);
       }
     }
-   } else if (warp == 1) {  // the whole warp, of which one thread issues
+   } else if (warp != 2) {  // the whole warp, of which one thread issues
+      const int g = warp >> 1;
       const int steps = (p.D + 15) / 16;
       const uint32_t id = idesc(16 * steps, true);
-      const uint32_t aq = by_columns(saddr(sq)), ak = by_columns(saddr(sk)), av = by_rows(saddr(sv));
+      const uint32_t aq = by_columns(saddr(sq) + g * C::kTile), ak = by_columns(saddr(sk));
+      const uint32_t av = by_rows(saddr(sv)), ts = tmem + g * kRows, to = tmem + C::kO + g * DP;
       constexpr uint32_t kStep = C::kTile >> 4;
-      bool ok = n > 0;
-      const auto scores = [&](int g, int j) {
-        if (j >= tiles[g]) return;
+      bool ok = tiles[g] == 0 || wait(&bar.q_full[g], 0);
+      const auto scores = [&](int j) {
+        const int s = j % C::kStages;
+        ok = wait(&bar.k_full[s], j / C::kStages);
+        if (!ok) return;
         fence_after();
         if (elect_one()) {
-          product_of_rows<DP / 16>(tmem + g * kRows, aq + g * kStep, ak + (j % C::kStages) * kStep, steps);
+          product_of_rows<DP / 16>(ts, aq, ak + s * kStep, steps);
           commit(&bar.s_full[g]);
+          if (j + C::kStages < n) commit(&bar.k_empty[s]);
         }
         __syncwarp();
       };
-      const auto give_back = [&](uint64_t* b) {
-        if (elect_one()) commit(b);
-        __syncwarp();
-      };
-      ok = ok && wait(&bar.q_full[0], 0) && wait(&bar.k_full[0], 0);
-      if (ok) scores(0, 0);
-      if (ok && tiles[1] > 0) ok = wait(&bar.q_full[1], 0);
-      if (ok) scores(1, 0);
-      if (ok && C::kStages < n) give_back(&bar.k_empty[0]);
-      for (int j = 0; j < n && ok; ++j) {
+      if (ok && tiles[g] > 0) scores(0);
+      for (int j = 0; j < tiles[g] && ok; ++j) {
         const int s = j % C::kStages;
         ok = rest && j == n - 1 ? wait(&bar.v_clear, 0) : wait(&bar.v_full[s], j / C::kStages);
-        if (ok && j + 1 < n) ok = wait(&bar.k_full[(j + 1) % C::kStages], (j + 1) / C::kStages);
-        for (int g = 0; g < 2 && ok; ++g) {
-          if (j < tiles[g]) {
-            ok = wait(&bar.p_full[g], j);
-            if (!ok) break;
-            fence_after();
-            if (elect_one()) {
-              product_of_p<32>(tmem + C::kO + g * DP, tmem + g * kRows, av + s * kStep, id, j > 0);
-              if (j == tiles[g] - 1) commit(&bar.o_full[g]);
-            }
-            __syncwarp();
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = wait(&bar.p_full[g][half], j);
+          if (!ok) break;
+          fence_after();
+          if (elect_one()) {
+            product_of_p(to, ts + 32 * half, av + s * kStep, id, half, j > 0 || half > 0);
+            if (half && j == tiles[g] - 1) commit(&bar.o_full[g]);
+            if (half && j + C::kStages < n) commit(&bar.v_empty[s]);
           }
-          scores(g, j + 1);
+          __syncwarp();
         }
-        // what is loaded after these waits for them
-        if (ok && j + C::kStages < n) give_back(&bar.v_empty[s]);
-        if (ok && j + 1 + C::kStages < n) give_back(&bar.k_empty[(j + 1) % C::kStages]);
+        if (ok && j + 1 < tiles[g]) scores(j + 1);
       }
-      if (!ok && n > 0 && elect_one()) drain(&bar.drained);
+      // tiles of keys that the other tile of queries alone sees
+      for (int j = tiles[g]; j + C::kStages < n && ok; ++j) {
+        const int s = j % C::kStages;
+        ok = wait(&bar.k_full[s], j / C::kStages) && wait(&bar.v_full[s], j / C::kStages);
+        if (ok && lane == 0) {
+          mbar_arrive(&bar.k_empty[s]);
+          mbar_arrive(&bar.v_empty[s]);
+        }
+      }
+      if (!ok && elect_one()) drain(&bar.drained[g]);
       __syncwarp();
    } else if (warp == 2) {
     if (rest) {
@@ -235,11 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i)
             if (32 * c + i >= limit) s[c][i] = 0xff800000u;
       }
-      float top = -INFINITY;
+      float tops[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) {
+        tops[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[c][i]));
+        for (int i = 2; i < 32; i += 2)
+          tops[c] = max3(tops[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+      }
+      float top = max3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
       top = fmaxf(top, m);
       // a row that has seen nothing takes over what it sees
       const bool rises = top > m && !((top - m) * c2 <= kRise);
@@ -275,13 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           e[i] = bf16x2(a, b);
         }
         st32(ts + 32 * half, e);
+        st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[g][half]);
       }
       const float2 both = split(sum);
       l += both.x + both.y;
-      st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[g]);
     }
     if (tiles[g] > 0 && ok) ok = __all_sync(0xffffffffu, wait(&bar.o_full[g], 0));
     const bool there = past < 0 && row < t.nq;
@@ -335,8 +342,8 @@ cudaError_t launch(const Attn& p, cudaStream_t st) {
   const int64_t grid = most_tiles(p, false, 2 * kRows) * p.Hq;
   if (grid == 0) return cudaSuccess;
   CUtensorMap mq, mk, mv;
-  if (!heads_map(&mq, p.q, p.Tq, p.Hq, p.D) || !heads_map(&mk, p.k, p.Tk, p.Hk, p.D) ||
-      !heads_map(&mv, p.v, p.Tk, p.Hk, p.D))
+  if (!heads_map(&mq, p.q, p.Tq, p.Hq, p.D, kRows) || !heads_map(&mk, p.k, p.Tk, p.Hk, p.D, kRows) ||
+      !heads_map(&mv, p.v, p.Tk, p.Hk, p.D, kRows))
     return cudaErrorInvalidValue;
   cudaError_t e = allow_smem<attn_fwd_tc_kernel<DP>>(C::kSmem);
   if (e != cudaSuccess) return e;
@@ -360,7 +367,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode() {
 
 }  // namespace
 
-bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D) {
+bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D, int rows) {
   const auto fn = encode();
   if (!fn) return false;
   // a dimension of one element: any stride does
@@ -368,7 +375,7 @@ bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D
   const cuuint64_t head = H > 1 ? (cuuint64_t)x.head * 2 : 16;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {head, token};
-  const cuuint32_t box[3] = {tc::kChunk, 1, tc::kRows}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {tc::kChunk, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -42,13 +42,22 @@ constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint64_t desc(uint32_t low) { return (uint64_t)kDescHigh << 32 | low; }
 // Columns summed over (the leading step is not used), or rows.
 __device__ __forceinline__ uint32_t by_columns(uint32_t tile) { return tile >> 4 | 1u << 16; }
-__device__ __forceinline__ uint32_t by_rows(uint32_t tile) {
-  return tile >> 4 | kChunkBytes >> 4 << 16;
+__device__ __forceinline__ uint32_t by_rows(uint32_t tile, int rows = kRows) {
+  return tile >> 4 | (uint32_t)rows * 128 >> 4 << 16;
 }
-__host__ __device__ constexpr uint32_t column_step(int k) {
-  return ((uint32_t)(k >> 2) * kChunkBytes + (uint32_t)(k & 3) * 32) >> 4;
+__host__ __device__ constexpr uint32_t column_step(int k, int rows = kRows) {
+  return ((uint32_t)(k >> 2) * (rows * 128) + (uint32_t)(k & 3) * 32) >> 4;
 }
 __host__ __device__ constexpr uint32_t row_step(int k) { return (uint32_t)k * 16 * 128 >> 4; }
+
+// 16 more columns summed over, of which the first three hold a number for each
+// row (see hlq_attn_bwd_tc.cu): [128 x 16] without swizzle, 8 rows x 16 bytes
+// together, the two halves of a row 128 bytes and eight rows 256 bytes apart.
+constexpr uint32_t kMoreBytes = kRows * 32;
+__device__ __forceinline__ uint64_t more_columns(uint32_t tile) {
+  return (uint64_t)(256 >> 4 | 1u << 14) << 32 | (tile >> 4 | (128u >> 4) << 16);
+}
+__device__ __forceinline__ uint32_t more_at(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
 
 // One thread of a converged warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
@@ -109,23 +118,24 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
-// d [128 x 128] = A B^T over the first `steps` x 16 columns of both tiles (of
+// d [128 x kN] = A B^T over the first `steps` x 16 columns of both tiles (of
 // kSteps at most).
-template <int kSteps>
+// B has kN rows.
+template <int kSteps, int kN = kRows>
 __device__ __forceinline__ void product_of_rows(uint32_t d, uint32_t a, uint32_t b, int steps) {
-  constexpr uint32_t id = idesc(kRows, false);
+  constexpr uint32_t id = idesc(kN, false);
 #pragma unroll
   for (int k = 0; k < kSteps; ++k)
-    if (k < steps) mma_ss(d, desc(a + column_step(k)), desc(b + column_step(k)), id, k > 0);
+    if (k < steps)
+      mma_ss(d, desc(a + column_step(k)), desc(b + column_step(k, kN)), id, k > 0);
 }
-// d [128 x n] (+)= P B over the 128 rows of B; P is in TMEM, its columns from 64
-// on kSecond columns behind the first.
-template <int kSecond>
+// d [128 x n] (+)= P B over rows 64 half .. of B; these columns of P are in TMEM
+// from p on.
 __device__ __forceinline__ void product_of_p(uint32_t d, uint32_t p, uint32_t b, uint32_t id,
-                                             bool add) {
+                                             int half, bool add) {
 #pragma unroll
-  for (int k = 0; k < kRows / 16; ++k)
-    mma_ts(d, p + (k >> 2) * kSecond + (k & 3) * 8, desc(b + row_step(k)), id, add || k > 0);
+  for (int k = 0; k < 4; ++k)
+    mma_ts(d, p + 8 * k, desc(b + row_step(4 * half + k)), id, add || k > 0);
 }
 
 // 32 columns of this thread's TMEM lane; the values are there after ld_wait.
@@ -168,6 +178,14 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -193,8 +211,7 @@ __device__ __forceinline__ void drain(uint64_t* bar) {
   }
 }
 
-// Registers of the calling warpgroup (of the launch's 168 a thread and three
-// warpgroups: 72 + 2 x 216).
+// Registers of the calling warpgroup: together no more than the launch's.
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -210,33 +227,38 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-// Tile of 128 rows of head h, chunk by chunk; `bar` expects its bytes.
-template <int kChunks>
+// Tile of kN rows of head h, chunk by chunk; `bar` expects its bytes.
+template <int kChunks, int kN = kRows>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
                                           int h, int row) {
 #pragma unroll
   for (int c = 0; c < kChunks; ++c)
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst) + c * kChunkBytes),
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst) + c * kN * 128),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c * kChunk), "r"(h), "r"(row), "r"(saddr(bar))
         : "memory");
 }
 
-// Zeros in rows `first` .. 127 of a tile, by one warp: rows behind a sequence's
+// Zeros in rows `first` .. kN - 1 of a tile, by one warp: rows behind a sequence's
 // last hold another sequence's values, and 0 times those need not be 0.
-template <int kChunks>
+template <int kChunks, int kN = kRows>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int first) {
   const int lane = threadIdx.x & 31;
-  for (int i = lane; i < (kRows - first) * kChunks * 8; i += 32) {
+  for (int i = lane; i < (kN - first) * kChunks * 8; i += 32) {
     const int piece = i & 7, rest = i >> 3, c = rest % kChunks, r = first + rest / kChunks;
-    *reinterpret_cast<uint4*>(tile + c * kChunkBytes + r * 128 + piece * 16) =
+    *reinterpret_cast<uint4*>(tile + c * kN * 128 + r * 128 + piece * 16) =
         make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
@@ -251,7 +273,7 @@ inline bool tma_heads(const Heads& x, int64_t T, int64_t H) {
   const auto stride = [](int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 39); };
   return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && stride(x.token, T) && stride(x.head, H);
 }
-// Map of x with boxes of 128 tokens x 1 head x 64 columns, zeros outside.
-bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D);
+// Map of x with boxes of `rows` tokens x 1 head x 64 columns, zeros outside.
+bool heads_map(CUtensorMap* map, const Heads& x, int64_t T, int64_t H, int64_t D, int rows);
 
 }  // namespace hlq
