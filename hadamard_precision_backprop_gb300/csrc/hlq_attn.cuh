@@ -19,6 +19,10 @@ struct AttnTile {
   int row0;            // the tile's first row within the sequence
 };
 
+__device__ __forceinline__ uint32_t operator/(uint32_t n, const Div& d) {
+  return (uint32_t)((uint64_t)n * d.m >> d.s);
+}
+
 // Rows [lo, hi) of sequence b; `bad` where the offsets are not in order (the
 // rows are then cut to those that exist).
 __device__ __forceinline__ int2 seq_rows(const int32_t* seqs, int b, int T, bool& bad) {
@@ -29,7 +33,7 @@ __device__ __forceinline__ int2 seq_rows(const int32_t* seqs, int b, int T, bool
   return make_int2(lo, hi);
 }
 
-// Tile t of `rows` queries (keys with kKeys) among the tiles of all sequences,
+// Tile t of `rows` queries (keys with kKeys; 64 or 128 or so) among the tiles of all sequences,
 // the last tile of a sequence first (with a causal mask it is the longest, if
 // they go by queries).  Returns -1, or where the tiles are used up the number
 // of tiles past the last one.  A whole warp calls it.
@@ -37,15 +41,13 @@ __device__ __forceinline__ int2 seq_rows(const int32_t* seqs, int b, int T, bool
 // With sequences of one length the tiles of all sequences that have the same
 // rank follow each other; else each lane looks at a sequence of its own and
 // the warp adds up their tiles, 32 sequences at a time.
-template <bool kKeys>
-__device__ __forceinline__ int find_tile(const Attn& p, int rows, int t, AttnTile& o) {
+template <bool kKeys, int rows>
+__device__ __forceinline__ int find_tile(const Attn& p, int t, AttnTile& o) {
   const int T = kKeys ? p.Tk : p.Tq;
   if (!p.seqs_q) {
-    const int Lq = p.Tq / p.batch, Lk = p.Tk / p.batch, L = kKeys ? Lk : Lq;
-    const int per = (L + rows - 1) / rows;
-    const int rank = t / p.batch, b = t - rank * p.batch;
-    if (rank >= per) return t - per * p.batch;
-    o = {b * Lq, Lq, b * Lk, Lk, (kKeys ? rank : per - 1 - rank) * rows};
+    const int per = ((kKeys ? p.Lk : p.Lq) + rows - 1) / rows;
+    const int rank = (int)((uint32_t)t / p.by_batch), b = t - rank * p.batch;
+    o = {b * p.Lq, p.Lq, b * p.Lk, p.Lk, (kKeys ? rank : per - 1 - rank) * rows};
     return -1;
   }
   const int32_t* seqs = kKeys ? p.seqs_k : p.seqs_q;

@@ -160,6 +160,9 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
                                                : make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 1) alloc(&bar.tmem, C::kColumns);
+  if (threadIdx.x == 64) {
+    prefetch(&mq), prefetch(&mk), prefetch(&mv), prefetch(&mg);
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -167,9 +170,10 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
   pdl_trigger();
   pdl_wait();
 
-  const int hk = blockIdx.x % p.Hk, group = p.Hq / p.Hk;
+  const uint32_t tile = blockIdx.x / p.by_hk;
+  const int hk = (int)(blockIdx.x - tile * p.Hk), group = p.group;
   AttnTile t;
-  const int past = find_tile<true>(p, kRows, blockIdx.x / p.Hk, t);
+  const int past = find_tile<true, kRows>(p, (int)tile, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
     return wait_for(b, phase, abort_flag, p.status);
   };
@@ -477,6 +481,9 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
     fence_proxy_async_smem();
   }
   if (warp == 1) alloc(&bar.tmem, C::kColumns);
+  if (threadIdx.x == 64) {
+    prefetch(&mq), prefetch(&mk), prefetch(&mv), prefetch(&mg);
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -484,9 +491,10 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
   pdl_trigger();
   pdl_wait();
 
-  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  const uint32_t tile = blockIdx.x / p.by_hq;
+  const int h = (int)(blockIdx.x - tile * p.Hq), hk = (int)((uint32_t)h / p.by_group);
   AttnTile t;
-  const int past = find_tile<false>(p, kRows, blockIdx.x / p.Hq, t);
+  const int past = find_tile<false, kRows>(p, (int)tile, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
     return wait_for(b, phase, abort_flag, p.status);
   };

@@ -19,6 +19,7 @@
 #include <cstring>
 
 #include "hlq_attn_tc.cuh"
+#include "hlq_host.h"
 #include "hlq_rows.cuh"
 
 namespace hlq {
@@ -26,16 +27,21 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
 constexpr float kRise = 8.f;
 
-template <int DP>
+// kQ tiles of queries in a CTA.  Two for one CTA an SM; one for two CTAs an SM,
+// which hide each other's beginning and end but bring the keys' tiles into
+// shared memory for each tile of queries.
+template <int DP, int kQ>
 struct FwdCfg {
   static constexpr int kChunks = DP / kChunk;
   static constexpr uint32_t kTile = kChunks * kChunkBytes;
-  static constexpr int kStages = DP == 64 ? 4 : 2;  // of K and of V each
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * kStages) * kTile + 256;
-  static constexpr uint32_t kO = 256, kColumns = 512;
+  static constexpr int kStages = (kQ == 2 ? 2 : 1) * (DP == 64 ? 2 : 1);  // of K and of V each
+  static constexpr size_t kSmem = 1024 + (size_t)(kQ + 2 * kStages) * kTile + 256;
+  static constexpr uint32_t kO = kQ * kRows, kColumns = kQ * 256;
+  static constexpr int kThreads = 128 * (1 + kQ), kCtas = 3 - kQ;
+  // of the launch's 168 (384 threads) or 128 (256 threads) a thread
+  static constexpr int kFewer = kQ == 2 ? 72 : 56, kMore = kQ == 2 ? 216 : 200;
 };
 
 struct FwdBars {
@@ -46,22 +52,22 @@ struct FwdBars {
 };
 static_assert(sizeof(FwdBars) <= 256, "barriers fit their 256 bytes");
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DP, int kQ>
+__global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCtas)
     attn_fwd_tc_kernel(const Attn p, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, int wide_out) {
-  using C = FwdCfg<DP>;
+  using C = FwdCfg<DP, kQ>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t *sq = smem, *sk = sq + 2 * C::kTile, *sv = sk + C::kStages * C::kTile;
+  uint8_t *sq = smem, *sk = sq + kQ * C::kTile, *sv = sk + C::kStages * C::kTile;
   FwdBars& bar = *reinterpret_cast<FwdBars*>(sv + C::kStages * C::kTile);
   volatile int* abort_flag = &bar.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < kQ; ++g) {
       mbar_init(&bar.q_full[g], 1);
       mbar_init(&bar.s_full[g], 1);
       mbar_init(&bar.p_full[g][0], 4);
@@ -71,9 +77,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bar.k_full[s], 1);
-      mbar_init(&bar.k_empty[s], 2);
+      mbar_init(&bar.k_empty[s], kQ);
       mbar_init(&bar.v_full[s], 1);
-      mbar_init(&bar.v_empty[s], 2);
+      mbar_init(&bar.v_empty[s], kQ);
     }
     mbar_init(&bar.v_last, 1);
     mbar_init(&bar.v_clear, 1);
@@ -82,6 +88,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 1) alloc(&bar.tmem, C::kColumns);
+  if (threadIdx.x == 64) {
+    prefetch(&mq), prefetch(&mk), prefetch(&mv);
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -89,16 +98,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   pdl_wait();
 
-  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  const uint32_t tile = blockIdx.x / p.by_hq;
+  const int h = (int)(blockIdx.x - tile * p.Hq), hk = (int)((uint32_t)h / p.by_group);
   AttnTile t;
-  const int past = find_tile<false>(p, 2 * kRows, blockIdx.x / p.Hq, t);
+  const int past = find_tile<false, kQ * kRows>(p, (int)tile, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
     return wait_for(b, phase, abort_flag, p.status);
   };
-  // tiles of keys that the two tiles of queries see
+  // tiles of keys that the tiles of queries see
   int tiles[2] = {0, 0};
   if (past < 0)
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < kQ; ++g) {
       const int last = min(t.row0 + (g + 1) * kRows, t.nq) - 1;
       if (last >= t.row0 + g * kRows) tiles[g] = (keys_of(p, t, last) + kRows - 1) / kRows;
     }
@@ -107,13 +117,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rest = n > 0 && t.nk < n * kRows ? t.nk - (n - 1) * kRows : 0;
 
   if (past >= 0) {
-    outside_rows<false>(p, 2 * kRows, past, threadIdx.x, kThreads, [&](int row) {
+    outside_rows<false>(p, kQ * kRows, past, threadIdx.x, C::kThreads, [&](int row) {
       p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
       for (int d = 0; d < p.D; ++d)
         store_elem(p.out.p, true, row * p.out.token + h * p.out.head + d, 0.f);
     });
   } else if (warp < 4) {
-   fewer_registers<72>();
+   fewer_registers<C::kFewer>();
    if (warp == 0) {
     if (lane == 0 && n > 0) {
       int k_done = 0, v_done = 0, q_done = 0, last_done = 0;
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_drain(&bar.v_last, 1, last_done);
       }
     }
-   } else if (warp != 2) {  // the whole warp, of which one thread issues
+   } else if (warp == 1 || (kQ == 2 && warp == 3)) {  // the whole warp, of which one thread issues
       const int g = warp >> 1;
       const int steps = (p.D + 15) / 16;
       const uint32_t id = idesc(16 * steps, true);
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    }
   } else {
-    more_registers<216>();
+    more_registers<C::kMore>();
     const int g = (warp - 4) >> 2;
     const int row = t.row0 + g * kRows + (warp & 3) * 32 + lane;  // of the sequence
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // 32 lanes a warp, in bits 16-31
@@ -336,19 +346,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int DP>
+template <int DP, int kQ>
 cudaError_t launch(const Attn& p, cudaStream_t st) {
-  using C = FwdCfg<DP>;
-  const int64_t grid = most_tiles(p, false, 2 * kRows) * p.Hq;
+  using C = FwdCfg<DP, kQ>;
+  const int64_t grid = most_tiles(p, false, kQ * kRows) * p.Hq;
   if (grid == 0) return cudaSuccess;
   CUtensorMap mq, mk, mv;
   if (!heads_map(&mq, p.q, p.Tq, p.Hq, p.D, kRows) || !heads_map(&mk, p.k, p.Tk, p.Hk, p.D, kRows) ||
       !heads_map(&mv, p.v, p.Tk, p.Hk, p.D, kRows))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<attn_fwd_tc_kernel<DP>>(C::kSmem);
+  cudaError_t e = allow_smem<attn_fwd_tc_kernel<DP, kQ>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int wide_out = p.D % 8 == 0 && tma_heads(p.out, p.Tq, p.Hq);
-  return launch_pdl(attn_fwd_tc_kernel<DP>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, p,
+  return launch_pdl(attn_fwd_tc_kernel<DP, kQ>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, st, p,
                     mq, mk, mv, wide_out);
 }
 
@@ -388,7 +398,15 @@ bool attn_tc(const Attn& p) {
 }
 
 cudaError_t launch_attn_tc(const Attn& p, cudaStream_t st) {
-  return p.D <= 64 ? launch<64>(p, st) : launch<128>(p, st);
+  // Two tiles of queries in a CTA where sequences are long and there are enough
+  // of them: one sequence of 16384 (4 heads of 128, causal) 188 us against 205
+  // with one tile, 16 of 1024 (16 heads of 64) 104 against 107; but 32 of 512 (16
+  // heads of 128) 90 against 84, 64 of 100 (12 heads of 64) 25 against 16, one of
+  // 2048 (4 heads of 128) 36 against 30.
+  const int64_t pairs = most_tiles(p, false, 2 * kRows) * p.Hq;
+  if (p.Tk / p.batch >= 1024 && pairs >= device_sm_count())
+    return p.D <= 64 ? launch<64, 2>(p, st) : launch<128, 2>(p, st);
+  return p.D <= 64 ? launch<64, 1>(p, st) : launch<128, 1>(p, st);
 }
 
 }  // namespace hlq

@@ -12,7 +12,7 @@
 // One CTA of 16 x 16 threads has a tile of rows (queries; keys in the keys'
 // pass) in shared memory and goes over tiles of the other side.  Thread
 // (ty, tx) has rows ty RM .., columns tx, tx + 16, .. of a tile of scores and
-// columns 4 tx + 64 c .. of a row of results, so that a row belongs to half a
+// columns 4 tx + 64 c .. (2 tx .. of 32) of a row of results, so that a row belongs to half a
 // warp: maxima and sums are shuffles, and the probabilities go through shared
 // memory without a barrier.  The backward pass goes over the keys' tiles (g_k,
 // g_v) and over the queries' tiles (g_q) in kernels of their own: two products
@@ -27,25 +27,46 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Tile sizes by head size: rows of the CTA's own side and of the other side.
-// 79 KB (D <= 128) and 108 KB (D <= 256) of shared memory forward, 120 and
-// 142 KB backward.
+// Tile sizes by head size: rows of the CTA's own side and of the other side.  A
+// CTA takes 19, 70, 78 or 108 KB of shared memory forward and 23, 87, 110 or 142
+// KB backward (D up to 32, 64, 128, 256), two of them an SM but for the last.
 template <int DP>
 struct Cfg {
   static constexpr int kLd = DP + 4;  // floats: rows 4 banks apart
-  static constexpr int kBM = DP <= 128 ? 64 : 32;
-  static constexpr int kBN = DP <= 64 ? 64 : 32;
+  static constexpr int kBM = DP == 64 || DP == 128 ? 64 : 32;
+  static constexpr int kBN = DP == 64 ? 64 : 32;
   static constexpr int kRM = kBM / 16, kRN = kBN / 16, kRD = DP / 16;
+  static constexpr int kVec = DP == 32 ? 2 : 4;  // columns of a result together
   static constexpr int kLdP = kBN + 4;
   static constexpr size_t kFwd = 4 * (size_t)(kBM * kLd + 2 * kBN * kLd + kBM * kLdP);
-  static constexpr size_t kBwd = 4 * (size_t)(2 * kBM * kLd + 2 * kBN * kLd + 2 * kBM * kLdP);
+  static constexpr size_t kBwd = 4 * (size_t)(2 * kBM * kLd + 2 * kBN * kLd + kBM * kLdP);
+  static constexpr int kCtas = DP <= 128 ? 2 : 1;
 };
 
-// Rows row0 .. row0 + n of head h as fp32, zeros in the rest of the tile.
+// Rows row0 .. row0 + n of head h as fp32, zeros in the rest of the tile.  By
+// four where heads begin on 16-byte boundaries and are of whole fours.
 template <int DP>
 __device__ __forceinline__ void load_tile(float* dst, const Heads& x, bool bf16, int64_t row0,
                                           int n, int rows, int h, int D) {
   const int64_t at = row0 * x.token + (int64_t)h * x.head;
+  if (D % 4 == 0 && reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.token % 4 == 0 &&
+      x.head % 4 == 0) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < rows * DP / 4; i += kThreads) {
+      const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < n && d < D) {
+        if (bf16) {
+          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x.p) + at + r * x.token + d);
+          v = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
+        } else {
+          v = *reinterpret_cast<const float4*>(static_cast<const float*>(x.p) + at + r * x.token + d);
+        }
+      }
+      *reinterpret_cast<float4*>(dst + r * Cfg<DP>::kLd + d) = v;
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
     const int r = i / DP, d = i % DP;
     dst[r * Cfg<DP>::kLd + d] =
@@ -80,11 +101,11 @@ __device__ __forceinline__ void rows_by_rows(const float* a, const float* b, int
   }
 }
 
-// acc[i][4 c + e] += sum_j P[row i][j] B[j][64 c + 4 tx + e].
+// acc[i][V c + e] += sum_j P[row i][j] B[j][16 V c + V tx + e], V = kVec.
 template <int DP, int RM, int BN>
 __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, int ty, int tx,
                                                 float (&acc)[RM][Cfg<DP>::kRD]) {
-  constexpr int kLd = Cfg<DP>::kLd, kLdP = BN + 4;
+  constexpr int kLd = Cfg<DP>::kLd, kLdP = BN + 4, kVec = Cfg<DP>::kVec;
 #pragma unroll 2
   for (int j = 0; j < BN; j += 4) {
     float p[RM][4];
@@ -96,15 +117,21 @@ __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, 
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-      for (int c = 0; c < DP / 64; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(b + (j + jj) * kLd + 64 * c + 4 * tx);
-#pragma unroll
-        for (int i = 0; i < RM; ++i) {
-          acc[i][4 * c + 0] = fmaf(p[i][jj], v.x, acc[i][4 * c + 0]);
-          acc[i][4 * c + 1] = fmaf(p[i][jj], v.y, acc[i][4 * c + 1]);
-          acc[i][4 * c + 2] = fmaf(p[i][jj], v.z, acc[i][4 * c + 2]);
-          acc[i][4 * c + 3] = fmaf(p[i][jj], v.w, acc[i][4 * c + 3]);
+      for (int c = 0; c < Cfg<DP>::kRD / kVec; ++c) {
+        const float* at = b + (j + jj) * kLd + 16 * kVec * c + kVec * tx;
+        float v[kVec];
+        if constexpr (kVec == 4) {
+          const float4 w = *reinterpret_cast<const float4*>(at);
+          v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        } else {
+          const float2 w = *reinterpret_cast<const float2*>(at);
+          v[0] = w.x, v[1] = w.y;
         }
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+          for (int e = 0; e < kVec; ++e)
+            acc[i][kVec * c + e] = fmaf(p[i][jj], v[e], acc[i][kVec * c + e]);
       }
   }
 }
@@ -120,7 +147,8 @@ __device__ __forceinline__ void store_rows(const Heads& x, bool bf16, int64_t ro
     const int64_t at = (row0 + r) * x.token + (int64_t)h * x.head;
 #pragma unroll
     for (int c = 0; c < Cfg<DP>::kRD; ++c) {
-      const int d = 64 * (c / 4) + 4 * tx + c % 4;
+      constexpr int kVec = Cfg<DP>::kVec;
+      const int d = 16 * kVec * (c / kVec) + kVec * tx + c % kVec;
       if (d < D) store_elem(x.p, bf16, at + d, factor * acc[i][c]);
     }
   }
@@ -146,16 +174,17 @@ __device__ __forceinline__ float half_warp_sum(float v) {
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const Attn p) {
+__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel(const Attn p) {
   using C = Cfg<DP>;
   constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
   extern __shared__ float smem[];
   float *sq = smem, *sk = sq + BM * C::kLd, *sv = sk + BN * C::kLd, *sp = sv + BN * C::kLd;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   pdl_wait();
-  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  const uint32_t tile = blockIdx.x / p.by_hq;
+  const int h = (int)(blockIdx.x - tile * p.Hq), hk = (int)((uint32_t)h / p.by_group);
   AttnTile t;
-  const int past = find_tile<false>(p, BM, blockIdx.x / p.Hq, t);
+  const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {  // rows of no sequence
     outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
       p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
@@ -306,17 +335,18 @@ __global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const Attn p) {
 // g_k and g_v of a tile of keys: over the query heads that share the key head
 // and the tiles of queries that see it.  Rows are keys, columns queries.
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_bwd_keys_simt_kernel(const Attn p) {
+__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_bwd_keys_simt_kernel(const Attn p) {
   using C = Cfg<DP>;
   constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
   extern __shared__ float smem[];
   float *sk = smem, *sv = sk + BM * C::kLd, *sq = sv + BM * C::kLd, *sg = sq + BN * C::kLd,
-        *sp = sg + BN * C::kLd, *sd = sp + BM * C::kLdP;
+        *sp = sg + BN * C::kLd;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   pdl_wait();
-  const int hk = blockIdx.x % p.Hk, group = p.Hq / p.Hk;
+  const uint32_t tile = blockIdx.x / p.by_hk;
+  const int hk = (int)(blockIdx.x - tile * p.Hk), group = p.group;
   AttnTile t;
-  const int past = find_tile<true>(p, BM, blockIdx.x / p.Hk, t);
+  const int past = find_tile<true, BM>(p, (int)tile, t);
   if (past >= 0) {
     outside_rows<true>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
       for (int d = 0; d < p.D; ++d) {
@@ -357,13 +387,18 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_keys_simt_kernel(const Attn
         for (int r = 0; r < RM; ++r) {
           const float e = ty * RM + r < sees ? exp2f(s[r][j] * c2 - lse2) : 0.f;
           sp[(ty * RM + r) * C::kLdP + tx + 16 * j] = e;
-          sd[(ty * RM + r) * C::kLdP + tx + 16 * j] =
-              ty * RM + r < sees ? e * (dp[r][j] - delta) : 0.f;
+          dp[r][j] = ty * RM + r < sees ? e * (dp[r][j] - delta) : 0.f;
         }
       }
       __syncwarp();
       rows_by_columns<DP, RM, BN>(sp, sg, ty, tx, gv);
-      rows_by_columns<DP, RM, BN>(sd, sq, ty, tx, gk);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < RN; ++j)
+#pragma unroll
+        for (int r = 0; r < RM; ++r) sp[(ty * RM + r) * C::kLdP + tx + 16 * j] = dp[r][j];
+      __syncwarp();
+      rows_by_columns<DP, RM, BN>(sp, sq, ty, tx, gk);
       __syncwarp();
     }
   store_rows<DP, RM>(p.gk, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, p.scale, gk);
@@ -372,7 +407,7 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_keys_simt_kernel(const Attn
 
 // g_q of a tile of queries.
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_bwd_queries_simt_kernel(const Attn p) {
+__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_bwd_queries_simt_kernel(const Attn p) {
   using C = Cfg<DP>;
   constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
   extern __shared__ float smem[];
@@ -380,9 +415,10 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_queries_simt_kernel(const A
         *sd = sv + BN * C::kLd;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   pdl_wait();
-  const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
+  const uint32_t tile = blockIdx.x / p.by_hq;
+  const int h = (int)(blockIdx.x - tile * p.Hq), hk = (int)((uint32_t)h / p.by_group);
   AttnTile t;
-  const int past = find_tile<false>(p, BM, blockIdx.x / p.Hq, t);
+  const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {
     outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
       for (int d = 0; d < p.D; ++d)
@@ -440,6 +476,8 @@ cudaError_t launch(const Attn& p, bool keys, int rows, size_t smem, cudaStream_t
 }  // namespace
 
 cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st) {
+  if (p.D <= 32)
+    return launch<attn_fwd_simt_kernel<32>>(p, false, Cfg<32>::kBM, Cfg<32>::kFwd, st);
   if (p.D <= 64) return launch<attn_fwd_simt_kernel<64>>(p, false, Cfg<64>::kBM, Cfg<64>::kFwd, st);
   if (p.D <= 128)
     return launch<attn_fwd_simt_kernel<128>>(p, false, Cfg<128>::kBM, Cfg<128>::kFwd, st);
@@ -468,6 +506,8 @@ cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st) {
 }
 
 cudaError_t launch_attn_bwd_keys_simt(const Attn& p, cudaStream_t st) {
+  if (p.D <= 32)
+    return launch<attn_bwd_keys_simt_kernel<32>>(p, true, Cfg<32>::kBM, Cfg<32>::kBwd, st);
   if (p.D <= 64)
     return launch<attn_bwd_keys_simt_kernel<64>>(p, true, Cfg<64>::kBM, Cfg<64>::kBwd, st);
   if (p.D <= 128)
@@ -476,6 +516,8 @@ cudaError_t launch_attn_bwd_keys_simt(const Attn& p, cudaStream_t st) {
 }
 
 cudaError_t launch_attn_bwd_queries_simt(const Attn& p, cudaStream_t st) {
+  if (p.D <= 32)
+    return launch<attn_bwd_queries_simt_kernel<32>>(p, false, Cfg<32>::kBM, Cfg<32>::kBwd, st);
   if (p.D <= 64)
     return launch<attn_bwd_queries_simt_kernel<64>>(p, false, Cfg<64>::kBM, Cfg<64>::kBwd, st);
   if (p.D <= 128)

@@ -26,6 +26,9 @@ constexpr int kRows = 128;        // rows of a tile
 constexpr int kChunk = 64;        // columns of a chunk
 constexpr uint32_t kChunkBytes = kRows * 128;
 
+__device__ __forceinline__ void prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -119,8 +122,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 
 // d [128 x kN] = A B^T over the first `steps` x 16 columns of both tiles (of
-// kSteps at most).
-// B has kN rows.
+// kSteps at most).  B has kN rows.
 template <int kSteps, int kN = kRows>
 __device__ __forceinline__ void product_of_rows(uint32_t d, uint32_t a, uint32_t b, int steps) {
   constexpr uint32_t id = idesc(kN, false);

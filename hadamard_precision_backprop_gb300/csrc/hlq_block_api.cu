@@ -76,6 +76,9 @@ Attn attn_of(const hlq_heads& q, const hlq_heads& k, const hlq_heads& v, int dt,
   p.seqs_q = seqs, p.seqs_k = seqs_k ? seqs_k : seqs;
   p.batch = (int)batch, p.Tq = (int)Tq, p.Tk = (int)Tk, p.Hq = (int)Hq, p.Hk = (int)Hk;
   p.D = (int)D;
+  p.Lq = (int)(Tq / batch), p.Lk = (int)(Tk / batch), p.group = (int)(Hq / Hk);
+  p.by_batch = div_by((uint32_t)batch), p.by_group = div_by((uint32_t)p.group);
+  p.by_hq = div_by((uint32_t)Hq), p.by_hk = div_by((uint32_t)Hk);
   p.causal = causal != 0;
   p.scale = scale;
   p.bf16 = dt == HLQ_BF16;

@@ -254,6 +254,16 @@ struct Heads {
   void* p;
   int64_t token, head;
 };
+// Division of 0 <= n < 2^31 by d >= 1: with 2^s >= d, m = ceil(2^(31 + s) / d) is
+// below 2^32 and n m / 2^(31 + s) is off by less than n / 2^31 / d < 1 / d.
+struct Div {
+  uint32_t d, m, s;
+};
+inline Div div_by(uint32_t d) {
+  uint32_t s = 0;
+  while (((uint64_t)1 << s) < d) ++s;
+  return {d, (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), 31 + s};
+}
 // One call of attention or of its backward pass.
 struct Attn {
   Heads q, k, v, out;         // out: written forward, read backward
@@ -263,6 +273,8 @@ struct Attn {
   Heads gout16;               // backward, workspace: g_out as bf16; p null where g_out itself is
   const int32_t *seqs_q, *seqs_k;  // both null: sequences of one length
   int batch, Tq, Tk, Hq, Hk, D;
+  int Lq, Lk, group;          // of sequences of one length; Hq / Hk
+  Div by_batch, by_hq, by_hk, by_group;
   int causal;
   float scale;
   bool bf16, gout_bf16, g_bf16;
