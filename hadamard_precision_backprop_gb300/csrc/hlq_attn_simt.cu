@@ -74,37 +74,46 @@ __device__ __forceinline__ void load_tile(float* dst, const Heads& x, bool bf16,
   }
 }
 
-// acc[i][j] = A[row i] . B[row j], rows as in the note at the top.
+// acc[i][j] = A[row i] . B[row j], rows as in the note at the top.  Two fp32 in
+// one instruction: the sums of the even and of the odd columns, added at the end.
 template <int DP, int RM, int RN>
 __device__ __forceinline__ void rows_by_rows(const float* a, const float* b, int ty, int tx,
                                              float (&acc)[RM][RN]) {
   constexpr int kLd = Cfg<DP>::kLd;
+  F2 two[RM][RN];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int j = 0; j < RN; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < RN; ++j) two[i][j] = f2(0.f);
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    float4 u[RM], w[RN];
+    ulonglong2 u[RM], w[RN];
 #pragma unroll
     for (int i = 0; i < RM; ++i)
-      u[i] = *reinterpret_cast<const float4*>(a + (ty * RM + i) * kLd + d);
+      u[i] = *reinterpret_cast<const ulonglong2*>(a + (ty * RM + i) * kLd + d);
 #pragma unroll
     for (int j = 0; j < RN; ++j)
-      w[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * kLd + d);
+      w[j] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * j) * kLd + d);
 #pragma unroll
     for (int i = 0; i < RM; ++i)
 #pragma unroll
       for (int j = 0; j < RN; ++j)
-        acc[i][j] = fmaf(u[i].w, w[j].w,
-                         fmaf(u[i].z, w[j].z, fmaf(u[i].y, w[j].y, fmaf(u[i].x, w[j].x, acc[i][j]))));
+        two[i][j] = fma2({u[i].y}, {w[j].y}, fma2({u[i].x}, {w[j].x}, two[i][j]));
   }
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) {
+      const float2 s = split(two[i][j]);
+      acc[i][j] = s.x + s.y;
+    }
 }
 
-// acc[i][V c + e] += sum_j P[row i][j] B[j][16 V c + V tx + e], V = kVec.
+// acc[i][V c + e] += sum_j P[row i][j] B[j][16 V c + V tx + e], V = kVec; acc by
+// pairs of columns.
 template <int DP, int RM, int BN>
 __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, int ty, int tx,
-                                                float (&acc)[RM][Cfg<DP>::kRD]) {
+                                                F2 (&acc)[RM][Cfg<DP>::kRD / 2]) {
   constexpr int kLd = Cfg<DP>::kLd, kLdP = BN + 4, kVec = Cfg<DP>::kVec;
 #pragma unroll 2
   for (int j = 0; j < BN; j += 4) {
@@ -119,19 +128,18 @@ __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, 
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::kRD / kVec; ++c) {
         const float* at = b + (j + jj) * kLd + 16 * kVec * c + kVec * tx;
-        float v[kVec];
+        F2 v[kVec / 2];
         if constexpr (kVec == 4) {
-          const float4 w = *reinterpret_cast<const float4*>(at);
-          v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+          const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(at);
+          v[0].b = w.x, v[1].b = w.y;
         } else {
-          const float2 w = *reinterpret_cast<const float2*>(at);
-          v[0] = w.x, v[1] = w.y;
+          v[0].b = *reinterpret_cast<const unsigned long long*>(at);
         }
 #pragma unroll
         for (int i = 0; i < RM; ++i)
 #pragma unroll
-          for (int e = 0; e < kVec; ++e)
-            acc[i][kVec * c + e] = fmaf(p[i][jj], v[e], acc[i][kVec * c + e]);
+          for (int e = 0; e < kVec / 2; ++e)
+            acc[i][kVec / 2 * c + e] = fma2(f2(p[i][jj]), v[e], acc[i][kVec / 2 * c + e]);
       }
   }
 }
@@ -139,27 +147,29 @@ __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, 
 template <int DP, int RM>
 __device__ __forceinline__ void store_rows(const Heads& x, bool bf16, int64_t row0, int n, int h,
                                            int D, int ty, int tx, float factor,
-                                           const float (&acc)[RM][Cfg<DP>::kRD]) {
+                                           const F2 (&acc)[RM][Cfg<DP>::kRD / 2]) {
+  constexpr int kVec = Cfg<DP>::kVec;
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
     const int r = ty * RM + i;
     if (r >= n) continue;
     const int64_t at = (row0 + r) * x.token + (int64_t)h * x.head;
 #pragma unroll
-    for (int c = 0; c < Cfg<DP>::kRD; ++c) {
-      constexpr int kVec = Cfg<DP>::kVec;
+    for (int c = 0; c < Cfg<DP>::kRD; c += 2) {
       const int d = 16 * kVec * (c / kVec) + kVec * tx + c % kVec;
-      if (d < D) store_elem(x.p, bf16, at + d, factor * acc[i][c]);
+      const float2 v = split(acc[i][c / 2]);
+      if (d < D) store_elem(x.p, bf16, at + d, factor * v.x);
+      if (d + 1 < D) store_elem(x.p, bf16, at + d + 1, factor * v.y);
     }
   }
 }
 
 template <int DP, int RM>
-__device__ __forceinline__ void clear(float (&acc)[RM][Cfg<DP>::kRD]) {
+__device__ __forceinline__ void clear(F2 (&acc)[RM][Cfg<DP>::kRD / 2]) {
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int c = 0; c < Cfg<DP>::kRD; ++c) acc[i][c] = 0.f;
+    for (int c = 0; c < Cfg<DP>::kRD / 2; ++c) acc[i][c] = f2(0.f);
 }
 
 __device__ __forceinline__ float half_warp_max(float v) {
@@ -196,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
   const int n = min(BM, t.nq - t.row0);
   const int keys = keys_of(p, t, t.row0 + n - 1);  // the last row sees the most
   load_tile<DP>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
-  float m[RM], l[RM], acc[RM][C::kRD];
+  float m[RM], l[RM];
+  F2 acc[RM][C::kRD / 2];
   clear<DP, RM>(acc);
 #pragma unroll
   for (int i = 0; i < RM; ++i) m[i] = -INFINITY, l[i] = 0.f;
@@ -231,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
       }
       l[i] = l[i] * keep + half_warp_sum(sum);
 #pragma unroll
-      for (int c = 0; c < C::kRD; ++c) acc[i][c] *= keep;
+      for (int c = 0; c < C::kRD / 2; ++c) acc[i][c] = acc[i][c] * f2(keep);
     }
     __syncwarp();
     rows_by_columns<DP, RM, BN>(sp, sv, ty, tx, acc);
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
   for (int i = 0; i < RM; ++i) {
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // an empty row is zeros
 #pragma unroll
-    for (int c = 0; c < C::kRD; ++c) acc[i][c] *= inv;
+    for (int c = 0; c < C::kRD / 2; ++c) acc[i][c] = acc[i][c] * f2(inv);
     const int r = ty * RM + i;
     if (tx == 0 && r < n)
       p.lse[(int64_t)(t.q0 + t.row0 + r) * p.Hq + h] =
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_bwd_keys_simt_k
   const int n = min(BM, t.nk - t.row0);
   load_tile<DP>(sk, p.k, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
   load_tile<DP>(sv, p.v, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
-  float gk[RM][C::kRD], gv[RM][C::kRD];
+  F2 gk[RM][C::kRD / 2], gv[RM][C::kRD / 2];
   clear<DP, RM>(gk);
   clear<DP, RM>(gv);
   // the first query that sees the tile's first key
@@ -430,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_bwd_queries_sim
   const int keys = keys_of(p, t, t.row0 + n - 1);
   load_tile<DP>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
   load_tile<DP>(sg, p.gout, p.gout_bf16, t.q0 + t.row0, n, BM, h, p.D);
-  float gq[RM][C::kRD], lse2[RM], delta[RM];
+  F2 gq[RM][C::kRD / 2];
+  float lse2[RM], delta[RM];
   clear<DP, RM>(gq);
 #pragma unroll
   for (int r = 0; r < RM; ++r) {
