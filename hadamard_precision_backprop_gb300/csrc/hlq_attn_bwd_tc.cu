@@ -60,37 +60,6 @@ __device__ __forceinline__ void product_of_parts(uint32_t d, uint32_t p, uint32_
     mma_ts(d, p + (k >> 1) * 32 + (k & 1) * 8, desc(b + row_step(k)), id, add || k > 0);
 }
 
-// 32 columns of a row of a result from TMEM, times `factor`; zeros with `zero`.
-// With `wide` rows are of whole 16 bytes.
-__device__ __forceinline__ void store_columns(const Heads& x, bool bf16, int wide, int64_t row,
-                                              int h, int c0, int D, bool there, uint32_t acc,
-                                              bool zero, float factor) {
-  const int64_t at = row * x.token + (int64_t)h * x.head + c0;
-  uint32_t o[32];
-  if (zero) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = 0;
-  } else {
-    __syncwarp();
-    ld32(acc + c0, o);
-    ld_wait(o);
-  }
-  if (!there) return;
-  if (wide) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      F8 v;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v.v[k] = factor * __uint_as_float(o[i + k]);
-      if (c0 + i < D) store8(x.p, bf16, at + i, v);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c0 + i < D) store_elem(x.p, bf16, at + i, factor * __uint_as_float(o[i]));
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Keys
 // ---------------------------------------------------------------------------
@@ -399,13 +368,14 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
     if (ok && n > 0) ok = __all_sync(0xffffffffu, wait(&bar.acc_full, 0));
     if (ok) {
       fence_after();
-      const bool there = key < t.nk;
+      // all tiles have been read: their place serves for the way out
+      const int row0 = t.row0 + (warp & 3) * 32, rows = max(0, min(32, t.nk - row0));
 #pragma unroll
-      for (int i = part; i < DP / 16; i += C::kWarps / 4) {  // 32 columns of g_v, then of g_k
-        const bool second = i >= DP / 32;
-        store_columns(second ? p.gk : p.gv, p.g_bf16, second ? wide_k : wide_v, t.k0 + key, hk,
-                      32 * (i % (DP / 32)), p.D, there, tmem + (second ? C::kK : C::kV) + lanes,
-                      n == 0, second ? p.scale : 1.f);
+      for (int i = part; i < DP / 32; i += C::kWarps / 4) {  // 64 columns of g_v, then of g_k
+        const bool second = i >= DP / 64;
+        store_64(smem + (warp - 4) * 8192, second ? p.gk : p.gv, p.g_bf16, second ? wide_k : wide_v,
+                 t.k0 + row0, rows, hk, 64 * (i % (DP / 64)), p.D,
+                 tmem + (second ? C::kK : C::kV) + lanes, n == 0, n == 0, second ? p.scale : 1.f);
       }
     }
   }
@@ -650,10 +620,12 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
       if (lane == 0) mbar_arrive(&bar.ds_full[j & 1]);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, wait(&bar.acc_full, 0));
-    if (ok) {
+    if (ok && part < DP / 64) {
       fence_after();
-      store_columns(p.gq, p.g_bf16, wide, t.q0 + row, h, 32 * part, p.D, there,
-                    tmem + C::kQ + lanes, n == 0, p.scale);
+      const int row0 = t.row0 + (warp & 3) * 32;
+      store_64(smem + (warp - 4) * 8192, p.gq, p.g_bf16, wide, t.q0 + row0,
+               max(0, min(32, t.nq - row0)), h, 64 * part, p.D, tmem + C::kQ + lanes, n == 0, n == 0,
+               p.scale);
     }
   }
   __syncwarp();

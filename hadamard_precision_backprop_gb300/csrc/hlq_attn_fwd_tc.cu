@@ -304,37 +304,18 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
     const bool there = past < 0 && row < t.nq;
     if (ok) {
       fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zeros
-      const int64_t at = (int64_t)(t.q0 + row) * p.out.token + (int64_t)h * p.out.head;
+      const float inv = 1.f / l;
       if (there)
         p.lse[(int64_t)(t.q0 + row) * p.Hq + h] =
             l == 0.f ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+      // Q has been read: its place serves for the way out.  A row that sees
+      // nothing is zeros, whatever TMEM holds.
+      const bool none = __all_sync(0xffffffffu, l == 0.f);
+      const int first = t.row0 + g * kRows + (warp & 3) * 32;
 #pragma unroll
-      for (int c = 0; c < DP / 32; ++c) {
-        uint32_t o[32];
-        if (tiles[g] > 0) {
-          __syncwarp();
-          ld32(to + 32 * c, o);
-          ld_wait(o);
-        }
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
-        if (there) {
-          if (wide_out) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              if (32 * c + i < p.D)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.p) + at + 32 * c + i) =
-                    make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]),
-                               bf16x2(v[i + 4], v[i + 5]), bf16x2(v[i + 6], v[i + 7]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i < p.D) store_elem(p.out.p, true, at + 32 * c + i, v[i]);
-          }
-        }
-      }
+      for (int c = 0; c < DP / 64; ++c)
+        store_64(sq + g * C::kTile + (warp & 3) * 4096, p.out, true, wide_out, t.q0 + first,
+                 max(0, min(32, t.nq - first)), h, 64 * c, p.D, to, none, l == 0.f, inv);
     }
   }
   __syncwarp();

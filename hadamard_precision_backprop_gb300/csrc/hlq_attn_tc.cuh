@@ -240,6 +240,80 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// 64 columns (from c0 on) of the 32 rows that a warp has in TMEM, lane = row, to
+// rows row0 .. row0 + n - 1 of x, times the lane's factor; zeros where the lane's
+// `zero` says so (`none`: in all lanes, and TMEM is not read).
+// With `wide` (rows of whole 16 bytes) they pass through shared memory, 8 KB of
+// the warp's own, so that a store covers whole rows: a lane's own row piece by
+// piece is 32 sectors for each store, which took 4000 clocks for 128 x 256 bf16.
+__device__ __forceinline__ void store_64(uint8_t* stage, const Heads& x, bool bf16, int wide,
+                                         int64_t row0, int n, int h, int c0, int D, uint32_t at,
+                                         bool none, bool zero, float factor) {
+  const int lane = threadIdx.x & 31;
+  const int64_t to = row0 * x.token + (int64_t)h * x.head + c0;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t o[32];
+    __syncwarp();
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0;
+    } else {
+      ld32(at + c0 + 32 * half, o);
+      ld_wait(o);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(zero ? 0.f : factor * __uint_as_float(o[i]));
+    if (!wide) {
+      if (lane < n)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c0 + 32 * half + i < D) {
+            const int64_t e = to + lane * x.token + 32 * half + i;
+            if (bf16)
+              static_cast<__nv_bfloat16*>(x.p)[e] = __float2bfloat16_rn(__uint_as_float(o[i]));
+            else
+              static_cast<float*>(x.p)[e] = __uint_as_float(o[i]);
+          }
+    } else if (bf16) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4)) =
+            make_uint4(bf16x2(__uint_as_float(o[8 * c]), __uint_as_float(o[8 * c + 1])),
+                       bf16x2(__uint_as_float(o[8 * c + 2]), __uint_as_float(o[8 * c + 3])),
+                       bf16x2(__uint_as_float(o[8 * c + 4]), __uint_as_float(o[8 * c + 5])),
+                       bf16x2(__uint_as_float(o[8 * c + 6]), __uint_as_float(o[8 * c + 7])));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + lane * 256 + (((8 * half + c) ^ (lane & 7)) << 4)) =
+            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+    }
+  }
+  __syncwarp();
+  if (!wide) return;
+  if (bf16) {
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (r < n && c0 + 8 * c < D)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x.p) + to + r * x.token + 8 * c) =
+            *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+    }
+  } else {
+    const int c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      if (r < n && c0 + 4 * c < D)
+        *reinterpret_cast<uint4*>(static_cast<float*>(x.p) + to + r * x.token + 4 * c) =
+            *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 7)) << 4));
+    }
+  }
+  __syncwarp();
+}
+
 // Tile of kN rows of head h, chunk by chunk; `bar` expects its bytes.
 template <int kChunks, int kN = kRows>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
