@@ -33,14 +33,17 @@ __device__ __forceinline__ int2 seq_rows(const int32_t* seqs, int b, int T, bool
   return make_int2(lo, hi);
 }
 
-// Tile t of `rows` queries (keys with kKeys; 64 or 128 or so) among the tiles of all sequences,
-// the last tile of a sequence first (with a causal mask it is the longest, if
-// they go by queries).  Returns -1, or where the tiles are used up the number
-// of tiles past the last one.  A whole warp calls it.
+// Tile t of `rows` queries (keys with kKeys) among the tiles of all sequences,
+// those with the most work first.  Returns -1, or where the tiles are used up the
+// number of tiles past the last one.  A whole warp calls it.
 //
 // With sequences of one length the tiles of all sequences that have the same
-// rank follow each other; else each lane looks at a sequence of its own and
-// the warp adds up their tiles, 32 sequences at a time.
+// rank follow each other.  Else each lane looks at a sequence of its own, 32 of
+// them at a time: with a causal mask the work of a sequence's tiles goes from its
+// number of tiles down to one, so for each amount from the most on the tiles that
+// have it (a sequence's tiles one after the other: 24 packed sequences of up to
+// 1500 tokens ended with a long one that began late); without a mask the tiles of
+// a sequence have the same work and follow each other.
 template <bool kKeys, int rows>
 __device__ __forceinline__ int find_tile(const Attn& p, int t, AttnTile& o) {
   const int T = kKeys ? p.Tk : p.Tq;
@@ -55,29 +58,41 @@ __device__ __forceinline__ int find_tile(const Attn& p, int t, AttnTile& o) {
   bool bad = false;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
-    int n = 0, sum;
+    int n = 0;
     if (b < p.batch) {
       const int2 r = seq_rows(seqs, b, T, bad);
       n = (r.y - r.x + rows - 1) / rows;
     }
-    sum = n;
+    const int all = __reduce_add_sync(0xffffffffu, n);
+    if (t < all) {
+      int first, index;  // the sequence's lane, and the tile of it
+      if (p.causal) {
+        int work = __reduce_max_sync(0xffffffffu, n);
+        unsigned mask;
+        while (t >= __popc(mask = __ballot_sync(0xffffffffu, n >= work))) {
+          t -= __popc(mask);
+          --work;
+        }
+        const bool mine = n >= work && __popc(mask & ((1u << lane) - 1)) == t;
+        first = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        index = kKeys ? __shfl_sync(0xffffffffu, n, first) - work : work - 1;
+      } else {
+        int sum = n;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, sum > t);
-    if (past) {
-      const int first = __ffs(past) - 1;
-      const int tile = __shfl_sync(0xffffffffu, sum - 1 - t, first);  // from the last one back
-      const int tiles = __shfl_sync(0xffffffffu, n, first);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += v;
+        }
+        first = __ffs(__ballot_sync(0xffffffffu, sum > t)) - 1;
+        index = __shfl_sync(0xffffffffu, sum, first) - 1 - t;
+      }
       const int2 q = seq_rows(p.seqs_q, b0 + first, p.Tq, bad);
       const int2 k = seq_rows(p.seqs_k, b0 + first, p.Tk, bad);
       if (bad) raise_flag(p.status, HLQ_DEV_BADCODE);
-      o = {q.x, q.y - q.x, k.x, k.y - k.x, (kKeys ? tiles - 1 - tile : tile) * rows};
+      o = {q.x, q.y - q.x, k.x, k.y - k.x, index * rows};
       return -1;
     }
-    t -= __shfl_sync(0xffffffffu, sum, 31);
+    t -= all;
   }
   if (bad) raise_flag(p.status, HLQ_DEV_BADCODE);
   return t;

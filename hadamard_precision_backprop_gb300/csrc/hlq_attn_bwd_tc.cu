@@ -29,6 +29,7 @@
 #include <cmath>
 
 #include "hlq_attn_tc.cuh"
+#include "hlq_host.h"
 #include "hlq_rows.cuh"
 
 namespace hlq {
@@ -39,12 +40,12 @@ using namespace tc;
 // By head size: rows of a tile of the other side, and the registers of the
 // warps that do not compute and of those that do (640 threads of 96 registers:
 // 128 x 64 + 512 x 104; 384 of 80: 128 x 48 + 256 x 96).
-template <int DP>
+template <int DP, int kRowsN>
 struct BwdCfg {
-  static constexpr int kN = DP == 64 ? 64 : 128;
+  static constexpr int kN = kRowsN;
   static constexpr int kWarps = kN / 8;  // that compute
-  static constexpr int kThreads = 32 * (4 + kWarps), kCtas = DP == 64 ? 2 : 1;
-  static constexpr int kFewer = DP == 64 ? 48 : 64, kMore = DP == 64 ? 96 : 104;
+  static constexpr int kThreads = 32 * (4 + kWarps), kCtas = kN == 64 ? 2 : 1;
+  static constexpr int kFewer = kN == 64 ? 48 : 64, kMore = kN == 64 ? 96 : 104;
   static constexpr int kChunks = DP / kChunk;
   static constexpr uint32_t kTile = kChunks * kChunkBytes;      // of the CTA's side
   static constexpr uint32_t kOther = kChunks * kN * 128;        // of the other side
@@ -64,8 +65,8 @@ __device__ __forceinline__ void product_of_parts(uint32_t d, uint32_t p, uint32_
 // Keys
 // ---------------------------------------------------------------------------
 template <int DP>
-struct KeysCfg : BwdCfg<DP> {
-  using B = BwdCfg<DP>;
+struct KeysCfg : BwdCfg<DP, DP> {
+  using B = BwdCfg<DP, DP>;
   static constexpr int kStages = DP == 64 ? 3 : 2;  // of Q and of G each
   static constexpr int kStats = 2;                  // of lse and delta
   static constexpr uint32_t kMoreN = B::kN * 32;
@@ -82,12 +83,16 @@ struct KeysBars {
 };
 static_assert(sizeof(KeysBars) <= 512, "barriers fit their 512 bytes");
 
-template <int DP>
-__global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
+// With kSplit a cluster of 2^log_split CTAs has the tile of keys, each some of
+// the query heads; they add up their sums through each other's shared memory, in
+// the order of their ranks.
+template <int DP, bool kSplit>
+__global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
     attn_bwd_keys_tc_kernel(const Attn p, const __grid_constant__ CUtensorMap mq,
                             const __grid_constant__ CUtensorMap mk,
                             const __grid_constant__ CUtensorMap mv,
-                            const __grid_constant__ CUtensorMap mg, int wide_k, int wide_v) {
+                            const __grid_constant__ CUtensorMap mg, int wide_k, int wide_v,
+                            int log_split) {
   using C = KeysCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -139,8 +144,12 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
   pdl_trigger();
   pdl_wait();
 
-  const uint32_t tile = blockIdx.x / p.by_hk;
-  const int hk = (int)(blockIdx.x - tile * p.Hk), group = p.group;
+  const uint32_t unit = kSplit ? blockIdx.x >> log_split : blockIdx.x, tile = unit / p.by_hk;
+  const int hk = (int)(unit - tile * p.Hk);
+  const int rank = kSplit ? (int)cluster_rank() : 0;
+  // of the query heads
+  const int h0 = hk * p.group + (kSplit ? rank * p.group >> log_split : 0);
+  const int heads = kSplit ? hk * p.group + ((rank + 1) * p.group >> log_split) - h0 : p.group;
   AttnTile t;
   const int past = find_tile<true, kRows>(p, (int)tile, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
@@ -153,12 +162,9 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
     if (p.causal) first = max(0, t.row0 + t.nq - t.nk) / C::kN;
     per_head = max(0, (t.nq + C::kN - 1) / C::kN - first);
   }
-  const int n = per_head * group;
+  const int n = per_head * heads;
   // rows of a head's last tile, if it is not full
   const int rest = t.nq % C::kN;
-  const auto head_of = [&](int it) { return hk * group + it / per_head; };
-  const auto tile_of = [&](int it) { return first + it % per_head; };
-
   if (past >= 0) {
     outside_rows<true>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row) {
       for (int d = 0; d < p.D; ++d) {
@@ -174,9 +180,10 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
         mbar_expect_tx(&bar.kv_full, 2 * C::kTile);
         load_tile<C::kChunks>(sk, &mk, &bar.kv_full, hk, t.k0 + t.row0);
         load_tile<C::kChunks>(sv, &mv, &bar.kv_full, hk, t.k0 + t.row0);
-        for (int it = 0; it < n; ++it) {
+        for (int it = 0, h = h0, i = first; it < n; ++it, ++i) {
           const int s = it % C::kStages, use = it / C::kStages;
-          const int row = t.q0 + tile_of(it) * C::kN, h = head_of(it);
+          if (i == first + per_head) i = first, ++h;
+          const int row = t.q0 + i * C::kN;
           if (use > 0 && !wait(&bar.q_empty[s], use - 1)) break;
           mbar_expect_tx(&bar.q_full[s], C::kOther);
           load_tile<C::kChunks, C::kN>(sq + s * C::kOther, &mq, &bar.q_full[s], h, row);
@@ -271,9 +278,10 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
       }
       __syncwarp();
     } else if (warp == 2) {  // clears the rows behind the sequence's end
-      for (int it = 0; it < n; ++it) {
+      for (int it = 0, left = per_head; it < n; ++it) {
         const int s = it % C::kStages, use = it / C::kStages;
-        const bool cut = rest && it % per_head == per_head - 1;
+        const bool cut = rest && left == 1;
+        left = left == 1 ? per_head : left - 1;
         if (!__all_sync(0xffffffffu, wait(&bar.q_full[s], use))) break;
         if (cut) clear_rows<C::kChunks, C::kN>(sq + s * C::kOther, rest);
         if (lane == 0) mbar_arrive(&bar.q_ready[s]);
@@ -285,10 +293,11 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
       // -lse / scale and -delta of the tiles' queries as three bf16 numbers each;
       // what is behind the end or sees nothing has a score of -3e38
       const float back = 1.f / (p.scale * kLog2e);
-      for (int it = 0; it < n; ++it) {
+      for (int it = 0, h = h0, i = first; it < n; ++it, ++i) {
         const int u = it % C::kStats;
-        const int i0 = tile_of(it) * C::kN + lane;
-        const int64_t at = (int64_t)head_of(it) * p.Tq + t.q0 + i0;
+        if (i == first + per_head) i = first, ++h;
+        const int i0 = i * C::kN + lane;
+        const int64_t at = (int64_t)h * p.Tq + t.q0 + i0;
         float v[2][C::kN / 32];  // all on their way before the first is used
 #pragma unroll
         for (int i = 0; i < C::kN / 32; ++i) {
@@ -313,6 +322,11 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
         if (lane == 0) mbar_arrive(&bar.stat_full[u]);
       }
     }
+    if constexpr (kSplit) {  // the two barriers of the other branch
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     more_registers<C::kMore>();
     const int part = (warp - 4) >> 2;  // of the columns
@@ -324,8 +338,9 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
     const int from = p.causal ? key + t.nq - t.nk : 0;
     const int last_from = p.causal ? t.row0 + kRows - 1 + t.nq - t.nk : 0;
     bool ok = true;
-    for (int it = 0; it < n; ++it) {
-      const int i0 = tile_of(it) * C::kN + 32 * part;
+    for (int it = 0, tile_q = first; it < n; ++it, ++tile_q) {
+      if (tile_q == first + per_head) tile_q = first;
+      const int i0 = tile_q * C::kN + 32 * part;
       ok = __all_sync(0xffffffffu, wait(&bar.s_full, it));
       if (!ok) break;
       fence_after();
@@ -373,10 +388,51 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
 #pragma unroll
       for (int i = part; i < DP / 32; i += C::kWarps / 4) {  // 64 columns of g_v, then of g_k
         const bool second = i >= DP / 64;
-        store_64(smem + (warp - 4) * 8192, second ? p.gk : p.gv, p.g_bf16, second ? wide_k : wide_v,
-                 t.k0 + row0, rows, hk, 64 * (i % (DP / 64)), p.D,
-                 tmem + (second ? C::kK : C::kV) + lanes, n == 0, n == 0, second ? p.scale : 1.f);
+        const uint32_t from = tmem + (second ? C::kK : C::kV) + lanes;
+        if (kSplit)
+          stage_64(smem + (4 * i + (warp & 3)) * 8192, 64 * (i % (DP / 64)), from, n == 0,
+                   second ? p.scale : 1.f);
+        else
+          store_64(smem + (warp - 4) * 8192, second ? p.gk : p.gv, p.g_bf16,
+                   second ? wide_k : wide_v, t.k0 + row0, rows, hk, 64 * (i % (DP / 64)), p.D, from,
+                   n == 0, n == 0, second ? p.scale : 1.f);
       }
+    }
+    if constexpr (kSplit) {
+      __syncwarp();
+      cluster_sync();
+      // block b: 64 columns of 32 rows, as 32 x 16 pieces of 16 bytes
+      for (int b = rank; b < DP / 8; b += 1 << log_split) {
+        const int i = b >> 2;
+        const bool second = i >= DP / 64;
+        const Heads& x = second ? p.gk : p.gv;
+        const int c0 = 64 * (i % (DP / 64));
+        for (int e = threadIdx.x - 128; e < 512; e += C::kThreads - 128) {
+          const int r = e >> 4, c = e & 15, row = t.row0 + 32 * (b & 3) + r, d = c0 + 4 * c;
+          if (row >= t.nk || d >= p.D) continue;
+          const uint32_t at = saddr(smem) + b * 8192 + r * 256 + ((c ^ (r & 7)) << 4);
+          float4 sum = load_cluster(cluster_map(at, 0));
+          for (int k = 1; k < 1 << log_split; ++k) {
+            const float4 v = load_cluster(cluster_map(at, k));
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+          }
+          const int64_t to = (int64_t)(t.k0 + row) * x.token + (int64_t)hk * x.head + d;
+          if (second ? wide_k : wide_v) {
+            if (p.g_bf16)
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(x.p) + to) =
+                  make_uint2(bf16x2(sum.x, sum.y), bf16x2(sum.z, sum.w));
+            else
+              *reinterpret_cast<float4*>(static_cast<float*>(x.p) + to) = sum;
+          } else {
+            store_elem(x.p, p.g_bf16, to, sum.x);
+            if (d + 1 < p.D) store_elem(x.p, p.g_bf16, to + 1, sum.y);
+            if (d + 2 < p.D) store_elem(x.p, p.g_bf16, to + 2, sum.z);
+            if (d + 3 < p.D) store_elem(x.p, p.g_bf16, to + 3, sum.w);
+          }
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // nobody's shared memory goes before it has been read
     }
   }
   __syncwarp();
@@ -391,14 +447,19 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
 // ---------------------------------------------------------------------------
 // Queries
 // ---------------------------------------------------------------------------
-template <int DP>
-struct QueriesCfg : BwdCfg<DP> {
-  using B = BwdCfg<DP>;
+template <int DP, int kN>
+struct QueriesCfg : BwdCfg<DP, kN> {
+  using B = BwdCfg<DP, kN>;
+  static constexpr bool kTight = DP == 128 && kN == 64;
   // K is read by the scores of a tile and, later, by g_q
-  static constexpr int kStagesK = DP == 64 ? 4 : 3, kStagesV = DP == 64 ? 3 : 2;
+  static constexpr int kStagesK = kTight ? 2 : DP == 64 ? 4 : 3;
+  static constexpr int kStagesV = kTight ? 1 : DP == 64 ? 3 : 2;
+  static constexpr int kDs = kTight ? 1 : 2;  // places of D
+  static constexpr size_t kSlack = kTight ? 0 : 1024;
   static constexpr size_t kSmem =
-      1024 + 2 * B::kTile + (size_t)(kStagesK + kStagesV) * B::kOther + 512;
-  static constexpr uint32_t kS = 0, kD = B::kN, kQ = 3 * B::kN, kColumns = 4 * B::kN;
+      kSlack + 2 * B::kTile + (size_t)(kStagesK + kStagesV) * B::kOther + 512;
+  static constexpr uint32_t kS = 0, kD = kN, kQ = kD + kDs * kN;
+  static constexpr uint32_t kColumns = kQ + DP <= 256 ? 256 : 512;
 };
 
 struct QueriesBars {
@@ -409,16 +470,21 @@ struct QueriesBars {
 };
 static_assert(sizeof(QueriesBars) <= 512, "barriers fit their 512 bytes");
 
-template <int DP>
-__global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
+template <int DP, int kN>
+__global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, kN>::kCtas)
     attn_bwd_queries_tc_kernel(const Attn p, const __grid_constant__ CUtensorMap mq,
                                const __grid_constant__ CUtensorMap mk,
                                const __grid_constant__ CUtensorMap mv,
                                const __grid_constant__ CUtensorMap mg, int wide) {
-  using C = QueriesCfg<DP>;
+  using C = QueriesCfg<DP, kN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
+  // shared memory begins on 1 KB where a kernel has no other, as this one
+  if (C::kSlack == 0 && smem != smem_raw) {
+    if (threadIdx.x == 0) raise_flag(p.status, HLQ_DEV_TIMEOUT);
+    return;
+  }
   uint8_t *sq = smem, *sg = sq + C::kTile, *sk = sg + C::kTile, *sv = sk + C::kStagesK * C::kOther;
   QueriesBars& bar = *reinterpret_cast<QueriesBars*>(sv + C::kStagesV * C::kOther);
   volatile int* abort_flag = &bar.abort;
@@ -524,12 +590,12 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
           }
           __syncwarp();
           ok = wait(&bar.v_full[u], j / C::kStagesV) &&
-               (j < 2 || wait(&bar.d_empty[j & 1], (j >> 1) - 1));  // g_q has read dS
+               (j < C::kDs || wait(&bar.d_empty[j % C::kDs], j / C::kDs - 1));  // g_q has read dS
           if (!ok) break;
           fence_after();
           if (elect_one()) {
-            product_of_rows<DP / 16, C::kN>(tmem + C::kD + C::kN * (j & 1), ag, av + u * kStep, steps);
-            commit(&bar.d_full[j & 1]);
+            product_of_rows<DP / 16, C::kN>(tmem + C::kD + C::kN * (j % C::kDs), ag, av + u * kStep, steps);
+            commit(&bar.d_full[j % C::kDs]);
             if (j + C::kStagesV < n) commit(&bar.v_empty[u]);
           }
           __syncwarp();
@@ -539,12 +605,12 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
         const uint32_t id = idesc(16 * steps, true), rk = by_rows(saddr(sk), C::kN);
         for (int j = 0; j < n && ok; ++j) {
           const int s = j % C::kStagesK;
-          ok = wait(&bar.ds_full[j & 1], j >> 1);  // and so K is there
+          ok = wait(&bar.ds_full[j % C::kDs], j / C::kDs);  // and so K is there
           if (!ok) break;
           fence_after();
           if (elect_one()) {
-            product_of_parts<C::kN>(tmem + C::kQ, tmem + C::kD + C::kN * (j & 1), rk + s * kStep, id, j > 0);
-            if (j + 2 < n) commit(&bar.d_empty[j & 1]);
+            product_of_parts<C::kN>(tmem + C::kQ, tmem + C::kD + C::kN * (j % C::kDs), rk + s * kStep, id, j > 0);
+            if (j + C::kDs < n) commit(&bar.d_empty[j % C::kDs]);
             if (j + C::kStagesK < n) commit(&bar.k_empty[s]);
           }
           __syncwarp();
@@ -594,10 +660,10 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
         const float2 a = split(fma2(f2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c22, lse2));
         prob[i] = exp2_fast(a.x), prob[i + 1] = exp2_fast(a.y);
       }
-      ok = __all_sync(0xffffffffu, wait(&bar.d_full[j & 1], j >> 1));
+      ok = __all_sync(0xffffffffu, wait(&bar.d_full[j % C::kDs], j / C::kDs));
       if (!ok) break;
       fence_after();
-      ld32(td + C::kN * (j & 1), x);
+      ld32(td + C::kN * (j % C::kDs), x);
       ld_wait(x);
       float ds[32];
 #pragma unroll
@@ -613,11 +679,11 @@ __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
       }
 #pragma unroll
       for (int i = 0; i < 32; i += 2) e[i / 2] = bf16x2(ds[i], ds[i + 1]);
-      st16(td + C::kN * (j & 1), e);
+      st16(td + C::kN * (j % C::kDs), e);
       st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.ds_full[j & 1]);
+      if (lane == 0) mbar_arrive(&bar.ds_full[j % C::kDs]);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, wait(&bar.acc_full, 0));
     if (ok && part < DP / 64) {
@@ -655,31 +721,45 @@ bool make_maps(Maps* m, const Attn& p, int rows_q, int rows_k) {
          heads_map(&m->g, g, p.Tq, p.Hq, p.D, rows_q);
 }
 
-template <int DP>
-cudaError_t launch_keys(const Attn& p, cudaStream_t st) {
+template <int DP, bool kSplit>
+cudaError_t launch_keys(const Attn& p, int log_split, cudaStream_t st) {
   using C = KeysCfg<DP>;
-  const int64_t grid = most_tiles(p, true, kRows) * p.Hk;
+  const int64_t grid = most_tiles(p, true, kRows) * p.Hk << log_split;
   if (grid == 0) return cudaSuccess;
   Maps m;
   if (!make_maps(&m, p, C::kN, kRows)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<attn_bwd_keys_tc_kernel<DP>>(C::kSmem);
+  cudaError_t e = allow_smem<attn_bwd_keys_tc_kernel<DP, kSplit>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_bwd_keys_tc_kernel<DP>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem,
-                    st, p, m.q, m.k, m.v, m.g, wide_rows(p.gk, p.g_bf16, p.Tk, p.Hk, p.D),
-                    wide_rows(p.gv, p.g_bf16, p.Tk, p.Hk, p.D));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1u << log_split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kSplit ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, attn_bwd_keys_tc_kernel<DP, kSplit>, p, m.q, m.k, m.v, m.g,
+                            wide_rows(p.gk, p.g_bf16, p.Tk, p.Hk, p.D),
+                            wide_rows(p.gv, p.g_bf16, p.Tk, p.Hk, p.D), log_split);
 }
 
-template <int DP>
+template <int DP, int kN>
 cudaError_t launch_queries(const Attn& p, cudaStream_t st) {
-  using C = QueriesCfg<DP>;
+  using C = QueriesCfg<DP, kN>;
   const int64_t grid = most_tiles(p, false, kRows) * p.Hq;
   if (grid == 0) return cudaSuccess;
   Maps m;
-  if (!make_maps(&m, p, kRows, C::kN)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<attn_bwd_queries_tc_kernel<DP>>(C::kSmem);
+  if (!make_maps(&m, p, kRows, kN)) return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem<attn_bwd_queries_tc_kernel<DP, kN>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_bwd_queries_tc_kernel<DP>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem,
-                    st, p, m.q, m.k, m.v, m.g, wide_rows(p.gq, p.g_bf16, p.Tq, p.Hq, p.D));
+  return launch_pdl(attn_bwd_queries_tc_kernel<DP, kN>, dim3((unsigned)grid), dim3(C::kThreads),
+                    C::kSmem, st, p, m.q, m.k, m.v, m.g,
+                    wide_rows(p.gq, p.g_bf16, p.Tq, p.Hq, p.D));
 }
 
 }  // namespace
@@ -688,10 +768,25 @@ bool attn_bwd_tc(const Attn& p) {
   return attn_tc(p) && (!p.gout_bf16 || tma_heads(p.gout, p.Tq, p.Hq));
 }
 cudaError_t launch_attn_bwd_keys_tc(const Attn& p, cudaStream_t st) {
-  return p.D <= 64 ? launch_keys<64>(p, st) : launch_keys<128>(p, st);
+  const int64_t ctas = most_tiles(p, true, kRows) * p.Hk;
+  // A cluster for a tile only where there are fewer tiles than SMs twice: one
+  // sequence of 16384 (4 heads of 128 that share one; causal) 938 -> 601 us for
+  // the whole backward pass, but 8 of 2048 (16 heads, 4 shared ones) 409 -> 459.
+  int split = 0;
+  while (split < 3 && 2 << split <= p.group && ctas << split < 2 * (int64_t)device_sm_count())
+    ++split;
+  if (split > 0)
+    return p.D <= 64 ? launch_keys<64, true>(p, split, st) : launch_keys<128, true>(p, split, st);
+  return p.D <= 64 ? launch_keys<64, false>(p, 0, st) : launch_keys<128, false>(p, 0, st);
 }
 cudaError_t launch_attn_bwd_queries_tc(const Attn& p, cudaStream_t st) {
-  return p.D <= 64 ? launch_queries<64>(p, st) : launch_queries<128>(p, st);
+  // Tiles of 64 keys and two CTAs an SM, but for few or long CTAs: 24 packed
+  // sequences (16 heads of 80) 59 us against 76 with tiles of 128, 64 x 197 (12
+  // heads of 64) 45 against 62; one sequence of 16384 (4 heads of 128; with the
+  // keys' pass) 981 against 935, one of 2048 63 against 52.
+  if (p.Tk / p.batch >= 4096 || most_tiles(p, false, kRows) * p.Hq < 2 * device_sm_count())
+    return p.D <= 64 ? launch_queries<64, 128>(p, st) : launch_queries<128, 128>(p, st);
+  return p.D <= 64 ? launch_queries<64, 64>(p, st) : launch_queries<128, 64>(p, st);
 }
 
 }  // namespace hlq

@@ -43,10 +43,15 @@ __device__ __forceinline__ void fence_after() {
 // more (descriptors put together for each of them: 110 to 130 clocks).
 constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint64_t desc(uint32_t low) { return (uint64_t)kDescHigh << 32 | low; }
+// The address of a descriptor is the one within the CTA: in a cluster the higher
+// bits of a shared address tell the CTA, and would be read as the leading step.
+__device__ __forceinline__ uint32_t desc_address(uint32_t tile) { return (tile & 0x3FFFFu) >> 4; }
 // Columns summed over (the leading step is not used), or rows.
-__device__ __forceinline__ uint32_t by_columns(uint32_t tile) { return tile >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t by_columns(uint32_t tile) {
+  return desc_address(tile) | 1u << 16;
+}
 __device__ __forceinline__ uint32_t by_rows(uint32_t tile, int rows = kRows) {
-  return tile >> 4 | (uint32_t)rows * 128 >> 4 << 16;
+  return desc_address(tile) | (uint32_t)rows * 128 >> 4 << 16;
 }
 __host__ __device__ constexpr uint32_t column_step(int k, int rows = kRows) {
   return ((uint32_t)(k >> 2) * (rows * 128) + (uint32_t)(k & 3) * 32) >> 4;
@@ -58,7 +63,7 @@ __host__ __device__ constexpr uint32_t row_step(int k) { return (uint32_t)k * 16
 // together, the two halves of a row 128 bytes and eight rows 256 bytes apart.
 constexpr uint32_t kMoreBytes = kRows * 32;
 __device__ __forceinline__ uint64_t more_columns(uint32_t tile) {
-  return (uint64_t)(256 >> 4 | 1u << 14) << 32 | (tile >> 4 | (128u >> 4) << 16);
+  return (uint64_t)(256 >> 4 | 1u << 14) << 32 | (desc_address(tile) | (128u >> 4) << 16);
 }
 __device__ __forceinline__ uint32_t more_at(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
 
@@ -312,6 +317,32 @@ __device__ __forceinline__ void store_64(uint8_t* stage, const Heads& x, bool bf
     }
   }
   __syncwarp();
+}
+
+// The same columns into 8 KB of shared memory as fp32, laid out as there.
+__device__ __forceinline__ void stage_64(uint8_t* stage, int c0, uint32_t at, bool none,
+                                         float factor) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t o[32];
+    __syncwarp();
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0;
+    } else {
+      ld32(at + c0 + 32 * half, o);
+      ld_wait(o);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = none ? 0.f : factor * __uint_as_float(o[4 * c + k]);
+      *reinterpret_cast<float4*>(stage + lane * 256 + (((8 * half + c) ^ (lane & 7)) << 4)) =
+          make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
 }
 
 // Tile of kN rows of head h, chunk by chunk; `bar` expects its bytes.
