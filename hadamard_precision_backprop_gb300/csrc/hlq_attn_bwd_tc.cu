@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
   volatile int* abort_flag = &bar.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (threadIdx.x == 64) prefetch(&mk), prefetch(&mv), prefetch(&mq), prefetch(&mg);
   if (threadIdx.x == 0) {
     mbar_init(&bar.kv_full, 1);
     for (int s = 0; s < C::kStages; ++s) {
@@ -134,13 +135,6 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
                                                : make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 1) alloc(&bar.tmem, C::kColumns);
-  if (threadIdx.x == 64) {
-    prefetch(&mq), prefetch(&mk), prefetch(&mv), prefetch(&mg);
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   pdl_trigger();
   pdl_wait();
 
@@ -164,7 +158,38 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
   }
   const int n = per_head * heads;
   // rows of a head's last tile, if it is not full
-  const int rest = t.nq % C::kN;
+  const int rest = past < 0 ? t.nq % C::kN : 0;
+  // Thread 0 has set up the barriers, and loads (the first tiles before the others
+  // come to the barrier below).
+  int q_done = 0, g_done = 0;
+  const auto load_q = [&](int it, int h, int i) {
+    const int s = it % C::kStages, use = it / C::kStages;
+    if (use > 0 && !wait(&bar.q_empty[s], use - 1)) return false;
+    mbar_expect_tx(&bar.q_full[s], C::kOther);
+    load_tile<C::kChunks, C::kN>(sq + s * C::kOther, &mq, &bar.q_full[s], h, t.q0 + i * C::kN);
+    ++q_done;
+    return true;
+  };
+  const auto load_g = [&](int it, int h, int i) {
+    const int s = it % C::kStages, use = it / C::kStages;
+    if (use > 0 && !wait(&bar.g_empty[s], use - 1)) return false;
+    mbar_expect_tx(&bar.g_full[s], C::kOther);
+    load_tile<C::kChunks, C::kN>(sg + s * C::kOther, &mg, &bar.g_full[s], h, t.q0 + i * C::kN);
+    ++g_done;
+    return true;
+  };
+  if (threadIdx.x == 0 && n > 0) {
+    mbar_expect_tx(&bar.kv_full, 2 * C::kTile);
+    load_tile<C::kChunks>(sk, &mk, &bar.kv_full, hk, t.k0 + t.row0);
+    load_q(0, h0, first);
+    load_tile<C::kChunks>(sv, &mv, &bar.kv_full, hk, t.k0 + t.row0);
+    load_g(0, h0, first);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
+
   if (past >= 0) {
     outside_rows<true>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row) {
       for (int d = 0; d < p.D; ++d) {
@@ -176,22 +201,9 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
     fewer_registers<C::kFewer>();
     if (warp == 0) {
       if (lane == 0 && n > 0) {
-        int q_done = 0, g_done = 0;
-        mbar_expect_tx(&bar.kv_full, 2 * C::kTile);
-        load_tile<C::kChunks>(sk, &mk, &bar.kv_full, hk, t.k0 + t.row0);
-        load_tile<C::kChunks>(sv, &mv, &bar.kv_full, hk, t.k0 + t.row0);
-        for (int it = 0, h = h0, i = first; it < n; ++it, ++i) {
-          const int s = it % C::kStages, use = it / C::kStages;
+        for (int it = 1, h = h0, i = first + 1; it < n; ++it, ++i) {
           if (i == first + per_head) i = first, ++h;
-          const int row = t.q0 + i * C::kN;
-          if (use > 0 && !wait(&bar.q_empty[s], use - 1)) break;
-          mbar_expect_tx(&bar.q_full[s], C::kOther);
-          load_tile<C::kChunks, C::kN>(sq + s * C::kOther, &mq, &bar.q_full[s], h, row);
-          ++q_done;
-          if (use > 0 && !wait(&bar.g_empty[s], use - 1)) break;
-          mbar_expect_tx(&bar.g_full[s], C::kOther);
-          load_tile<C::kChunks, C::kN>(sg + s * C::kOther, &mg, &bar.g_full[s], h, row);
-          ++g_done;
+          if (!load_q(it, h, i) || !load_g(it, h, i)) break;
         }
         if (*abort_flag) {
           ring_drain(&bar.kv_full, 1, 1);
@@ -490,6 +502,7 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
   volatile int* abort_flag = &bar.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (threadIdx.x == 64) prefetch(&mq), prefetch(&mk), prefetch(&mg), prefetch(&mv);
   if (threadIdx.x == 0) {
     mbar_init(&bar.qg_full, 1);
     for (int s = 0; s < C::kStagesK; ++s) {
@@ -517,13 +530,6 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
     fence_proxy_async_smem();
   }
   if (warp == 1) alloc(&bar.tmem, C::kColumns);
-  if (threadIdx.x == 64) {
-    prefetch(&mq), prefetch(&mk), prefetch(&mv), prefetch(&mg);
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   pdl_trigger();
   pdl_wait();
 
@@ -538,6 +544,35 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
   const int n = (keys + C::kN - 1) / C::kN;
   // rows of the sequence's last tile of keys, if this CTA goes as far and it is not full
   const int rest = n > 0 && t.nk < n * C::kN ? t.nk - (n - 1) * C::kN : 0;
+  int k_done = 0, v_done = 0, last_done = 0;
+  const auto load_k = [&](int j) {
+    const int s = j % C::kStagesK;
+    if (j >= C::kStagesK && !wait(&bar.k_empty[s], j / C::kStagesK - 1)) return false;
+    uint64_t* full = rest && j == n - 1 ? &bar.k_last : &bar.k_full[s];
+    mbar_expect_tx(full, C::kOther);
+    load_tile<C::kChunks, C::kN>(sk + s * C::kOther, &mk, full, hk, t.k0 + j * C::kN);
+    ++(full == &bar.k_last ? last_done : k_done);
+    return true;
+  };
+  const auto load_v = [&](int j) {
+    const int u = j % C::kStagesV;
+    if (j >= C::kStagesV && !wait(&bar.v_empty[u], j / C::kStagesV - 1)) return false;
+    mbar_expect_tx(&bar.v_full[u], C::kOther);
+    load_tile<C::kChunks, C::kN>(sv + u * C::kOther, &mv, &bar.v_full[u], hk, t.k0 + j * C::kN);
+    ++v_done;
+    return true;
+  };
+  if (threadIdx.x == 0 && n > 0) {
+    mbar_expect_tx(&bar.qg_full, 2 * C::kTile);
+    load_tile<C::kChunks>(sq, &mq, &bar.qg_full, h, t.q0 + t.row0);
+    load_k(0);
+    load_tile<C::kChunks>(sg, &mg, &bar.qg_full, h, t.q0 + t.row0);
+    load_v(0);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
 
   if (past >= 0) {
     outside_rows<false>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row) {
@@ -548,22 +583,8 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
     fewer_registers<C::kFewer>();
     if (warp == 0) {
       if (lane == 0 && n > 0) {
-        int k_done = 0, v_done = 0, last_done = 0;
-        mbar_expect_tx(&bar.qg_full, 2 * C::kTile);
-        load_tile<C::kChunks>(sq, &mq, &bar.qg_full, h, t.q0 + t.row0);
-        load_tile<C::kChunks>(sg, &mg, &bar.qg_full, h, t.q0 + t.row0);
-        for (int j = 0; j < n; ++j) {
-          const int s = j % C::kStagesK, u = j % C::kStagesV;
-          if (j >= C::kStagesK && !wait(&bar.k_empty[s], j / C::kStagesK - 1)) break;
-          uint64_t* full = rest && j == n - 1 ? &bar.k_last : &bar.k_full[s];
-          mbar_expect_tx(full, C::kOther);
-          load_tile<C::kChunks, C::kN>(sk + s * C::kOther, &mk, full, hk, t.k0 + j * C::kN);
-          ++(full == &bar.k_last ? last_done : k_done);
-          if (j >= C::kStagesV && !wait(&bar.v_empty[u], j / C::kStagesV - 1)) break;
-          mbar_expect_tx(&bar.v_full[u], C::kOther);
-          load_tile<C::kChunks, C::kN>(sv + u * C::kOther, &mv, &bar.v_full[u], hk, t.k0 + j * C::kN);
-          ++v_done;
-        }
+        for (int j = 1; j < n; ++j)
+          if (!load_k(j) || !load_v(j)) break;
         if (*abort_flag) {
           ring_drain(&bar.qg_full, 1, 1);
           ring_drain(bar.k_full, C::kStagesK, k_done);
