@@ -1,9 +1,9 @@
 // hlq_attn_bwd_tc.cu -- attention's backward pass in bf16 on the tensor cores
 // (tcgen05, TMEM, TMA), heads up to 128.
 //
-// Two kernels, so that every gradient is summed in one place in a fixed order
-// (seven products of a tile of queries and one of keys where five with atomics
-// would do):
+// Two kinds of CTAs, so that every gradient is summed in one place in a fixed
+// order (seven products of a tile of queries and one of keys where five with
+// atomics would do):
 //
 // Keys: a CTA has a tile of 128 keys of a key head and goes over the tiles of
 // queries of all query heads that share it.  Rows are keys, columns queries:
@@ -40,9 +40,9 @@ using namespace tc;
 // By head size: rows of a tile of the other side, and the registers of the
 // warps that do not compute and of those that do (640 threads of 96 registers:
 // 128 x 64 + 512 x 104; 384 of 80: 128 x 48 + 256 x 96).
-template <int DP, int kRowsN>
+template <int DP>
 struct BwdCfg {
-  static constexpr int kN = kRowsN;
+  static constexpr int kN = DP;
   static constexpr int kWarps = kN / 8;  // that compute
   static constexpr int kThreads = 32 * (4 + kWarps), kCtas = kN == 64 ? 2 : 1;
   static constexpr int kFewer = kN == 64 ? 48 : 64, kMore = kN == 64 ? 96 : 104;
@@ -61,12 +61,18 @@ __device__ __forceinline__ void product_of_parts(uint32_t d, uint32_t p, uint32_
     mma_ts(d, p + (k >> 1) * 32 + (k & 1) * 8, desc(b + row_step(k)), id, add || k > 0);
 }
 
+// What a pass reads, and whether the rows of its results are of whole 16 bytes.
+struct Maps {
+  CUtensorMap q, k, v, g;
+  int wide_q, wide_k, wide_v;
+};
+
 // ---------------------------------------------------------------------------
 // Keys
 // ---------------------------------------------------------------------------
 template <int DP>
-struct KeysCfg : BwdCfg<DP, DP> {
-  using B = BwdCfg<DP, DP>;
+struct KeysCfg : BwdCfg<DP> {
+  using B = BwdCfg<DP>;
   static constexpr int kStages = DP == 64 ? 3 : 2;  // of Q and of G each
   static constexpr int kStats = 2;                  // of lse and delta
   static constexpr uint32_t kMoreN = B::kN * 32;
@@ -87,12 +93,8 @@ static_assert(sizeof(KeysBars) <= 512, "barriers fit their 512 bytes");
 // the query heads; they add up their sums through each other's shared memory, in
 // the order of their ranks.
 template <int DP, bool kSplit>
-__global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
-    attn_bwd_keys_tc_kernel(const Attn p, const __grid_constant__ CUtensorMap mq,
-                            const __grid_constant__ CUtensorMap mk,
-                            const __grid_constant__ CUtensorMap mv,
-                            const __grid_constant__ CUtensorMap mg, int wide_k, int wide_v,
-                            int log_split) {
+__device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint32_t block,
+                                          int log_split) {
   using C = KeysCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
   volatile int* abort_flag = &bar.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 64) prefetch(&mk), prefetch(&mv), prefetch(&mq), prefetch(&mg);
+  if (threadIdx.x == 64) prefetch(&maps.k), prefetch(&maps.v), prefetch(&maps.q), prefetch(&maps.g);
   if (threadIdx.x == 0) {
     mbar_init(&bar.kv_full, 1);
     for (int s = 0; s < C::kStages; ++s) {
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
   pdl_trigger();
   pdl_wait();
 
-  const uint32_t unit = kSplit ? blockIdx.x >> log_split : blockIdx.x, tile = unit / p.by_hk;
+  const uint32_t unit = kSplit ? block >> log_split : block, tile = unit / p.by_hk;
   const int hk = (int)(unit - tile * p.Hk);
   const int rank = kSplit ? (int)cluster_rank() : 0;
   // of the query heads
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
     const int s = it % C::kStages, use = it / C::kStages;
     if (use > 0 && !wait(&bar.q_empty[s], use - 1)) return false;
     mbar_expect_tx(&bar.q_full[s], C::kOther);
-    load_tile<C::kChunks, C::kN>(sq + s * C::kOther, &mq, &bar.q_full[s], h, t.q0 + i * C::kN);
+    load_tile<C::kChunks, C::kN>(sq + s * C::kOther, &maps.q, &bar.q_full[s], h, t.q0 + i * C::kN);
     ++q_done;
     return true;
   };
@@ -174,15 +176,15 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
     const int s = it % C::kStages, use = it / C::kStages;
     if (use > 0 && !wait(&bar.g_empty[s], use - 1)) return false;
     mbar_expect_tx(&bar.g_full[s], C::kOther);
-    load_tile<C::kChunks, C::kN>(sg + s * C::kOther, &mg, &bar.g_full[s], h, t.q0 + i * C::kN);
+    load_tile<C::kChunks, C::kN>(sg + s * C::kOther, &maps.g, &bar.g_full[s], h, t.q0 + i * C::kN);
     ++g_done;
     return true;
   };
   if (threadIdx.x == 0 && n > 0) {
     mbar_expect_tx(&bar.kv_full, 2 * C::kTile);
-    load_tile<C::kChunks>(sk, &mk, &bar.kv_full, hk, t.k0 + t.row0);
+    load_tile<C::kChunks>(sk, &maps.k, &bar.kv_full, hk, t.k0 + t.row0);
     load_q(0, h0, first);
-    load_tile<C::kChunks>(sv, &mv, &bar.kv_full, hk, t.k0 + t.row0);
+    load_tile<C::kChunks>(sv, &maps.v, &bar.kv_full, hk, t.k0 + t.row0);
     load_g(0, h0, first);
   }
   fence_before();
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
                    second ? p.scale : 1.f);
         else
           store_64(smem + (warp - 4) * 8192, second ? p.gk : p.gv, p.g_bf16,
-                   second ? wide_k : wide_v, t.k0 + row0, rows, hk, 64 * (i % (DP / 64)), p.D, from,
+                   second ? maps.wide_k : maps.wide_v, t.k0 + row0, rows, hk, 64 * (i % (DP / 64)), p.D, from,
                    n == 0, n == 0, second ? p.scale : 1.f);
       }
     }
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
           }
           const int64_t to = (int64_t)(t.k0 + row) * x.token + (int64_t)hk * x.head + d;
-          if (second ? wide_k : wide_v) {
+          if (second ? maps.wide_k : maps.wide_v) {
             if (p.g_bf16)
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(x.p) + to) =
                   make_uint2(bf16x2(sum.x, sum.y), bf16x2(sum.z, sum.w));
@@ -459,19 +461,15 @@ __global__ void __launch_bounds__(KeysCfg<DP>::kThreads, KeysCfg<DP>::kCtas)
 // ---------------------------------------------------------------------------
 // Queries
 // ---------------------------------------------------------------------------
-template <int DP, int kN>
-struct QueriesCfg : BwdCfg<DP, kN> {
-  using B = BwdCfg<DP, kN>;
-  static constexpr bool kTight = DP == 128 && kN == 64;
+template <int DP>
+struct QueriesCfg : BwdCfg<DP> {
+  using B = BwdCfg<DP>;
   // K is read by the scores of a tile and, later, by g_q
-  static constexpr int kStagesK = kTight ? 2 : DP == 64 ? 4 : 3;
-  static constexpr int kStagesV = kTight ? 1 : DP == 64 ? 3 : 2;
-  static constexpr int kDs = kTight ? 1 : 2;  // places of D
-  static constexpr size_t kSlack = kTight ? 0 : 1024;
+  static constexpr int kStagesK = DP == 64 ? 4 : 3, kStagesV = DP == 64 ? 3 : 2;
+  static constexpr int kDs = 2;  // places of D
   static constexpr size_t kSmem =
-      kSlack + 2 * B::kTile + (size_t)(kStagesK + kStagesV) * B::kOther + 512;
-  static constexpr uint32_t kS = 0, kD = kN, kQ = kD + kDs * kN;
-  static constexpr uint32_t kColumns = kQ + DP <= 256 ? 256 : 512;
+      1024 + 2 * B::kTile + (size_t)(kStagesK + kStagesV) * B::kOther + 512;
+  static constexpr uint32_t kS = 0, kD = B::kN, kQ = kD + kDs * B::kN, kColumns = kQ + DP;
 };
 
 struct QueriesBars {
@@ -482,27 +480,18 @@ struct QueriesBars {
 };
 static_assert(sizeof(QueriesBars) <= 512, "barriers fit their 512 bytes");
 
-template <int DP, int kN>
-__global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, kN>::kCtas)
-    attn_bwd_queries_tc_kernel(const Attn p, const __grid_constant__ CUtensorMap mq,
-                               const __grid_constant__ CUtensorMap mk,
-                               const __grid_constant__ CUtensorMap mv,
-                               const __grid_constant__ CUtensorMap mg, int wide) {
-  using C = QueriesCfg<DP, kN>;
+template <int DP>
+__device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, uint32_t block) {
+  using C = QueriesCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  // shared memory begins on 1 KB where a kernel has no other, as this one
-  if (C::kSlack == 0 && smem != smem_raw) {
-    if (threadIdx.x == 0) raise_flag(p.status, HLQ_DEV_TIMEOUT);
-    return;
-  }
   uint8_t *sq = smem, *sg = sq + C::kTile, *sk = sg + C::kTile, *sv = sk + C::kStagesK * C::kOther;
   QueriesBars& bar = *reinterpret_cast<QueriesBars*>(sv + C::kStagesV * C::kOther);
   volatile int* abort_flag = &bar.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 64) prefetch(&mq), prefetch(&mk), prefetch(&mg), prefetch(&mv);
+  if (threadIdx.x == 64) prefetch(&maps.q), prefetch(&maps.k), prefetch(&maps.g), prefetch(&maps.v);
   if (threadIdx.x == 0) {
     mbar_init(&bar.qg_full, 1);
     for (int s = 0; s < C::kStagesK; ++s) {
@@ -533,8 +522,8 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
   pdl_trigger();
   pdl_wait();
 
-  const uint32_t tile = blockIdx.x / p.by_hq;
-  const int h = (int)(blockIdx.x - tile * p.Hq), hk = (int)((uint32_t)h / p.by_group);
+  const uint32_t tile = block / p.by_hq;
+  const int h = (int)(block - tile * p.Hq), hk = (int)((uint32_t)h / p.by_group);
   AttnTile t;
   const int past = find_tile<false, kRows>(p, (int)tile, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
@@ -550,7 +539,7 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
     if (j >= C::kStagesK && !wait(&bar.k_empty[s], j / C::kStagesK - 1)) return false;
     uint64_t* full = rest && j == n - 1 ? &bar.k_last : &bar.k_full[s];
     mbar_expect_tx(full, C::kOther);
-    load_tile<C::kChunks, C::kN>(sk + s * C::kOther, &mk, full, hk, t.k0 + j * C::kN);
+    load_tile<C::kChunks, C::kN>(sk + s * C::kOther, &maps.k, full, hk, t.k0 + j * C::kN);
     ++(full == &bar.k_last ? last_done : k_done);
     return true;
   };
@@ -558,15 +547,15 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
     const int u = j % C::kStagesV;
     if (j >= C::kStagesV && !wait(&bar.v_empty[u], j / C::kStagesV - 1)) return false;
     mbar_expect_tx(&bar.v_full[u], C::kOther);
-    load_tile<C::kChunks, C::kN>(sv + u * C::kOther, &mv, &bar.v_full[u], hk, t.k0 + j * C::kN);
+    load_tile<C::kChunks, C::kN>(sv + u * C::kOther, &maps.v, &bar.v_full[u], hk, t.k0 + j * C::kN);
     ++v_done;
     return true;
   };
   if (threadIdx.x == 0 && n > 0) {
     mbar_expect_tx(&bar.qg_full, 2 * C::kTile);
-    load_tile<C::kChunks>(sq, &mq, &bar.qg_full, h, t.q0 + t.row0);
+    load_tile<C::kChunks>(sq, &maps.q, &bar.qg_full, h, t.q0 + t.row0);
     load_k(0);
-    load_tile<C::kChunks>(sg, &mg, &bar.qg_full, h, t.q0 + t.row0);
+    load_tile<C::kChunks>(sg, &maps.g, &bar.qg_full, h, t.q0 + t.row0);
     load_v(0);
   }
   fence_before();
@@ -710,7 +699,7 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
     if (ok && part < DP / 64) {
       fence_after();
       const int row0 = t.row0 + (warp & 3) * 32;
-      store_64(smem + (warp - 4) * 8192, p.gq, p.g_bf16, wide, t.q0 + row0,
+      store_64(smem + (warp - 4) * 8192, p.gq, p.g_bf16, maps.wide_q, t.q0 + row0,
                max(0, min(32, t.nq - row0)), h, 64 * part, p.D, tmem + C::kQ + lanes, n == 0, n == 0,
                p.scale);
     }
@@ -724,6 +713,24 @@ __global__ void __launch_bounds__(QueriesCfg<DP, kN>::kThreads, QueriesCfg<DP, k
   }
 }
 
+// ---------------------------------------------------------------------------
+// Kernels
+// ---------------------------------------------------------------------------
+// Both in one launch, the keys' CTAs first (they are alike in threads, and
+// nearly in shared memory): what one leaves of the SMs the other takes.  One
+// after the other 64 x 197 (12 heads of 64) took 110 us with the rows' pass where
+// this takes 103, one sequence of 300 (8 heads of 64) 18 where this takes 11.
+template <int DP, bool kSplit>
+__global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
+    attn_bwd_tc_kernel(const Attn p, const __grid_constant__ Maps keys,
+                       const __grid_constant__ Maps queries, uint32_t keys_ctas, uint32_t ctas,
+                       int log_split) {
+  if (blockIdx.x < keys_ctas)
+    keys_body<DP, kSplit>(p, keys, blockIdx.x, log_split);
+  else if (!kSplit || blockIdx.x < ctas)  // whole clusters are launched
+    queries_body<DP>(p, queries, blockIdx.x - keys_ctas);
+}
+
 // Rows of g [T, H, D] of whole 16 bytes.
 int wide_rows(const Heads& g, bool bf16, int64_t T, int64_t H, int64_t D) {
   const int64_t per = bf16 ? 8 : 4;
@@ -731,11 +738,11 @@ int wide_rows(const Heads& g, bool bf16, int64_t T, int64_t H, int64_t D) {
          (T <= 1 || g.token % per == 0) && (H <= 1 || g.head % per == 0);
 }
 
-struct Maps {
-  CUtensorMap q, k, v, g;
-};
 bool make_maps(Maps* m, const Attn& p, int rows_q, int rows_k) {
   const Heads& g = p.gout16.p ? p.gout16 : p.gout;
+  m->wide_q = wide_rows(p.gq, p.g_bf16, p.Tq, p.Hq, p.D);
+  m->wide_k = wide_rows(p.gk, p.g_bf16, p.Tk, p.Hk, p.D);
+  m->wide_v = wide_rows(p.gv, p.g_bf16, p.Tk, p.Hk, p.D);
   return heads_map(&m->q, p.q, p.Tq, p.Hq, p.D, rows_q) &&
          heads_map(&m->k, p.k, p.Tk, p.Hk, p.D, rows_k) &&
          heads_map(&m->v, p.v, p.Tk, p.Hk, p.D, rows_k) &&
@@ -743,18 +750,22 @@ bool make_maps(Maps* m, const Attn& p, int rows_q, int rows_k) {
 }
 
 template <int DP, bool kSplit>
-cudaError_t launch_keys(const Attn& p, int log_split, cudaStream_t st) {
-  using C = KeysCfg<DP>;
-  const int64_t grid = most_tiles(p, true, kRows) * p.Hk << log_split;
-  if (grid == 0) return cudaSuccess;
-  Maps m;
-  if (!make_maps(&m, p, C::kN, kRows)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<attn_bwd_keys_tc_kernel<DP, kSplit>>(C::kSmem);
+cudaError_t launch(const Attn& p, int log_split, cudaStream_t st) {
+  using K = KeysCfg<DP>;
+  using Q = QueriesCfg<DP>;
+  constexpr size_t kSmem = K::kSmem > Q::kSmem ? K::kSmem : Q::kSmem;
+  const int64_t keys = most_tiles(p, true, kRows) * p.Hk << log_split;
+  const int64_t ctas = keys + most_tiles(p, false, kRows) * p.Hq;
+  if (ctas == 0) return cudaSuccess;
+  Maps mk, mq;
+  if (!make_maps(&mk, p, K::kN, kRows) || !make_maps(&mq, p, kRows, Q::kN))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem<attn_bwd_tc_kernel<DP, kSplit>>(kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = dim3((unsigned)(((ctas - 1) >> log_split) + 1) << log_split);
+  cfg.blockDim = dim3(K::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -764,23 +775,8 @@ cudaError_t launch_keys(const Attn& p, int log_split, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kSplit ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_bwd_keys_tc_kernel<DP, kSplit>, p, m.q, m.k, m.v, m.g,
-                            wide_rows(p.gk, p.g_bf16, p.Tk, p.Hk, p.D),
-                            wide_rows(p.gv, p.g_bf16, p.Tk, p.Hk, p.D), log_split);
-}
-
-template <int DP, int kN>
-cudaError_t launch_queries(const Attn& p, cudaStream_t st) {
-  using C = QueriesCfg<DP, kN>;
-  const int64_t grid = most_tiles(p, false, kRows) * p.Hq;
-  if (grid == 0) return cudaSuccess;
-  Maps m;
-  if (!make_maps(&m, p, kRows, kN)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<attn_bwd_queries_tc_kernel<DP, kN>>(C::kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attn_bwd_queries_tc_kernel<DP, kN>, dim3((unsigned)grid), dim3(C::kThreads),
-                    C::kSmem, st, p, m.q, m.k, m.v, m.g,
-                    wide_rows(p.gq, p.g_bf16, p.Tq, p.Hq, p.D));
+  return cudaLaunchKernelEx(&cfg, attn_bwd_tc_kernel<DP, kSplit>, p, mk, mq, (uint32_t)keys,
+                            (uint32_t)ctas, log_split);
 }
 
 }  // namespace
@@ -788,26 +784,21 @@ cudaError_t launch_queries(const Attn& p, cudaStream_t st) {
 bool attn_bwd_tc(const Attn& p) {
   return attn_tc(p) && (!p.gout_bf16 || tma_heads(p.gout, p.Tq, p.Hq));
 }
-cudaError_t launch_attn_bwd_keys_tc(const Attn& p, cudaStream_t st) {
-  const int64_t ctas = most_tiles(p, true, kRows) * p.Hk;
-  // A cluster for a tile only where there are fewer tiles than SMs twice: one
-  // sequence of 16384 (4 heads of 128 that share one; causal) 938 -> 601 us for
-  // the whole backward pass, but 8 of 2048 (16 heads, 4 shared ones) 409 -> 459.
+
+cudaError_t launch_attn_bwd_tc(const Attn& p, cudaStream_t st) {
+  // A cluster for a tile of keys only where there are fewer tiles than SMs twice
+  // and each has eight tiles of queries or more: one sequence of 16384 (4 heads of
+  // 128 that share one; causal) 738 -> 601 us, 5 of 400 (8 heads of 64 that share
+  // one) 57 -> 30; but 8 of 2048 (16 heads of 128, 4 shared ones) 409 -> 459, 40
+  // of 60 (4 heads of 64, 2 shared ones) 12 -> 20.
+  const int64_t tiles = most_tiles(p, true, kRows) * p.Hk, n = p.D <= 64 ? 64 : 128;
+  const int64_t each = (p.Tq / p.batch + n - 1) / n * p.group;
   int split = 0;
-  while (split < 3 && 2 << split <= p.group && ctas << split < 2 * (int64_t)device_sm_count())
-    ++split;
-  if (split > 0)
-    return p.D <= 64 ? launch_keys<64, true>(p, split, st) : launch_keys<128, true>(p, split, st);
-  return p.D <= 64 ? launch_keys<64, false>(p, 0, st) : launch_keys<128, false>(p, 0, st);
-}
-cudaError_t launch_attn_bwd_queries_tc(const Attn& p, cudaStream_t st) {
-  // Tiles of 64 keys and two CTAs an SM, but for few or long CTAs: 24 packed
-  // sequences (16 heads of 80) 59 us against 76 with tiles of 128, 64 x 197 (12
-  // heads of 64) 45 against 62; one sequence of 16384 (4 heads of 128; with the
-  // keys' pass) 981 against 935, one of 2048 63 against 52.
-  if (p.Tk / p.batch >= 4096 || most_tiles(p, false, kRows) * p.Hq < 2 * device_sm_count())
-    return p.D <= 64 ? launch_queries<64, 128>(p, st) : launch_queries<128, 128>(p, st);
-  return p.D <= 64 ? launch_queries<64, 64>(p, st) : launch_queries<128, 64>(p, st);
+  if (each >= 8)
+    while (split < 3 && 2 << split <= p.group && tiles << split < 2 * (int64_t)device_sm_count())
+      ++split;
+  if (split > 0) return p.D <= 64 ? launch<64, true>(p, split, st) : launch<128, true>(p, split, st);
+  return p.D <= 64 ? launch<64, false>(p, 0, st) : launch<128, false>(p, 0, st);
 }
 
 }  // namespace hlq

@@ -286,8 +286,7 @@ cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st);
 // delta, lse2 and g_out as bf16 (where p.gout16 has room for it)
 cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st);
 bool attn_bwd_tc(const Attn& p);
-cudaError_t launch_attn_bwd_keys_tc(const Attn& p, cudaStream_t st);
-cudaError_t launch_attn_bwd_queries_tc(const Attn& p, cudaStream_t st);
+cudaError_t launch_attn_bwd_tc(const Attn& p, cudaStream_t st);
 cudaError_t launch_attn_bwd_keys_simt(const Attn& p, cudaStream_t st);
 cudaError_t launch_attn_bwd_queries_simt(const Attn& p, cudaStream_t st);
 
