@@ -181,12 +181,10 @@ hlq_status hlq_attention_backward(const hlq_heads* g_out, int gout_dt, const hlq
   const bool tc = attn_bwd_tc(p);
   if (tc && !p.gout_bf16) p.gout16 = {ws + w.gout16, Hq * w.head16, w.head16};
   if (Tq > 0) HLQ_LAUNCH("attn_bwd_rows", s, launch_attn_bwd_rows(p, s));
-  if (tc) {
+  if (tc)
     HLQ_LAUNCH("attn_bwd_tc", s, launch_attn_bwd_tc(p, s));
-    return HLQ_OK;
-  }
-  if (Tk > 0) HLQ_LAUNCH("attn_bwd_keys", s, launch_attn_bwd_keys_simt(p, s));
-  if (Tq > 0) HLQ_LAUNCH("attn_bwd_queries", s, launch_attn_bwd_queries_simt(p, s));
+  else
+    HLQ_LAUNCH("attn_bwd", s, launch_attn_bwd_simt(p, s));
   return HLQ_OK;
 }
 

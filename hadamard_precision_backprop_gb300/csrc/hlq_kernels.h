@@ -287,8 +287,7 @@ cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st);
 cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st);
 bool attn_bwd_tc(const Attn& p);
 cudaError_t launch_attn_bwd_tc(const Attn& p, cudaStream_t st);
-cudaError_t launch_attn_bwd_keys_simt(const Attn& p, cudaStream_t st);
-cudaError_t launch_attn_bwd_queries_simt(const Attn& p, cudaStream_t st);
+cudaError_t launch_attn_bwd_simt(const Attn& p, cudaStream_t st);
 
 struct Dropout {
   const void *x, *residual;  // residual may be null; it has y's type
