@@ -269,80 +269,98 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
 // probabilities are 0.  With p.gout16 g_out rounded to bf16 as well.  What rows of
 // no sequence give is used nowhere.
 //
-// With kWide kLanes lanes have eight of a row's elements each, 16 bytes (32) at
-// a time, a warp has some heads of a token one after the other, and a CTA eight
-// tokens, whose values it stores together: 45 us for 16384 tokens x 32 heads of
-// 128 in bf16 (268 MB; 0.89 of the copy rate), against 97 with a warp on several
-// tokens of a head and 71 with single elements.  Else kLanes lanes have the
-// elements of a row in turn.
-template <bool kWide, int kLanes>
+// kLanes lanes have eight of a row's elements each, 16 bytes (32) at a time, a
+// warp has some heads of a token one after the other, and a CTA eight tokens,
+// whose values it stores together: 44 us for 16384 tokens x 32 heads of 128 in bf16
+// (268 MB: 0.9 of the copy rate), against 72 with the elements widened as they
+// come (fewer CTAs an SM) and 97 with a warp on several tokens of one head.
+template <bool kG, bool kO, int kLanes>
 __global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const Attn p) {
+  constexpr int kRows = 4, kGroups = 32 / kLanes, kHeads = kRows * kGroups;
+  __shared__ float all[2][kHeads][8 + 1];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % kLanes;
+  const uint32_t blocks = (p.Hq + kHeads - 1) / kHeads, group = blockIdx.x / blocks;
+  const int h0 = (int)(blockIdx.x - group * blocks) * kHeads;
+  const int64_t t0 = (int64_t)group * 8, t = t0 + warp;
+  const bool here = t < p.Tq && 8 * part < p.D;
+  // as they come, and all on their way before the first is widened
+  uint4 g[kRows][kG ? 1 : 2], o[kRows][kO ? 1 : 2];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int h = h0 + r * kGroups + lane / kLanes;
+    if (here && h < p.Hq) {
+      const int64_t at = t * p.gout.token + h * p.gout.head + 8 * part;
+      const int64_t ao = t * p.out.token + h * p.out.head + 8 * part;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p.gout.p) + at * (kG ? 2 : 4));
+      const uint4* u = reinterpret_cast<const uint4*>(static_cast<const char*>(p.out.p) + ao * (kO ? 2 : 4));
+#pragma unroll
+      for (int k = 0; k < (kG ? 1 : 2); ++k) g[r][k] = q[k];
+#pragma unroll
+      for (int k = 0; k < (kO ? 1 : 2); ++k) o[r][k] = u[k];
+    }
+  }
+  if (lane < kHeads && t < p.Tq && h0 + lane < p.Hq) {
+    const float lse = p.lse[t * p.Hq + h0 + lane];
+    all[1][lane][warp] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  }
+  const auto floats = [](const uint4* v) {
+    return join8(*reinterpret_cast<const float4*>(v), *reinterpret_cast<const float4*>(v + 1));
+  };
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int h = h0 + r * kGroups + lane / kLanes;
+    float sum = 0.f;
+    if (here && h < p.Hq) {
+      F8 a, b;
+      if constexpr (kG) a = widen8(g[r][0]);
+      else a = floats(g[r]);
+      if constexpr (kO) b = widen8(o[r][0]);
+      else b = floats(o[r]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = fmaf(a.v[k], b.v[k], sum);
+      if (!kG && p.gout16.p)
+        store8(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + 8 * part, a);
+    }
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (part == 0) all[0][r * kGroups + lane / kLanes][warp] = sum;
+  }
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i < kHeads * 8 && h0 + i / 8 < p.Hq && t0 + i % 8 < p.Tq) {
+    const int64_t at = (int64_t)(h0 + i / 8) * p.Tq + t0 + i % 8;
+    p.delta[at] = all[0][i / 8][i % 8];
+    p.lse2[at] = all[1][i / 8][i % 8];
+  }
+}
+
+// The same for any alignment: eight lanes have the elements of a row in turn.
+__global__ void __launch_bounds__(256) attn_bwd_rows_any_kernel(const Attn p) {
+  constexpr int kLanes = 8;
   pdl_trigger();
   pdl_wait();
   const int part = threadIdx.x % kLanes;
-  if constexpr (kWide) {
-    constexpr int kRows = 4, kGroups = 32 / kLanes, kHeads = kRows * kGroups;
-    __shared__ float all[2][kHeads][8 + 1];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t blocks = (p.Hq + kHeads - 1) / kHeads, group = blockIdx.x / blocks;
-    const int h0 = (int)(blockIdx.x - group * blocks) * kHeads;
-    const int64_t t0 = (int64_t)group * 8, t = t0 + warp;
-    const bool here = t < p.Tq && 8 * part < p.D;
-    F8 g[kRows], o[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int h = h0 + r * kGroups + lane / kLanes;
-      if (here && h < p.Hq) {
-        g[r] = load8(p.gout.p, p.gout_bf16, t * p.gout.token + h * p.gout.head + 8 * part);
-        o[r] = load8(p.out.p, p.bf16, t * p.out.token + h * p.out.head + 8 * part);
-      }
-    }
-    if (lane < kHeads && t < p.Tq && h0 + lane < p.Hq) {
-      const float lse = p.lse[t * p.Hq + h0 + lane];
-      all[1][lane][warp] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  const int64_t first = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+  const bool there = first < (int64_t)p.Tq * p.Hq;
+  const int64_t t = there ? first / p.Hq : 0;
+  const int h = there ? (int)(first - t * p.Hq) : 0;
+  const int64_t go = t * p.gout.token + h * p.gout.head, oo = t * p.out.token + h * p.out.head;
+  float sum = 0.f;
+  if (there)
+    for (int d = part; d < p.D; d += kLanes) {
+      const float g = load_elem(p.gout.p, p.gout_bf16, go + d);
+      sum = fmaf(g, load_elem(p.out.p, p.bf16, oo + d), sum);
+      if (p.gout16.p)
+        store_elem(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + d, g);
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int h = h0 + r * kGroups + lane / kLanes;
-      float sum = 0.f;
-      if (here && h < p.Hq) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum = fmaf(g[r].v[k], o[r].v[k], sum);
-        if (p.gout16.p)
-          store8(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + 8 * part, g[r]);
-      }
-#pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (part == 0) all[0][r * kGroups + lane / kLanes][warp] = sum;
-    }
-    __syncthreads();
-    const int i = threadIdx.x;
-    if (i < kHeads * 8 && h0 + i / 8 < p.Hq && t0 + i % 8 < p.Tq) {
-      const int64_t at = (int64_t)(h0 + i / 8) * p.Tq + t0 + i % 8;
-      p.delta[at] = all[0][i / 8][i % 8];
-      p.lse2[at] = all[1][i / 8][i % 8];
-    }
-  } else {
-    const int64_t first = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-    const bool there = first < (int64_t)p.Tq * p.Hq;
-    const int64_t t = there ? first / p.Hq : 0;
-    const int h = there ? (int)(first - t * p.Hq) : 0;
-    const int64_t go = t * p.gout.token + h * p.gout.head, oo = t * p.out.token + h * p.out.head;
-    float sum = 0.f;
-    if (there)
-      for (int d = part; d < p.D; d += kLanes) {
-        const float g = load_elem(p.gout.p, p.gout_bf16, go + d);
-        sum = fmaf(g, load_elem(p.out.p, p.bf16, oo + d), sum);
-        if (p.gout16.p)
-          store_elem(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + d, g);
-      }
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (there && part == 0) {
-      const float lse = p.lse[first];
-      p.delta[(int64_t)h * p.Tq + t] = sum;
-      p.lse2[(int64_t)h * p.Tq + t] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-    }
+  for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (there && part == 0) {
+    const float lse = p.lse[first];
+    p.delta[(int64_t)h * p.Tq + t] = sum;
+    p.lse2[(int64_t)h * p.Tq + t] = lse == -INFINITY ? INFINITY : lse * kLog2e;
   }
 }
 
@@ -509,6 +527,17 @@ cudaError_t launch_bwd(const Attn& p, cudaStream_t st) {
                     st, p, (uint32_t)keys);
 }
 
+template <bool kG, bool kO>
+cudaError_t launch_rows(const Attn& p, cudaStream_t st) {
+  const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
+  const int64_t heads = 4 * (32 / lanes);
+  const unsigned grid = (unsigned)((p.Tq + (int64_t)7) / 8 * ((p.Hq + heads - 1) / heads));
+  return launch_pdl(lanes == 8    ? attn_bwd_rows_kernel<kG, kO, 8>
+                    : lanes == 16 ? attn_bwd_rows_kernel<kG, kO, 16>
+                                  : attn_bwd_rows_kernel<kG, kO, 32>,
+                    dim3(grid), dim3(256), 0, st, p);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st) {
@@ -534,16 +563,11 @@ cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st) {
            x.head % per == 0;
   };
   if (wide(p.gout, p.gout_bf16) && wide(p.out, p.bf16)) {
-    const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    const int64_t heads = 4 * (32 / lanes);
-    const unsigned grid = (unsigned)((p.Tq + (int64_t)7) / 8 * ((p.Hq + heads - 1) / heads));
-    return launch_pdl(lanes == 8    ? attn_bwd_rows_kernel<true, 8>
-                      : lanes == 16 ? attn_bwd_rows_kernel<true, 16>
-                                    : attn_bwd_rows_kernel<true, 32>,
-                      dim3(grid), dim3(256), 0, st, p);
+    return p.gout_bf16 ? (p.bf16 ? launch_rows<true, true>(p, st) : launch_rows<true, false>(p, st))
+                       : (p.bf16 ? launch_rows<false, true>(p, st) : launch_rows<false, false>(p, st));
   }
-  return launch_pdl(attn_bwd_rows_kernel<false, 8>, dim3((unsigned)((rows + 31) / 32)), dim3(256),
-                    0, st, p);
+  return launch_pdl(attn_bwd_rows_any_kernel, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, st,
+                    p);
 }
 
 }  // namespace hlq
