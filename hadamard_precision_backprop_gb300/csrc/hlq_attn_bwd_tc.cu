@@ -20,6 +20,12 @@
 //   S = Q K^T, D = G V^T, dS = P (D - delta), g_q += dS K
 // D has two places: it is there before the probabilities are.
 //
+// The products take G, P and dS in bf16.  Where g_out comes as fp32, its rounding
+// is the only one: P and dS are two bf16 numbers each (there is room for the second
+// beside the first), for three products more.  Errors relative to the gradients'
+// norm, with results in bf16 (64 x 197; their own rounding alone is 0.0017): 0.0031
+// with one number each, 0.0024 with two, and as much with a g_out of bf16 and one.
+//
 // In both, warp 0 loads, warp 2 clears rows behind a sequence's end, and the
 // warps from 4 on compute: a thread has a row and 32 columns of a tile.  The
 // products for one tile run while the probabilities of another are computed.
@@ -37,6 +43,22 @@ namespace {
 
 using namespace tc;
 
+// 32 probabilities or gradients of a row as bf16 pairs, in the first half of the
+// columns that they were computed from; with kTwo what the rounding left, as bf16
+// again, in the other half.
+template <bool kTwo>
+__device__ __forceinline__ void put_pairs(uint32_t at, const float (&v)[32]) {
+  uint32_t e[16], rest[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    e[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+    if (kTwo) rest[i] = bf16x2(v[2 * i] - bf16_lo(e[i]), v[2 * i + 1] - bf16_hi(e[i]));
+  }
+  st16(at, e);
+  if (kTwo) st16(at + 16, rest);
+  st_wait();
+}
+
 // By head size: rows of a tile of the other side, and the registers of the
 // warps that do not compute and of those that do (640 threads of 96 registers:
 // 128 x 64 + 512 x 104; 384 of 80: 128 x 48 + 256 x 96).
@@ -52,13 +74,17 @@ struct BwdCfg {
 };
 
 // P or dS as the first operand, 32 columns (two steps) in each 32 columns of
-// the fp32 tile that they were computed from.
-template <int kN>
+// the fp32 tile that they were computed from; with kTwo what their rounding left
+// as well.
+template <int kN, bool kTwo>
 __device__ __forceinline__ void product_of_parts(uint32_t d, uint32_t p, uint32_t b, uint32_t id,
                                                  bool add) {
 #pragma unroll
-  for (int k = 0; k < kN / 16; ++k)
-    mma_ts(d, p + (k >> 1) * 32 + (k & 1) * 8, desc(b + row_step(k)), id, add || k > 0);
+  for (int two = 0; two < (kTwo ? 2 : 1); ++two)
+#pragma unroll
+    for (int k = 0; k < kN / 16; ++k)
+      mma_ts(d, p + (k >> 1) * 32 + (k & 1) * 8 + 16 * two, desc(b + row_step(k)), id,
+             add || k > 0 || two > 0);
 }
 
 // What a pass reads, and whether the rows of its results are of whole 16 bytes.
@@ -92,7 +118,7 @@ static_assert(sizeof(KeysBars) <= 512, "barriers fit their 512 bytes");
 // With kSplit a cluster of 2^log_split CTAs has the tile of keys, each some of
 // the query heads; they add up their sums through each other's shared memory, in
 // the order of their ranks.
-template <int DP, bool kSplit>
+template <int DP, bool kSplit, bool kTwo>
 __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint32_t block,
                                           int log_split) {
   using C = KeysCfg<DP>;
@@ -257,7 +283,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          product_of_parts<C::kN>(tmem + C::kV, tmem + C::kS, rg + s * kStep, id, it > 0);
+          product_of_parts<C::kN, kTwo>(tmem + C::kV, tmem + C::kS, rg + s * kStep, id, it > 0);
           if (reused) commit(&bar.g_empty[s]);
         }
         __syncwarp();
@@ -272,7 +298,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          product_of_parts<C::kN>(tmem + C::kK, tmem + C::kD, rq + s * kStep, id, it > 0);
+          product_of_parts<C::kN, kTwo>(tmem + C::kK, tmem + C::kD, rq + s * kStep, id, it > 0);
           if (reused) commit(&bar.q_empty[s]);
         }
         __syncwarp();
@@ -358,7 +384,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
       ok = __all_sync(0xffffffffu, wait(&bar.s_full, it));
       if (!ok) break;
       fence_after();
-      uint32_t x[32], e[16];
+      uint32_t x[32];
       float prob[32];
       ld32(ts, x);
       ld_wait(x);
@@ -372,10 +398,8 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
       for (int i = 0; i < 32; i += 2) {
         const float2 a = split(f2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])) * c22);
         prob[i] = exp2_fast(a.x), prob[i + 1] = exp2_fast(a.y);
-        e[i / 2] = bf16x2(prob[i], prob[i + 1]);
       }
-      st16(ts, e);
-      st_wait();
+      put_pairs<kTwo>(ts, prob);
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full);
@@ -385,11 +409,12 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
       ld32(td, x);
       ld_wait(x);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2)
-        e[i / 2] = pack_bf16(f2(prob[i], prob[i + 1]) *
-                             f2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-      st16(td, e);
-      st_wait();
+      for (int i = 0; i < 32; i += 2) {
+        const float2 a = split(f2(prob[i], prob[i + 1]) *
+                               f2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+        prob[i] = a.x, prob[i + 1] = a.y;
+      }
+      put_pairs<kTwo>(td, prob);
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ds_full);
@@ -480,7 +505,7 @@ struct QueriesBars {
 };
 static_assert(sizeof(QueriesBars) <= 512, "barriers fit their 512 bytes");
 
-template <int DP>
+template <int DP, bool kTwo>
 __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, uint32_t block) {
   using C = QueriesCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
@@ -619,7 +644,7 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
           if (!ok) break;
           fence_after();
           if (elect_one()) {
-            product_of_parts<C::kN>(tmem + C::kQ, tmem + C::kD + C::kN * (j % C::kDs), rk + s * kStep, id, j > 0);
+            product_of_parts<C::kN, kTwo>(tmem + C::kQ, tmem + C::kD + C::kN * (j % C::kDs), rk + s * kStep, id, j > 0);
             if (j + C::kDs < n) commit(&bar.d_empty[j % C::kDs]);
             if (j + C::kStagesK < n) commit(&bar.k_empty[s]);
           }
@@ -658,7 +683,7 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
       ok = __all_sync(0xffffffffu, wait(&bar.s_full, j));
       if (!ok) break;
       fence_after();
-      uint32_t x[32], e[16];
+      uint32_t x[32];
       float prob[32];
       ld32(ts, x);
       ld_wait(x);
@@ -687,10 +712,7 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
         for (int i = 0; i < 32; ++i)
           if (i >= sees - j0) ds[i] = 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) e[i / 2] = bf16x2(ds[i], ds[i + 1]);
-      st16(td + C::kN * (j % C::kDs), e);
-      st_wait();
+      put_pairs<kTwo>(td + C::kN * (j % C::kDs), ds);
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ds_full[j % C::kDs]);
@@ -720,15 +742,15 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
 // nearly in shared memory): what one leaves of the SMs the other takes.  One
 // after the other 64 x 197 (12 heads of 64) took 110 us with the rows' pass where
 // this takes 103, one sequence of 300 (8 heads of 64) 18 where this takes 11.
-template <int DP, bool kSplit>
+template <int DP, bool kSplit, bool kTwo>
 __global__ void __launch_bounds__(BwdCfg<DP>::kThreads, BwdCfg<DP>::kCtas)
     attn_bwd_tc_kernel(const Attn p, const __grid_constant__ Maps keys,
                        const __grid_constant__ Maps queries, uint32_t keys_ctas, uint32_t ctas,
                        int log_split) {
   if (blockIdx.x < keys_ctas)
-    keys_body<DP, kSplit>(p, keys, blockIdx.x, log_split);
+    keys_body<DP, kSplit, kTwo>(p, keys, blockIdx.x, log_split);
   else if (!kSplit || blockIdx.x < ctas)  // whole clusters are launched
-    queries_body<DP>(p, queries, blockIdx.x - keys_ctas);
+    queries_body<DP, kTwo>(p, queries, blockIdx.x - keys_ctas);
 }
 
 // Rows of g [T, H, D] of whole 16 bytes.
@@ -749,7 +771,7 @@ bool make_maps(Maps* m, const Attn& p, int rows_q, int rows_k) {
          heads_map(&m->g, g, p.Tq, p.Hq, p.D, rows_q);
 }
 
-template <int DP, bool kSplit>
+template <int DP, bool kSplit, bool kTwo>
 cudaError_t launch(const Attn& p, int log_split, cudaStream_t st) {
   using K = KeysCfg<DP>;
   using Q = QueriesCfg<DP>;
@@ -760,7 +782,7 @@ cudaError_t launch(const Attn& p, int log_split, cudaStream_t st) {
   Maps mk, mq;
   if (!make_maps(&mk, p, K::kN, kRows) || !make_maps(&mq, p, kRows, Q::kN))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<attn_bwd_tc_kernel<DP, kSplit>>(kSmem);
+  cudaError_t e = allow_smem<attn_bwd_tc_kernel<DP, kSplit, kTwo>>(kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((ctas - 1) >> log_split) + 1) << log_split);
@@ -775,8 +797,14 @@ cudaError_t launch(const Attn& p, int log_split, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kSplit ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_bwd_tc_kernel<DP, kSplit>, p, mk, mq, (uint32_t)keys,
+  return cudaLaunchKernelEx(&cfg, attn_bwd_tc_kernel<DP, kSplit, kTwo>, p, mk, mq, (uint32_t)keys,
                             (uint32_t)ctas, log_split);
+}
+
+template <int DP, bool kSplit>
+cudaError_t launch_types(const Attn& p, int log_split, cudaStream_t st) {
+  return p.gout16.p ? launch<DP, kSplit, true>(p, log_split, st)
+                    : launch<DP, kSplit, false>(p, log_split, st);
 }
 
 }  // namespace
@@ -797,8 +825,9 @@ cudaError_t launch_attn_bwd_tc(const Attn& p, cudaStream_t st) {
   if (each >= 8)
     while (split < 3 && 2 << split <= p.group && tiles << split < 2 * (int64_t)device_sm_count())
       ++split;
-  if (split > 0) return p.D <= 64 ? launch<64, true>(p, split, st) : launch<128, true>(p, split, st);
-  return p.D <= 64 ? launch<64, false>(p, 0, st) : launch<128, false>(p, 0, st);
+  if (split > 0)
+    return p.D <= 64 ? launch_types<64, true>(p, split, st) : launch_types<128, true>(p, split, st);
+  return p.D <= 64 ? launch_types<64, false>(p, 0, st) : launch_types<128, false>(p, 0, st);
 }
 
 }  // namespace hlq

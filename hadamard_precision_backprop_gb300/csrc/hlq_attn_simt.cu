@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
   store_rows<DP, RM>(p.out, p.bf16, t.q0 + t.row0, n, h, p.D, ty, tx, 1.f, acc);
 }
 
-// delta = g_out . out, and lse in units of log 2, both [Hq, Tq] (a tile's
+// delta = g_out . out (of g_out as bf16 where the products take it so: the gradients
+// are then exactly those of the rounded g_out), and lse in units of log 2, both [Hq, Tq] (a tile's
 // values are together); +infinity for a row that sees nothing, so that all its
 // probabilities are 0.  With p.gout16 g_out rounded to bf16 as well.  What rows of
 // no sequence give is used nowhere.
@@ -318,10 +319,14 @@ __global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const Attn p) {
       else a = floats(g[r]);
       if constexpr (kO) b = widen8(o[r][0]);
       else b = floats(o[r]);
+      if (!kG && p.gout16.p) {
+        const int64_t at = t * p.gout16.token + h * p.gout16.head + 8 * part;
+        store8(p.gout16.p, true, at, a);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a.v[k] = __bfloat162float(__float2bfloat16_rn(a.v[k]));
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum = fmaf(a.v[k], b.v[k], sum);
-      if (!kG && p.gout16.p)
-        store8(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + 8 * part, a);
     }
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -350,10 +355,12 @@ __global__ void __launch_bounds__(256) attn_bwd_rows_any_kernel(const Attn p) {
   float sum = 0.f;
   if (there)
     for (int d = part; d < p.D; d += kLanes) {
-      const float g = load_elem(p.gout.p, p.gout_bf16, go + d);
-      sum = fmaf(g, load_elem(p.out.p, p.bf16, oo + d), sum);
-      if (p.gout16.p)
+      float g = load_elem(p.gout.p, p.gout_bf16, go + d);
+      if (p.gout16.p) {
         store_elem(p.gout16.p, true, t * p.gout16.token + h * p.gout16.head + d, g);
+        g = __bfloat162float(__float2bfloat16_rn(g));
+      }
+      sum = fmaf(g, load_elem(p.out.p, p.bf16, oo + d), sum);
     }
 #pragma unroll
   for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

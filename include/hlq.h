@@ -710,8 +710,9 @@ hlq_status hlq_attention(const hlq_heads *q, const hlq_heads *k, const hlq_heads
  * g_out [Tq, Hq, D] of either dtype (gout_dt); q, k, v, out of dtype dt; g_q, g_k,
  * g_v of either dtype (g_dt); they may be parts of one [T, (Hq + 2 Hk) D] tensor.
  * Rows of no sequence have gradients of 0, and so have queries that see nothing.
- * bf16 on the tensor cores as above: g_out, p and ds are rounded to bf16 for
- * their products (also where the gradients are fp32); all sums are fp32.
+ * bf16 on the tensor cores as above: g_out is rounded to bf16 for its products
+ * (also where the gradients are fp32), and p and ds are unless g_out is fp32 (then
+ * they enter as two bf16 numbers each, 16 bits); all sums are fp32.
  * Infinities and NaN in a sequence may reach all its gradients, and no others.
  * Workspace: hlq_attention_backward_workspace_bytes.
  */

@@ -83,7 +83,8 @@ def backward(g, q, k, v, out, lse, lens_q, lens_k, first_q, first_k, causal, sca
         delta = (gg * out[rq]).sum(-1).t()[..., None]
         delta_size = (gg * out[rq]).abs().sum(-1).t()[..., None]
         ds = p * (dp - delta)
-        ds_off = (u + off) * ds.abs() + p * (u_g * dp_size + (D + 4) * F32 * (dp_size + delta_size))
+        # a rounded g_out meets v - out: sum |g| |v - out| <= sum |g| |v| + sum |g| |out|
+        ds_off = (u + off) * ds.abs() + p * ((u_g + (D + 4) * F32) * (dp_size + delta_size))
         res[2][rk] = shared(torch.einsum("hij,ihd->jhd", p, gg))
         n = (nq * group + 8) * F32
         tol[2][rk] = shared(torch.einsum("hij,ihd->jhd", (u + u_g + off + n) * p, gg.abs()))
