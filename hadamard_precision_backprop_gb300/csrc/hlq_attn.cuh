@@ -56,13 +56,21 @@ __device__ __forceinline__ int find_tile(const Attn& p, int t, AttnTile& o) {
   const int32_t* seqs = kKeys ? p.seqs_k : p.seqs_q;
   const int lane = threadIdx.x & 31;
   bool bad = false;
+  int next[4] = {0, 0, 0, 0};  // tiles of the lane's sequences, of four steps at a time
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0;
-    if (b < p.batch) {
-      const int2 r = seq_rows(seqs, b, T, bad);
-      n = (r.y - r.x + rows - 1) / rows;
+    if (b0 % 128 == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int b = b0 + 32 * k + lane;
+        next[k] = 0;
+        if (b < p.batch) {
+          const int2 r = seq_rows(seqs, b, T, bad);
+          next[k] = (r.y - r.x + rows - 1) / rows;
+        }
+      }
     }
+    const int n = next[0];
+    next[0] = next[1], next[1] = next[2], next[2] = next[3];
     const int all = __reduce_add_sync(0xffffffffu, n);
     if (t < all) {
       int first, index;  // the sequence's lane, and the tile of it
@@ -108,7 +116,8 @@ inline int64_t most_tiles(const Attn& p, bool keys, int rows) {
 }
 
 // Rows of chunk `chunk` of the rows that belong to no sequence (before the
-// first and behind the last): calls f(row) for this thread's.
+// first and behind the last): calls f(row, d) for this thread's elements, d from
+// 0 to D - 1.
 template <bool kKeys, typename F>
 __device__ __forceinline__ void outside_rows(const Attn& p, int rows, int chunk, int thread,
                                              int threads, F&& f) {
@@ -118,10 +127,12 @@ __device__ __forceinline__ void outside_rows(const Attn& p, int rows, int chunk,
   bool bad = false;
   const int front = seq_rows(seqs, 0, T, bad).x;
   const int back = max(front, seq_rows(seqs, p.batch - 1, T, bad).y);
-  const int64_t n = (int64_t)front + (T - back);
   const int64_t first = (int64_t)chunk * rows;
-  for (int64_t i = first + thread; i < first + rows && i < n; i += threads)
-    f((int)(i < front ? i : back + (i - front)));
+  const int n = (int)min((int64_t)rows, (int64_t)front + (T - back) - first);
+  for (int e = thread; e < n * p.D; e += threads) {
+    const int64_t i = first + e / p.D;
+    f((int)(i < front ? i : back + (i - front)), e % p.D);
+  }
 }
 
 // Keys that query i of a tile's sequence sees: the last query sees all of

@@ -219,11 +219,9 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
 
   if (past >= 0) {
-    outside_rows<true>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row) {
-      for (int d = 0; d < p.D; ++d) {
-        store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
-        store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
-      }
+    outside_rows<true>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+      store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
+      store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
     });
   } else if (warp < 4) {
     fewer_registers<C::kFewer>();
@@ -351,7 +349,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
         for (int i = 0; i < C::kN / 32; ++i)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float x = k == 0 ? fmaxf(-3e38f, -v[0][i] * back) : -v[1][i];
+            const float x = k == 0 ? fminf(3e38f, fmaxf(-3e38f, -v[0][i] * back)) : -v[1][i];
             const float hi = __bfloat162float(__float2bfloat16_rn(x));
             const float mid = __bfloat162float(__float2bfloat16_rn(x - hi));
             *reinterpret_cast<uint2*>(stats + (2 * u + k) * C::kMoreN + more_at(32 * i + lane)) =
@@ -589,9 +587,8 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
 
   if (past >= 0) {
-    outside_rows<false>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row) {
-      for (int d = 0; d < p.D; ++d)
-        store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
+    outside_rows<false>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+      store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
     });
   } else if (warp < 4) {
     fewer_registers<C::kFewer>();

@@ -117,10 +117,9 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
   const int rest = n > 0 && t.nk < n * kRows ? t.nk - (n - 1) * kRows : 0;
 
   if (past >= 0) {
-    outside_rows<false>(p, kQ * kRows, past, threadIdx.x, C::kThreads, [&](int row) {
-      p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
-      for (int d = 0; d < p.D; ++d)
-        store_elem(p.out.p, true, row * p.out.token + h * p.out.head + d, 0.f);
+    outside_rows<false>(p, kQ * kRows, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+      if (d == 0) p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
+      store_elem(p.out.p, true, row * p.out.token + h * p.out.head + d, 0.f);
     });
   } else if (warp < 4) {
    fewer_registers<C::kFewer>();

@@ -199,10 +199,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
   AttnTile t;
   const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {  // rows of no sequence
-    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
-      p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
-      for (int d = 0; d < p.D; ++d)
-        store_elem(p.out.p, p.bf16, row * p.out.token + h * p.out.head + d, 0.f);
+    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row, int d) {
+      if (d == 0) p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
+      store_elem(p.out.p, p.bf16, row * p.out.token + h * p.out.head + d, 0.f);
     });
     return;
   }
@@ -387,11 +386,9 @@ __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
   AttnTile t;
   const int past = find_tile<true, BM>(p, (int)tile, t);
   if (past >= 0) {
-    outside_rows<true>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
-      for (int d = 0; d < p.D; ++d) {
-        store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
-        store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
-      }
+    outside_rows<true>(p, BM, past, threadIdx.x, kThreads, [&](int row, int d) {
+      store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
+      store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
     });
     return;
   }
@@ -459,9 +456,8 @@ __device__ __forceinline__ void queries_body(const Attn& p, uint32_t block) {
   AttnTile t;
   const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {
-    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row) {
-      for (int d = 0; d < p.D; ++d)
-        store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
+    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row, int d) {
+      store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
     });
     return;
   }

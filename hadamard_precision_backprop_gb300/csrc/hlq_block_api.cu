@@ -48,7 +48,8 @@ hlq_status check_sizes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D
 // The checks that both passes share, after check_sizes.
 hlq_status check_seqs(int64_t Tq, int64_t Tk, int64_t batch, const int32_t* seqs,
                       const int32_t* seqs_k, float scale) {
-  if (!(scale > 0.f) || std::isinf(scale)) return HLQ_ERR_INVALID_ARG;
+  // beyond these its product with log2(e), or the inverse, may leave fp32's range
+  if (!(scale >= 0x1p-64f && scale <= 0x1p64f)) return HLQ_ERR_INVALID_ARG;
   if (!seqs && seqs_k) return HLQ_ERR_INVALID_ARG;
   if (!seqs && (Tq % batch != 0 || Tk % batch != 0)) return HLQ_ERR_SHAPE;
   if (seqs && !seqs_k && Tq != Tk) return HLQ_ERR_SHAPE;

@@ -693,7 +693,8 @@ typedef struct {
  * bytes; the probabilities are then rounded to bf16 for their product with v.
  * Maxima, sums and out are held in fp32 and out is rounded once.
  * Any other alignment or D: products in fp32, slower.
- * D <= 256; Tq Hq, Tk Hk < 2^31; (batch + 1) Hq < 2^30; scale > 0.
+ * D <= 256; Tq Hq, Tk Hk < 2^31; (batch + 1) Hq < 2^30; scale from 2^-64 to 2^64.
+ * No output may overlap an input.
  */
 hlq_status hlq_attention(const hlq_heads *q, const hlq_heads *k, const hlq_heads *v, int dt,
                          int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D,
@@ -710,6 +711,8 @@ hlq_status hlq_attention(const hlq_heads *q, const hlq_heads *k, const hlq_heads
  * g_out [Tq, Hq, D] of either dtype (gout_dt); q, k, v, out of dtype dt; g_q, g_k,
  * g_v of either dtype (g_dt); they may be parts of one [T, (Hq + 2 Hk) D] tensor.
  * Rows of no sequence have gradients of 0, and so have queries that see nothing.
+ * out, lse: what the forward pass gave for these inputs.  No output may overlap an
+ * input or an element of another output.
  * bf16 on the tensor cores as above: g_out is rounded to bf16 for its products
  * (also where the gradients are fp32), and p and ds are unless g_out is fp32 (then
  * they enter as two bf16 numbers each, 16 bits); all sums are fp32.

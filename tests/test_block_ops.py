@@ -53,6 +53,8 @@ def test_attention_validation(L, call):
     assert call(L, scale=-1.0) == 1
     assert call(L, scale=NAN) == 1
     assert call(L, scale=INF) == 1
+    assert call(L, scale=2.0 ** -65) == 1
+    assert call(L, scale=2.0 ** 65) == 1
     assert call(L, seqs_k=FAKE) == 1                    # offsets of the keys alone
     assert call(L, Tq=-1) == 2
     assert call(L, Hk=3) == 2
