@@ -166,6 +166,14 @@ def test_rows_of_no_sequence(causal, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_batch_that_is_mostly_padding(dtype):
+    """Two short sequences in 3000 rows; queries and keys with offsets of their own."""
+    c = Case(dtype, [5, 64], [130, 9], 4, 2, 64, True, front=700, back=2231)
+    c.check_forward(U[dtype])
+    c.check_backward(U[dtype], F32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("poison", [math.nan, math.inf])
 def test_a_sequence_of_nan_reaches_no_other(poison, dtype):
     """The sequence between two others holds NaN or infinities; tiles of 64 and 128 rows reach into it."""
@@ -197,6 +205,23 @@ def test_large_scores(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 1e-6, 3.0])
+def test_scales(scale, dtype):
+    c = Case(dtype, [150], [150], 2, 1, 64, True, scale=scale)
+    c.check_forward(U[dtype])
+    c.check_backward(U[dtype], F32)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("heads", [(8, 1, 64), (7, 1, 128), (12, 2, 80), (3, 1, 64)], ids=str)
+def test_key_heads_that_many_share(heads, causal):
+    """Long enough that a tile of keys is shared out over a cluster, evenly or not."""
+    c = Case(BF16, [600, 70], [600, 70], *heads, causal)
+    c.check_backward(U[BF16], BF16)
+    c.check_backward(U[BF16], F32, F32, packed=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_scale_and_broadcast_inputs(dtype):
     """A scale of the caller's; one key head expanded to four (strides of 0)."""
     c = Case(dtype, [130, 40], [130, 40], 4, 4, 64, True, scale=0.3)
@@ -219,7 +244,7 @@ def test_equal_calls_give_equal_bits_and_offsets_do_not_matter(dtype):
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
-@pytest.mark.parametrize("many", [40, 1000])
+@pytest.mark.parametrize("many", [40, 129, 1000])
 def test_many_sequences(many):
     """More sequences than a warp looks at in one step, most of them short or empty."""
     lens = [(7 * i * i) % 11 + (150 if i % 97 == 5 else 0) for i in range(many)]
