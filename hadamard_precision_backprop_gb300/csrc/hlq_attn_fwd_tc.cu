@@ -1,20 +1,31 @@
 // hlq_attn_fwd_tc.cu -- attention's forward pass in bf16 on the tensor cores
 // (tcgen05, TMEM, TMA), heads up to 128.
 //
-// A CTA has two tiles of 128 queries of one head and goes over the keys' tiles
-// of 128.  Per tile of keys and of queries:
+// A CTA has one or two tiles of 128 queries of one head and goes over the keys'
+// tiles of 128.  Per tile of keys and of queries:
 //   S = Q K^T (TMEM, fp32)  ->  P = exp2(c S - c m), bf16, in the place of S
 //   O += P V (TMEM, fp32)
 // warp 0 loads (TMA), warps 1 and 3 issue the products of the first and of the
 // second tile of queries, warp 2 clears V's rows behind the sequence's end,
-// warps 4-7 and 8-11 are the softmax of the two tiles, a thread to a row: maximum
-// and sum need no shuffles.  While one tile's softmax runs, the products of the
-// other one do; the product with V begins when half of P is there.
+// warps 4-7 and 8-11 are the softmax of the tiles, a thread to a row: maximum and
+// sum need no shuffles.  While one tile's softmax runs, the products of the other
+// one do (of the same CTA, or of the SM's other CTA); the product with V begins
+// when half of P is there.
 //
 // m is the maximum of the tiles so far when it was last taken over; it is taken
 // over again only where the row's maximum has risen by more than 8 in units of
 // log 2 (P then stays below 2^8, which costs bf16 nothing), so that O is
 // rescaled rarely.  Sums are those of the unrounded probabilities, in fp32.
+//
+// What bounds it: a tile's chain of product, softmax and product, of which two
+// run side by side in an SM.  A step of 128 x 128 of a head of 128 is 1024 clocks
+// of the tensor pipe (64 for each 128 x 128 x 16) and, for each of the four
+// schedulers, 512 of exponentials (4 a warp) and about as many of multiplications,
+// maxima, sums and conversions; the reads and writes of TMEM and the waits between
+// them are what is left.  Tensor pipe busy for 46 % (4 sequences of 2048).
+// Causal, 32 heads of 128 with 8 of keys, 8 sequences of 2048: 258-266 us (1.03
+// to 1.07 PFLOP/s of the half that is not masked); 4 heads, one sequence of 16384:
+// 187-206 us, where the longest tile's 128 steps are the time.
 #include <cmath>
 #include <cstring>
 
@@ -122,101 +133,103 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
       store_elem(p.out.p, true, row * p.out.token + h * p.out.head + d, 0.f);
     });
   } else if (warp < 4) {
-   fewer_registers<C::kFewer>();
-   if (warp == 0) {
-    if (lane == 0 && n > 0) {
-      int k_done = 0, v_done = 0, q_done = 0, last_done = 0;
-      const auto load_q = [&](int g) {
-        mbar_expect_tx(&bar.q_full[g], C::kTile);
-        load_tile<C::kChunks>(sq + g * C::kTile, &mq, &bar.q_full[g], h, t.q0 + t.row0 + g * kRows);
-        ++q_done;
-      };
-      const auto load_k = [&](int j) {
-        const int s = j % C::kStages;
-        if (j >= C::kStages && !wait(&bar.k_empty[s], j / C::kStages - 1)) return false;
-        mbar_expect_tx(&bar.k_full[s], C::kTile);
-        load_tile<C::kChunks>(sk + s * C::kTile, &mk, &bar.k_full[s], hk, t.k0 + j * kRows);
-        ++k_done;
-        return true;
-      };
-      const auto load_v = [&](int j) {
-        const int s = j % C::kStages;
-        if (j >= C::kStages && !wait(&bar.v_empty[s], j / C::kStages - 1)) return false;
-        uint64_t* full = rest && j == n - 1 ? &bar.v_last : &bar.v_full[s];
-        mbar_expect_tx(full, C::kTile);
-        load_tile<C::kChunks>(sv + s * C::kTile, &mv, full, hk, t.k0 + j * kRows);
-        ++(full == &bar.v_last ? last_done : v_done);
-        return true;
-      };
-      load_q(0);
-      load_k(0);
-      if (tiles[1] > 0) load_q(1);
-      for (int j = 0; j < n; ++j)
-        if ((j > 0 && !load_k(j)) || !load_v(j)) break;
-      if (*abort_flag) {  // let the copies under way land
-        ring_drain(bar.q_full, 2, q_done);
-        ring_drain(bar.k_full, C::kStages, k_done);
-        ring_drain(bar.v_full, C::kStages, v_done);
-        ring_drain(&bar.v_last, 1, last_done);
-      }
-    }
-   } else if (warp == 1 || (kQ == 2 && warp == 3)) {  // the whole warp, of which one thread issues
-      const int g = warp >> 1;
-      const int steps = (p.D + 15) / 16;
-      const uint32_t id = idesc(16 * steps, true);
-      const uint32_t aq = by_columns(saddr(sq) + g * C::kTile), ak = by_columns(saddr(sk));
-      const uint32_t av = by_rows(saddr(sv)), ts = tmem + g * kRows, to = tmem + C::kO + g * DP;
-      constexpr uint32_t kStep = C::kTile >> 4;
-      bool ok = tiles[g] == 0 || wait(&bar.q_full[g], 0);
-      const auto scores = [&](int j) {
-        const int s = j % C::kStages;
-        ok = wait(&bar.k_full[s], j / C::kStages);
-        if (!ok) return;
-        fence_after();
-        if (elect_one()) {
-          product_of_rows<DP / 16>(ts, aq, ak + s * kStep, steps);
-          commit(&bar.s_full[g]);
-          if (j + C::kStages < n) commit(&bar.k_empty[s]);
+    fewer_registers<C::kFewer>();
+    if (warp == 0) {
+      if (lane == 0 && n > 0) {
+        int k_done = 0, v_done = 0, last_done = 0;
+        const auto load_q = [&](int g) {
+          mbar_expect_tx(&bar.q_full[g], C::kTile);
+          load_tile<C::kChunks>(sq + g * C::kTile, &mq, &bar.q_full[g], h,
+                                t.q0 + t.row0 + g * kRows);
+        };
+        const auto load_k = [&](int j) {
+          const int s = j % C::kStages;
+          if (j >= C::kStages && !wait(&bar.k_empty[s], j / C::kStages - 1)) return false;
+          mbar_expect_tx(&bar.k_full[s], C::kTile);
+          load_tile<C::kChunks>(sk + s * C::kTile, &mk, &bar.k_full[s], hk, t.k0 + j * kRows);
+          ++k_done;
+          return true;
+        };
+        const auto load_v = [&](int j) {
+          const int s = j % C::kStages;
+          if (j >= C::kStages && !wait(&bar.v_empty[s], j / C::kStages - 1)) return false;
+          uint64_t* full = rest && j == n - 1 ? &bar.v_last : &bar.v_full[s];
+          mbar_expect_tx(full, C::kTile);
+          load_tile<C::kChunks>(sv + s * C::kTile, &mv, full, hk, t.k0 + j * kRows);
+          ++(full == &bar.v_last ? last_done : v_done);
+          return true;
+        };
+        // only what is waited for: with fewer keys than queries the first tile of
+        // queries may see none
+        if (tiles[0] > 0) load_q(0);
+        load_k(0);
+        if (tiles[1] > 0) load_q(1);
+        for (int j = 0; j < n; ++j)
+          if ((j > 0 && !load_k(j)) || !load_v(j)) break;
+        if (*abort_flag) {  // let the copies under way land
+          for (int g = 0; g < kQ; ++g) ring_drain(&bar.q_full[g], 1, tiles[g] > 0);
+          ring_drain(bar.k_full, C::kStages, k_done);
+          ring_drain(bar.v_full, C::kStages, v_done);
+          ring_drain(&bar.v_last, 1, last_done);
         }
-        __syncwarp();
-      };
-      if (ok && tiles[g] > 0) scores(0);
-      for (int j = 0; j < tiles[g] && ok; ++j) {
-        const int s = j % C::kStages;
-        ok = rest && j == n - 1 ? wait(&bar.v_clear, 0) : wait(&bar.v_full[s], j / C::kStages);
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = wait(&bar.p_full[g][half], j);
-          if (!ok) break;
+      }
+    } else if (warp == 1 || (kQ == 2 && warp == 3)) {  // the whole warp, of which one thread issues
+        const int g = warp >> 1;
+        const int steps = (p.D + 15) / 16;
+        const uint32_t id = idesc(16 * steps, true);
+        const uint32_t aq = by_columns(saddr(sq) + g * C::kTile), ak = by_columns(saddr(sk));
+        const uint32_t av = by_rows(saddr(sv)), ts = tmem + g * kRows, to = tmem + C::kO + g * DP;
+        constexpr uint32_t kStep = C::kTile >> 4;
+        bool ok = tiles[g] == 0 || wait(&bar.q_full[g], 0);
+        const auto scores = [&](int j) {
+          const int s = j % C::kStages;
+          ok = wait(&bar.k_full[s], j / C::kStages);
+          if (!ok) return;
           fence_after();
           if (elect_one()) {
-            product_of_p(to, ts + 32 * half, av + s * kStep, id, half, j > 0 || half > 0);
-            if (half && j == tiles[g] - 1) commit(&bar.o_full[g]);
-            if (half && j + C::kStages < n) commit(&bar.v_empty[s]);
+            product_of_rows<DP / 16>(ts, aq, ak + s * kStep, steps);
+            commit(&bar.s_full[g]);
+            if (j + C::kStages < n) commit(&bar.k_empty[s]);
           }
           __syncwarp();
+        };
+        if (ok && tiles[g] > 0) scores(0);
+        for (int j = 0; j < tiles[g] && ok; ++j) {
+          const int s = j % C::kStages;
+          ok = rest && j == n - 1 ? wait(&bar.v_clear, 0) : wait(&bar.v_full[s], j / C::kStages);
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = wait(&bar.p_full[g][half], j);
+            if (!ok) break;
+            fence_after();
+            if (elect_one()) {
+              product_of_p(to, ts + 32 * half, av + s * kStep, id, half, j > 0 || half > 0);
+              if (half && j == tiles[g] - 1) commit(&bar.o_full[g]);
+              if (half && j + C::kStages < n) commit(&bar.v_empty[s]);
+            }
+            __syncwarp();
+          }
+          if (ok && j + 1 < tiles[g]) scores(j + 1);
         }
-        if (ok && j + 1 < tiles[g]) scores(j + 1);
-      }
-      // tiles of keys that the other tile of queries alone sees
-      for (int j = tiles[g]; j + C::kStages < n && ok; ++j) {
-        const int s = j % C::kStages;
-        ok = wait(&bar.k_full[s], j / C::kStages) && wait(&bar.v_full[s], j / C::kStages);
-        if (ok && lane == 0) {
-          mbar_arrive(&bar.k_empty[s]);
-          mbar_arrive(&bar.v_empty[s]);
+        // tiles of keys that the other tile of queries alone sees
+        for (int j = tiles[g]; j + C::kStages < n && ok; ++j) {
+          const int s = j % C::kStages;
+          ok = wait(&bar.k_full[s], j / C::kStages) && wait(&bar.v_full[s], j / C::kStages);
+          if (ok && lane == 0) {
+            mbar_arrive(&bar.k_empty[s]);
+            mbar_arrive(&bar.v_empty[s]);
+          }
         }
-      }
-      if (!ok && elect_one()) drain(&bar.drained[g]);
-      __syncwarp();
-   } else if (warp == 2) {
-    if (rest) {
-      const int s = (n - 1) % C::kStages;
-      if (wait(&bar.v_last, 0)) {
-        clear_rows<C::kChunks>(sv + s * C::kTile, rest);
-        if (lane == 0) mbar_arrive(&bar.v_clear);
+        if (!ok && elect_one()) drain(&bar.drained[g]);
+        __syncwarp();
+    } else if (warp == 2) {
+      if (rest) {
+        const int s = (n - 1) % C::kStages;
+        if (wait(&bar.v_last, 0)) {
+          clear_rows<C::kChunks>(sv + s * C::kTile, rest);
+          if (lane == 0) mbar_arrive(&bar.v_clear);
+        }
       }
     }
-   }
   } else {
     more_registers<C::kMore>();
     const int g = (warp - 4) >> 2;

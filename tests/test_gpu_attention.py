@@ -165,6 +165,44 @@ def test_rows_of_no_sequence(causal, D, dtype):
     c.check_backward(U[dtype], BF16, packed=True)
 
 
+@pytest.mark.parametrize("D", [64, 128, 72])
+@pytest.mark.parametrize("lens_q,lens_k,heads,causal", [
+    ([1150], [1150], (32, 8), True), ([1150], [1150], (32, 8), False), ([1024] * 5, [1024] * 5, (8, 4), True),
+    ([1280, 0, 130, 2600], [1280, 0, 130, 2600], (16, 2), True), ([300, 1025], [1900, 770], (31, 1), True),
+    ([1400], [1025], (26, 13), True)], ids=str)
+def test_long_sequences_of_many_heads(lens_q, lens_k, heads, causal, D):
+    """Two tiles of queries a CTA: the last with one or none of them, either of them seeing no key."""
+    varied = len(lens_q) in (2, 4)
+    c = Case(BF16, lens_q, lens_k, *heads, D, causal, front=3 * varied, back=200 * varied)
+    c.check_forward(U[BF16])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 100])
+def test_offsets_past_32_bits(D, dtype):
+    """Tokens 2^23 + 8 elements apart: from the 256th on an element's offset passes 2^31."""
+    T, step = 300, 2 ** 23 + 8
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    small = [randn(gen, T, h, D).to(dtype) for h in (4, 2, 2, 4, 4)]
+    kw = dict(batch=2, causal=True)
+
+    def far(x, room, at):
+        view = room[at:].as_strided((T, x.shape[1], D), (step, D, 1))
+        view.copy_(x)
+        return view
+
+    room = torch.empty(T * step, dtype=dtype, device="cuda")
+    q, k, v, g = (far(x, room, i * 1024) for i, x in enumerate(small[:4]))
+    out = far(small[4], room, 4096)
+    want, want_lse = hlq.hlq_attention(*small[:3], **kw)
+    got, lse = hlq.hlq_attention(q, k, v, out=out, **kw)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    grads = [far(torch.zeros_like(x), room, (5 + i) * 1024) for i, x in enumerate(small[:3])]
+    for x, y in zip(hlq.hlq_attention_backward(g, q, k, v, got, lse, g_q=grads[0], g_k=grads[1], g_v=grads[2], **kw),
+                    hlq.hlq_attention_backward(small[3], *small[:3], want, want_lse, **kw)):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_a_batch_that_is_mostly_padding(dtype):
     """Two short sequences in 3000 rows; queries and keys with offsets of their own."""

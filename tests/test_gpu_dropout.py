@@ -21,10 +21,10 @@ def _built():
     assert hlq.hlq_read_device_status(clear=True) == 0
 
 
-def halves(n, seed):
-    """The 16-bit numbers of elements 0 .. n - 1: Philox4x32-10, eight for each block."""
+def halves(n, seed, first=0):
+    """The 16-bit numbers of n elements from `first` (a multiple of 8): Philox4x32-10, eight for each block."""
     with np.errstate(over="ignore"):
-        c = [np.arange((n + 7) // 8, dtype=np.uint64), None, None, None]
+        c = [np.arange(first // 8, (first + n + 7) // 8, dtype=np.uint64), None, None, None]
         c = [c[0] & np.uint64(0xFFFFFFFF), c[0] >> np.uint64(32), np.full_like(c[0], 4), np.zeros_like(c[0])]
         k0, k1 = seed & 0xFFFFFFFF, seed >> 32 & 0xFFFFFFFF
         for _ in range(10):
@@ -64,6 +64,19 @@ def test_values(shape, x_dt, y_dt, residual):
         y = hlq.hlq_dropout(x, p, seed, residual=r, out_dtype=y_dt)
         assert y.dtype == y_dt
         check(y, x, p, seed, r)
+
+
+@pytest.mark.parametrize("T,C", [(2 ** 23 + 1, 4096), (33, 2 ** 30)])
+def test_elements_past_32_bits(T, C):
+    """Above 2^35 elements: the blocks' numbers pass 32 bits too."""
+    if torch.cuda.mem_get_info()[0] < 2 * T * C + 2 ** 30:
+        pytest.skip("needs 70 GB of device memory")
+    x = torch.ones(T, C, dtype=BF16, device="cuda")
+    y = hlq.hlq_dropout(x, 0.5, 11, out=x).view(-1)
+    for first in (0, 2 ** 31 - 800, 2 ** 32 - 800, 2 ** 35 - 800, T * C - 4096):
+        n = min(4096, T * C - first)
+        want = 2.0 * torch.from_numpy(halves(n, 11, first) >= 32768).to("cuda")
+        assert torch.equal(y[first:first + n].float(), want)
 
 
 def test_share_kept_and_other_seeds():
