@@ -9,7 +9,7 @@
 //   g_q_i = scale sum_j ds_ij k_j,  g_k_j = scale sum_i ds_ij q_i,
 //   g_v_j = sum_i p_ij g_out_i
 //
-// One CTA of 16 x 16 threads has a tile of rows (queries; keys in the keys'
+// One CTA of 8 x 16 or 16 x 16 threads has a tile of rows (queries; keys in the keys'
 // pass) in shared memory and goes over tiles of the other side.  Thread
 // (ty, tx) has rows ty RM .., columns tx, tx + 16, .. of a tile of scores and
 // columns 4 tx + 64 c .. (2 tx .. of 32) of a row of results, so that a row belongs to half a
@@ -17,45 +17,45 @@
 // memory without a barrier.  The backward pass goes over the keys' tiles (g_k,
 // g_v) and over the queries' tiles (g_q) in CTAs of their own: two products
 // more than one pass with atomics would take, and equal calls give equal bits.
-// Shared memory's loads bound it (a thread's 4 x 4 scores take 8 of 16 bytes for
-// 64 multiplications): 33 TFLOP/s forward and 24 backward (of five products) for
-// 4 x 1024 tokens, 8 heads of 64 and of 128 (forward 31).
+// What bounds it is shared memory beside the multiplications (a thread's 4 x 4
+// scores take 8 loads of 16 bytes for 64 of them), and each tile's barriers and
+// first loads: 4 x 1024 tokens, 8 heads, 34 TFLOP/s forward and 28 (of five
+// products) backward for heads of 64, 32 and 26 for heads of 128.
 #include <cmath>
 
 #include "hlq_attn.cuh"
+#include "hlq_host.h"
 #include "hlq_rows.cuh"
 
 namespace hlq {
 namespace {
 
-constexpr int kThreads = 256;
-
-// Tile sizes by head size: rows of the CTA's own side and of the other side.  A
-// CTA takes 19, 70, 78 or 108 KB of shared memory forward and 23, 87, 110 or 142
-// KB backward (D up to 32, 64, 128, 256), two of them an SM but for the last.
-template <int DP>
+// kT threads with a tile of BM rows of the CTA's own side, and BN of the other side;
+// heads up to D, kC CTAs an SM.
+template <int D, int BM, int BN, int kT, int kC>
 struct Cfg {
+  static constexpr int DP = D;
+  static constexpr int kThreads = kT, kCtas = kC;
   static constexpr int kLd = DP + 4;  // floats: rows 4 banks apart
-  static constexpr int kBM = DP == 64 || DP == 128 ? 64 : 32;
-  static constexpr int kBN = DP == 64 ? 64 : 32;
-  static constexpr int kRM = kBM / 16, kRN = kBN / 16, kRD = DP / 16;
+  static constexpr int kBM = BM, kBN = BN;
+  static constexpr int kRM = kBM * 16 / kThreads, kRN = kBN / 16, kRD = DP / 16;
   static constexpr int kVec = DP == 32 ? 2 : 4;  // columns of a result together
   static constexpr int kLdP = kBN + 4;
   static constexpr size_t kFwd = 4 * (size_t)(kBM * kLd + 2 * kBN * kLd + kBM * kLdP);
   static constexpr size_t kBwd = 4 * (size_t)(2 * kBM * kLd + 2 * kBN * kLd + kBM * kLdP);
-  static constexpr int kCtas = DP <= 128 ? 2 : 1;
 };
 
 // Rows row0 .. row0 + n of head h as fp32, zeros in the rest of the tile.  By
 // four where heads begin on 16-byte boundaries and are of whole fours.
-template <int DP>
+template <class C>
 __device__ __forceinline__ void load_tile(float* dst, const Heads& x, bool bf16, int64_t row0,
                                           int n, int rows, int h, int D) {
+  constexpr int DP = C::DP;
   const int64_t at = row0 * x.token + (int64_t)h * x.head;
   if (D % 4 == 0 && reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.token % 4 == 0 &&
       x.head % 4 == 0) {
 #pragma unroll 4
-    for (int i = threadIdx.x; i < rows * DP / 4; i += kThreads) {
+    for (int i = threadIdx.x; i < rows * DP / 4; i += C::kThreads) {
       const int r = i / (DP / 4), d = i % (DP / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < n && d < D) {
@@ -66,23 +66,23 @@ __device__ __forceinline__ void load_tile(float* dst, const Heads& x, bool bf16,
           v = *reinterpret_cast<const float4*>(static_cast<const float*>(x.p) + at + r * x.token + d);
         }
       }
-      *reinterpret_cast<float4*>(dst + r * Cfg<DP>::kLd + d) = v;
+      *reinterpret_cast<float4*>(dst + r * C::kLd + d) = v;
     }
     return;
   }
-  for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
+  for (int i = threadIdx.x; i < rows * DP; i += C::kThreads) {
     const int r = i / DP, d = i % DP;
-    dst[r * Cfg<DP>::kLd + d] =
+    dst[r * C::kLd + d] =
         r < n && d < D ? load_elem(x.p, bf16, at + r * x.token + d) : 0.f;
   }
 }
 
 // acc[i][j] = A[row i] . B[row j], rows as in the note at the top.  Two fp32 in
 // one instruction: the sums of the even and of the odd columns, added at the end.
-template <int DP, int RM, int RN>
+template <class C, int RM, int RN>
 __device__ __forceinline__ void rows_by_rows(const float* a, const float* b, int ty, int tx,
                                              float (&acc)[RM][RN]) {
-  constexpr int kLd = Cfg<DP>::kLd;
+  constexpr int kLd = C::kLd, DP = C::DP;
   F2 two[RM][RN];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
@@ -114,10 +114,10 @@ __device__ __forceinline__ void rows_by_rows(const float* a, const float* b, int
 
 // acc[i][V c + e] += sum_j P[row i][j] B[j][16 V c + V tx + e], V = kVec; acc by
 // pairs of columns.
-template <int DP, int RM, int BN>
+template <class C, int RM, int BN>
 __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, int ty, int tx,
-                                                F2 (&acc)[RM][Cfg<DP>::kRD / 2]) {
-  constexpr int kLd = Cfg<DP>::kLd, kLdP = BN + 4, kVec = Cfg<DP>::kVec;
+                                                F2 (&acc)[RM][C::kRD / 2]) {
+  constexpr int kLd = C::kLd, kLdP = BN + 4, kVec = C::kVec;
 #pragma unroll 2
   for (int j = 0; j < BN; j += 4) {
     float p[RM][4];
@@ -129,7 +129,7 @@ __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, 
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-      for (int c = 0; c < Cfg<DP>::kRD / kVec; ++c) {
+      for (int c = 0; c < C::kRD / kVec; ++c) {
         const float* at = b + (j + jj) * kLd + 16 * kVec * c + kVec * tx;
         F2 v[kVec / 2];
         if constexpr (kVec == 4) {
@@ -147,18 +147,18 @@ __device__ __forceinline__ void rows_by_columns(const float* P, const float* b, 
   }
 }
 
-template <int DP, int RM>
+template <class C, int RM>
 __device__ __forceinline__ void store_rows(const Heads& x, bool bf16, int64_t row0, int n, int h,
                                            int D, int ty, int tx, float factor,
-                                           const F2 (&acc)[RM][Cfg<DP>::kRD / 2]) {
-  constexpr int kVec = Cfg<DP>::kVec;
+                                           const F2 (&acc)[RM][C::kRD / 2]) {
+  constexpr int kVec = C::kVec;
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
     const int r = ty * RM + i;
     if (r >= n) continue;
     const int64_t at = (row0 + r) * x.token + (int64_t)h * x.head;
 #pragma unroll
-    for (int c = 0; c < Cfg<DP>::kRD; c += 2) {
+    for (int c = 0; c < C::kRD; c += 2) {
       const int d = 16 * kVec * (c / kVec) + kVec * tx + c % kVec;
       const float2 v = split(acc[i][c / 2]);
       if (d < D) store_elem(x.p, bf16, at + d, factor * v.x);
@@ -167,12 +167,12 @@ __device__ __forceinline__ void store_rows(const Heads& x, bool bf16, int64_t ro
   }
 }
 
-template <int DP, int RM>
-__device__ __forceinline__ void clear(F2 (&acc)[RM][Cfg<DP>::kRD / 2]) {
+template <class C, int RM>
+__device__ __forceinline__ void clear(F2 (&acc)[RM][C::kRD / 2]) {
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int c = 0; c < Cfg<DP>::kRD / 2; ++c) acc[i][c] = f2(0.f);
+    for (int c = 0; c < C::kRD / 2; ++c) acc[i][c] = f2(0.f);
 }
 
 __device__ __forceinline__ float half_warp_max(float v) {
@@ -186,9 +186,8 @@ __device__ __forceinline__ float half_warp_sum(float v) {
   return v;
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel(const Attn p) {
-  using C = Cfg<DP>;
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_fwd_simt_kernel(const Attn p) {
   constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
   extern __shared__ float smem[];
   float *sq = smem, *sk = sq + BM * C::kLd, *sv = sk + BN * C::kLd, *sp = sv + BN * C::kLd;
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
   AttnTile t;
   const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {  // rows of no sequence
-    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row, int d) {
+    outside_rows<false>(p, BM, past, threadIdx.x, C::kThreads, [&](int row, int d) {
       if (d == 0) p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
       store_elem(p.out.p, p.bf16, row * p.out.token + h * p.out.head + d, 0.f);
     });
@@ -207,21 +206,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
   }
   const int n = min(BM, t.nq - t.row0);
   const int keys = keys_of(p, t, t.row0 + n - 1);  // the last row sees the most
-  load_tile<DP>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
+  load_tile<C>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
   float m[RM], l[RM];
   F2 acc[RM][C::kRD / 2];
-  clear<DP, RM>(acc);
+  clear<C, RM>(acc);
 #pragma unroll
   for (int i = 0; i < RM; ++i) m[i] = -INFINITY, l[i] = 0.f;
   const float c2 = p.scale * kLog2e;
   for (int j0 = 0; j0 < keys; j0 += BN) {
     __syncthreads();  // the tiles before have been read
     const int nk = min(BN, keys - j0);
-    load_tile<DP>(sk, p.k, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
-    load_tile<DP>(sv, p.v, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    load_tile<C>(sk, p.k, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    load_tile<C>(sv, p.v, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
     __syncthreads();
     float s[RM][RN];
-    rows_by_rows<DP, RM, RN>(sq, sk, ty, tx, s);
+    rows_by_rows<C, RM, RN>(sq, sk, ty, tx, s);
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
       const int sees = keys_of(p, t, t.row0 + ty * RM + i) - j0;
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
       for (int c = 0; c < C::kRD / 2; ++c) acc[i][c] = acc[i][c] * f2(keep);
     }
     __syncwarp();
-    rows_by_columns<DP, RM, BN>(sp, sv, ty, tx, acc);
+    rows_by_columns<C, RM, BN>(sp, sv, ty, tx, acc);
     __syncwarp();
   }
 #pragma unroll
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) attn_fwd_simt_kernel
       p.lse[(int64_t)(t.q0 + t.row0 + r) * p.Hq + h] =
           l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
   }
-  store_rows<DP, RM>(p.out, p.bf16, t.q0 + t.row0, n, h, p.D, ty, tx, 1.f, acc);
+  store_rows<C, RM>(p.out, p.bf16, t.q0 + t.row0, n, h, p.D, ty, tx, 1.f, acc);
 }
 
 // delta = g_out . out (of g_out as bf16 where the products take it so: the gradients
@@ -372,9 +371,8 @@ __global__ void __launch_bounds__(256) attn_bwd_rows_any_kernel(const Attn p) {
 
 // g_k and g_v of a tile of keys: over the query heads that share the key head
 // and the tiles of queries that see it.  Rows are keys, columns queries.
-template <int DP>
+template <class C>
 __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
-  using C = Cfg<DP>;
   constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
   extern __shared__ float smem[];
   float *sk = smem, *sv = sk + BM * C::kLd, *sq = sv + BM * C::kLd, *sg = sq + BN * C::kLd,
@@ -386,18 +384,18 @@ __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
   AttnTile t;
   const int past = find_tile<true, BM>(p, (int)tile, t);
   if (past >= 0) {
-    outside_rows<true>(p, BM, past, threadIdx.x, kThreads, [&](int row, int d) {
+    outside_rows<true>(p, BM, past, threadIdx.x, C::kThreads, [&](int row, int d) {
       store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
       store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
     });
     return;
   }
   const int n = min(BM, t.nk - t.row0);
-  load_tile<DP>(sk, p.k, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
-  load_tile<DP>(sv, p.v, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
+  load_tile<C>(sk, p.k, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
+  load_tile<C>(sv, p.v, p.bf16, t.k0 + t.row0, n, BM, hk, p.D);
   F2 gk[RM][C::kRD / 2], gv[RM][C::kRD / 2];
-  clear<DP, RM>(gk);
-  clear<DP, RM>(gv);
+  clear<C, RM>(gk);
+  clear<C, RM>(gv);
   // the first query that sees the tile's first key
   const int first = p.causal ? max(0, t.row0 + t.nq - t.nk) / BN * BN : 0;
   const float c2 = p.scale * kLog2e;
@@ -405,12 +403,12 @@ __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
     for (int i0 = first; i0 < t.nq; i0 += BN) {
       __syncthreads();
       const int nq = min(BN, t.nq - i0);
-      load_tile<DP>(sq, p.q, p.bf16, t.q0 + i0, nq, BN, h, p.D);
-      load_tile<DP>(sg, p.gout, p.gout_bf16, t.q0 + i0, nq, BN, h, p.D);
+      load_tile<C>(sq, p.q, p.bf16, t.q0 + i0, nq, BN, h, p.D);
+      load_tile<C>(sg, p.gout, p.gout_bf16, t.q0 + i0, nq, BN, h, p.D);
       __syncthreads();
       float s[RM][RN], dp[RM][RN];
-      rows_by_rows<DP, RM, RN>(sk, sq, ty, tx, s);
-      rows_by_rows<DP, RM, RN>(sv, sg, ty, tx, dp);
+      rows_by_rows<C, RM, RN>(sk, sq, ty, tx, s);
+      rows_by_rows<C, RM, RN>(sv, sg, ty, tx, dp);
 #pragma unroll
       for (int j = 0; j < RN; ++j) {
         const int i = i0 + tx + 16 * j;  // the query
@@ -427,24 +425,23 @@ __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
         }
       }
       __syncwarp();
-      rows_by_columns<DP, RM, BN>(sp, sg, ty, tx, gv);
+      rows_by_columns<C, RM, BN>(sp, sg, ty, tx, gv);
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < RN; ++j)
 #pragma unroll
         for (int r = 0; r < RM; ++r) sp[(ty * RM + r) * C::kLdP + tx + 16 * j] = dp[r][j];
       __syncwarp();
-      rows_by_columns<DP, RM, BN>(sp, sq, ty, tx, gk);
+      rows_by_columns<C, RM, BN>(sp, sq, ty, tx, gk);
       __syncwarp();
     }
-  store_rows<DP, RM>(p.gk, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, p.scale, gk);
-  store_rows<DP, RM>(p.gv, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, 1.f, gv);
+  store_rows<C, RM>(p.gk, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, p.scale, gk);
+  store_rows<C, RM>(p.gv, p.g_bf16, t.k0 + t.row0, n, hk, p.D, ty, tx, 1.f, gv);
 }
 
 // g_q of a tile of queries.
-template <int DP>
+template <class C>
 __device__ __forceinline__ void queries_body(const Attn& p, uint32_t block) {
-  using C = Cfg<DP>;
   constexpr int BM = C::kBM, BN = C::kBN, RM = C::kRM, RN = C::kRN;
   extern __shared__ float smem[];
   float *sq = smem, *sg = sq + BM * C::kLd, *sk = sg + BM * C::kLd, *sv = sk + BN * C::kLd,
@@ -456,18 +453,18 @@ __device__ __forceinline__ void queries_body(const Attn& p, uint32_t block) {
   AttnTile t;
   const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {
-    outside_rows<false>(p, BM, past, threadIdx.x, kThreads, [&](int row, int d) {
+    outside_rows<false>(p, BM, past, threadIdx.x, C::kThreads, [&](int row, int d) {
       store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
     });
     return;
   }
   const int n = min(BM, t.nq - t.row0);
   const int keys = keys_of(p, t, t.row0 + n - 1);
-  load_tile<DP>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
-  load_tile<DP>(sg, p.gout, p.gout_bf16, t.q0 + t.row0, n, BM, h, p.D);
+  load_tile<C>(sq, p.q, p.bf16, t.q0 + t.row0, n, BM, h, p.D);
+  load_tile<C>(sg, p.gout, p.gout_bf16, t.q0 + t.row0, n, BM, h, p.D);
   F2 gq[RM][C::kRD / 2];
   float lse2[RM], delta[RM];
-  clear<DP, RM>(gq);
+  clear<C, RM>(gq);
 #pragma unroll
   for (int r = 0; r < RM; ++r) {
     const bool there = ty * RM + r < n;
@@ -479,12 +476,12 @@ __device__ __forceinline__ void queries_body(const Attn& p, uint32_t block) {
   for (int j0 = 0; j0 < keys; j0 += BN) {
     __syncthreads();
     const int nk = min(BN, keys - j0);
-    load_tile<DP>(sk, p.k, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
-    load_tile<DP>(sv, p.v, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    load_tile<C>(sk, p.k, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
+    load_tile<C>(sv, p.v, p.bf16, t.k0 + j0, nk, BN, hk, p.D);
     __syncthreads();
     float s[RM][RN], dp[RM][RN];
-    rows_by_rows<DP, RM, RN>(sq, sk, ty, tx, s);
-    rows_by_rows<DP, RM, RN>(sg, sv, ty, tx, dp);
+    rows_by_rows<C, RM, RN>(sq, sk, ty, tx, s);
+    rows_by_rows<C, RM, RN>(sg, sv, ty, tx, dp);
 #pragma unroll
     for (int r = 0; r < RM; ++r) {
       const int sees = keys_of(p, t, t.row0 + ty * RM + r) - j0;
@@ -494,39 +491,39 @@ __device__ __forceinline__ void queries_body(const Attn& p, uint32_t block) {
             tx + 16 * j < sees ? exp2f(s[r][j] * c2 - lse2[r]) * (dp[r][j] - delta[r]) : 0.f;
     }
     __syncwarp();
-    rows_by_columns<DP, RM, BN>(sd, sk, ty, tx, gq);
+    rows_by_columns<C, RM, BN>(sd, sk, ty, tx, gq);
     __syncwarp();
   }
-  store_rows<DP, RM>(p.gq, p.g_bf16, t.q0 + t.row0, n, h, p.D, ty, tx, p.scale, gq);
+  store_rows<C, RM>(p.gq, p.g_bf16, t.q0 + t.row0, n, h, p.D, ty, tx, p.scale, gq);
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas)
     attn_bwd_simt_kernel(const Attn p, uint32_t keys_ctas) {
   if (blockIdx.x < keys_ctas)
-    keys_body<DP>(p, blockIdx.x);
+    keys_body<C>(p, blockIdx.x);
   else
-    queries_body<DP>(p, blockIdx.x - keys_ctas);
+    queries_body<C>(p, blockIdx.x - keys_ctas);
 }
 
-template <int DP>
+template <class C>
 cudaError_t launch_fwd(const Attn& p, cudaStream_t st) {
-  const int64_t grid = most_tiles(p, false, Cfg<DP>::kBM) * p.Hq;
+  const int64_t grid = most_tiles(p, false, C::kBM) * p.Hq;
   if (grid == 0) return cudaSuccess;
-  cudaError_t e = allow_smem<attn_fwd_simt_kernel<DP>>(Cfg<DP>::kFwd);
+  cudaError_t e = allow_smem<attn_fwd_simt_kernel<C>>(C::kFwd);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_fwd_simt_kernel<DP>, dim3((unsigned)grid), dim3(kThreads), Cfg<DP>::kFwd,
+  return launch_pdl(attn_fwd_simt_kernel<C>, dim3((unsigned)grid), dim3(C::kThreads), C::kFwd,
                     st, p);
 }
 
-template <int DP>
+template <class C>
 cudaError_t launch_bwd(const Attn& p, cudaStream_t st) {
-  const int64_t keys = most_tiles(p, true, Cfg<DP>::kBM) * p.Hk;
-  const int64_t grid = keys + most_tiles(p, false, Cfg<DP>::kBM) * p.Hq;
+  const int64_t keys = most_tiles(p, true, C::kBM) * p.Hk;
+  const int64_t grid = keys + most_tiles(p, false, C::kBM) * p.Hq;
   if (grid == 0) return cudaSuccess;
-  cudaError_t e = allow_smem<attn_bwd_simt_kernel<DP>>(Cfg<DP>::kBwd);
+  cudaError_t e = allow_smem<attn_bwd_simt_kernel<C>>(C::kBwd);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_bwd_simt_kernel<DP>, dim3((unsigned)grid), dim3(kThreads), Cfg<DP>::kBwd,
+  return launch_pdl(attn_bwd_simt_kernel<C>, dim3((unsigned)grid), dim3(C::kThreads), C::kBwd,
                     st, p, (uint32_t)keys);
 }
 
@@ -543,18 +540,37 @@ cudaError_t launch_rows(const Attn& p, cudaStream_t st) {
 
 }  // namespace
 
+// Tiles by head size.  Forward: 32 rows and 128 threads, three or four CTAs an SM.
+// Against 64 rows and 256 threads (D 32: 32 by 32 and 256), four sequences, 8 heads:
+// D 32 1024 tokens 148 us against 263, 400 tokens 32 against 52; D 64 254 against
+// 267, 50 against 62; D 128 532 against 548, 95 against 116.
 cudaError_t launch_attn_simt(const Attn& p, cudaStream_t st) {
-  return p.D <= 32    ? launch_fwd<32>(p, st)
-         : p.D <= 64  ? launch_fwd<64>(p, st)
-         : p.D <= 128 ? launch_fwd<128>(p, st)
-                      : launch_fwd<256>(p, st);
+  return p.D <= 32    ? launch_fwd<Cfg<32, 32, 64, 128, 4>>(p, st)
+         : p.D <= 64  ? launch_fwd<Cfg<64, 32, 64, 128, 3>>(p, st)
+         : p.D <= 128 ? launch_fwd<Cfg<128, 32, 32, 128, 3>>(p, st)
+                      : launch_fwd<Cfg<256, 32, 32, 256, 1>>(p, st);
 }
 
+// Backward: 64 rows and 256 threads where that leaves three CTAs for each SM or more, else
+// as forward: D 64 4 x 1024 tokens (8 heads) 769 us against 854, 5 x 129 (6 heads) 50
+// against 43; D 128 1671 against 1805, 87 against 71.  D up to 32: as forward, but
+// where all CTAs of 32 rows run at once each has 256 threads and 32 columns
+// (4 x 1024 719 against 456, 5 x 129 23.7 against 29.9).
 cudaError_t launch_attn_bwd_simt(const Attn& p, cudaStream_t st) {
-  return p.D <= 32    ? launch_bwd<32>(p, st)
-         : p.D <= 64  ? launch_bwd<64>(p, st)
-         : p.D <= 128 ? launch_bwd<128>(p, st)
-                      : launch_bwd<256>(p, st);
+  const auto ctas = [&](int rows) {
+    return most_tiles(p, true, rows) * p.Hk + most_tiles(p, false, rows) * p.Hq;
+  };
+  const int64_t sms = device_sm_count();
+  if (p.D <= 32)
+    return ctas(32) <= 2 * sms ? launch_bwd<Cfg<32, 32, 32, 256, 2>>(p, st)
+                               : launch_bwd<Cfg<32, 32, 64, 128, 4>>(p, st);
+  if (p.D <= 64)
+    return ctas(64) < 3 * sms ? launch_bwd<Cfg<64, 32, 64, 128, 3>>(p, st)
+                              : launch_bwd<Cfg<64, 64, 64, 256, 2>>(p, st);
+  if (p.D <= 128)
+    return ctas(64) < 3 * sms ? launch_bwd<Cfg<128, 32, 32, 128, 3>>(p, st)
+                              : launch_bwd<Cfg<128, 64, 32, 256, 2>>(p, st);
+  return launch_bwd<Cfg<256, 32, 32, 256, 1>>(p, st);
 }
 
 cudaError_t launch_attn_bwd_rows(const Attn& p, cudaStream_t st) {

@@ -177,6 +177,15 @@ def test_long_sequences_of_many_heads(lens_q, lens_k, heads, causal, D):
     c.check_forward(U[BF16])
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,D", [(F32, 32), (F32, 20), (F32, 64), (F32, 50), (F32, 128), (F32, 72), (F32, 160), (BF16, 132)])
+def test_many_tiles_in_fp32(dtype, D, causal):
+    lens = [70, 1, 130, 0] * 9
+    c = Case(dtype, lens, lens, 12, 4, D, causal, front=2, back=67)
+    c.check_forward(U[dtype])
+    c.check_backward(U[dtype], F32)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 100])
 def test_offsets_past_32_bits(D, dtype):
