@@ -1058,9 +1058,10 @@ def hlq_attention(q, k, v, seqs=None, seqs_k=None, batch: int = 1, causal: bool 
     if lse is None:
         lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
     _need_buf(lse, (Tq, Hq), torch.float32, index, "lse")
+    scale = max(D, 1) ** -0.5 if scale is None else scale
     rc = lib().hlq_attention(pq, pk, pv, _code(q.dtype), Tq, k.shape[0], Hq, k.shape[1], D, ps, psk,
-                             batch, 1 if causal else 0, D ** -0.5 if scale is None else scale, po,
-                             lse.data_ptr(), _raw_stream(index))
+                             batch, 1 if causal else 0, scale, po, lse.data_ptr(),
+                             _raw_stream(index))
     _check(rc, "hlq_attention")
     return out, lse
 
@@ -1114,8 +1115,8 @@ def hlq_attention_backward(g_out, q, k, v, out, lse, seqs=None, seqs_k=None, bat
     ws, pws, n_ws = _workspace(ws, n_ws, index, q.device)
     rc = lib().hlq_attention_backward(
         pg, gout_dt, pq, pk, pv, po, dt, lse.data_ptr(), Tq, Tk, Hq, Hk, D, ps, psk, batch,
-        1 if causal else 0, D ** -0.5 if scale is None else scale, pgq, pgk, pgv, _code(g_dtype),
-        pws, n_ws, _raw_stream(index))
+        1 if causal else 0, max(D, 1) ** -0.5 if scale is None else scale, pgq, pgk, pgv,
+        _code(g_dtype), pws, n_ws, _raw_stream(index))
     _check(rc, "hlq_attention_backward")
     return g_all if packed else (g_q, g_k, g_v)
 

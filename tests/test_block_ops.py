@@ -152,6 +152,8 @@ def test_binding_refuses_what_does_not_fit():
         hlq.hlq_attention(q.half(), k.half(), k.half())
     with pytest.raises(hlq.HLQError, match="SHAPE"):
         hlq.hlq_attention(q, k, k, batch=3)
+    with pytest.raises(hlq.HLQError, match="SHAPE"):
+        hlq.hlq_attention(q[..., :0], k[..., :0], k[..., :0])
     with pytest.raises(hlq.HLQError, match="UNSUPPORTED"):
         hlq.hlq_attention(*[torch.zeros(8, 2, 257, device="cuda")] * 3)
     lse = torch.zeros(8, 4, device="cuda")

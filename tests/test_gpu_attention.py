@@ -291,13 +291,41 @@ def test_equal_calls_give_equal_bits_and_offsets_do_not_matter(dtype):
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
-@pytest.mark.parametrize("many", [40, 129, 1000])
-def test_many_sequences(many):
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("many,front,back", [(40, 0, 0), (128, 300, 1), (129, 0, 0), (256, 5, 0), (257, 130, 515), (1000, 1, 0), (1025, 257, 129)])
+def test_many_sequences(many, front, back, causal, dtype):
     """More sequences than a warp looks at in one step, most of them short or empty."""
     lens = [(7 * i * i) % 11 + (150 if i % 97 == 5 else 0) for i in range(many)]
-    c = Case(BF16, lens, lens, 2, 1, 64, True)
-    c.check_forward(U[BF16])
-    c.check_backward(U[BF16], BF16)
+    lens_k = lens if many % 2 else [(5 * i) % 9 + (270 if i % 89 == 3 else 0) for i in range(many)]
+    c = Case(dtype, lens, lens_k, 2, 1, 64, causal, front=front, back=back)
+    c.check_forward(U[dtype])
+    c.check_backward(U[dtype], BF16)
+
+
+@pytest.mark.parametrize("at", [0, 3, 130, 299])
+def test_bad_offsets_among_many(at):
+    q = torch.randn(3000, 1, 64, device="cuda").to(BF16)
+    off = 10 * torch.arange(301, dtype=torch.int32)
+    for bad in (-7, 3001, int(off[at]) + 25):
+        seqs = off.clone()
+        seqs[at] = bad
+        hlq.hlq_read_device_status(clear=True)
+        out, lse = hlq.hlq_attention(q, q, q, seqs=seqs.cuda())
+        assert hlq.hlq_read_device_status(clear=True) & hlq.DEV_BADCODE
+        hlq.hlq_attention_backward(q, q, q, q, out, lse, seqs=seqs.cuda())
+        assert hlq.hlq_read_device_status(clear=True) & hlq.DEV_BADCODE
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("offsets", [False, True])
+def test_no_keys_or_no_queries_at_all(offsets, dtype):
+    for lens_q, lens_k in (([130, 5], [0, 0]), ([0, 0], [130, 5]), ([0, 0], [0, 0])):
+        if not offsets:
+            lens_q, lens_k = [max(lens_q)] * 2, [max(lens_k)] * 2
+        c = Case(dtype, lens_q, lens_k, 4, 2, 64, True, offsets=offsets)
+        c.check_forward(U[dtype])
+        c.check_backward(U[dtype], F32)
 
 
 def test_bad_offsets_raise_the_flag():
