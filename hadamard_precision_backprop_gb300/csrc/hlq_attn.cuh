@@ -164,23 +164,22 @@ inline int64_t most_tiles(const Attn& p, bool keys, int rows) {
 }
 
 // Rows of chunk `chunk` of the rows that belong to no sequence (before the
-// first and behind the last): calls f(row, d) for this thread's elements, d from
-// 0 to D - 1.
+// first and behind the last), a warp for each: calls f(row, d) for this thread's
+// elements, d from 0 to D - 1.
 template <bool kKeys, typename F>
-__device__ __forceinline__ void outside_rows(const Attn& p, int rows, int chunk, int thread,
-                                             int threads, F&& f) {
+__device__ __forceinline__ void outside_rows(const Attn& p, int rows, int chunk, F&& f) {
   if (!p.seqs_q) return;
   const int32_t* seqs = kKeys ? p.seqs_k : p.seqs_q;
   const int T = kKeys ? p.Tk : p.Tq;
   bool bad = false;
   const int front = seq_rows(seqs, 0, T, bad).x;
   const int back = max(front, seq_rows(seqs, p.batch - 1, T, bad).y);
-  const int64_t first = (int64_t)chunk * rows;
-  const int n = (int)max((int64_t)0, min((int64_t)rows, (int64_t)front + (T - back) - first));
-  for (int e = thread; e < n * p.D; e += threads) {
-    const int64_t i = first + e / p.D;
-    f((int)(i < front ? i : back + (i - front)), e % p.D);
-  }
+  const int64_t first = (int64_t)chunk * rows, n = (int64_t)front + (T - back);
+#pragma unroll 1
+  for (int64_t i = first + threadIdx.x / 32; i < first + rows && i < n; i += blockDim.x / 32)
+#pragma unroll 1
+    for (int d = threadIdx.x % 32; d < p.D; d += 32)
+      f((int)(i < front ? i : back + (i - front)), d);
 }
 
 // Keys that query i of a tile's sequence sees: the last query sees all of

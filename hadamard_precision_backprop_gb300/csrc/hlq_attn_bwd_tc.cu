@@ -219,7 +219,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
 
   if (past >= 0) {
-    outside_rows<true>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+    outside_rows<true>(p, kRows, past, [&](int row, int d) {
       store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
       store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
     });
@@ -587,7 +587,7 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
 
   if (past >= 0) {
-    outside_rows<false>(p, kRows, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+    outside_rows<false>(p, kRows, past, [&](int row, int d) {
       store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
     });
   } else if (warp < 4) {

@@ -23,9 +23,9 @@
 // schedulers, 512 of exponentials (4 a warp) and about as many of multiplications,
 // maxima, sums and conversions; the reads and writes of TMEM and the waits between
 // them are what is left.  Tensor pipe busy for 46 % (4 sequences of 2048).
-// Causal, 32 heads of 128 with 8 of keys, 8 sequences of 2048: 258-266 us (1.03
-// to 1.07 PFLOP/s of the half that is not masked); 4 heads, one sequence of 16384:
-// 187-206 us, where the longest tile's 128 steps are the time.
+// Causal, 32 heads of 128 with 8 of keys, 8 sequences of 2048: 257 us (1.07
+// PFLOP/s of the half that is not masked); 4 heads, one sequence of 16384:
+// 184 us (1.49 PFLOP/s), where the longest tile's 128 steps are the time.
 #include <cmath>
 #include <cstring>
 
@@ -48,20 +48,26 @@ struct FwdCfg {
   static constexpr int kChunks = DP / kChunk;
   static constexpr uint32_t kTile = kChunks * kChunkBytes;
   static constexpr int kStages = (kQ == 2 ? 2 : 1) * (DP == 64 ? 2 : 1);  // of K and of V each
-  static constexpr size_t kSmem = 1024 + (size_t)(kQ + 2 * kStages) * kTile + 256;
+  static constexpr size_t kSmem = 1024 + (size_t)(kQ + 2 * kStages) * kTile + 512;
   static constexpr uint32_t kO = kQ * kRows, kColumns = kQ * 256;
   static constexpr int kThreads = 128 * (1 + kQ), kCtas = 3 - kQ;
+  // The softmax of two tiles goes in turns, so that one's products run beside the
+  // other's softmax whatever the tiles began with: one sequence of 16384 (4 heads of
+  // 128, causal) 184 us, without turns 195 or 231 from one build to the next, with
+  // the maxima out of turn 191; 8 of 2048 257 against 258.  Heads of 64, where the
+  // products are half as long, lose by it: 2 of 8192 (8 heads) 350 against 320.
+  static constexpr bool kTurns = kQ == 2 && DP == 128;
   // of the launch's 168 (384 threads) or 128 (256 threads) a thread
   static constexpr int kFewer = kQ == 2 ? 72 : 56, kMore = kQ == 2 ? 216 : 200;
 };
 
 struct FwdBars {
   uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_empty[4], v_last, v_clear, s_full[2],
-      p_full[2][2], o_full[2], drained[2];
+      p_full[2][2], turn[2][4], o_full[2], drained[2];
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(FwdBars) <= 256, "barriers fit their 256 bytes");
+static_assert(sizeof(FwdBars) <= 512, "barriers fit their 512 bytes");
 
 template <int DP, int kQ>
 __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCtas)
@@ -83,6 +89,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
       mbar_init(&bar.s_full[g], 1);
       mbar_init(&bar.p_full[g][0], 4);
       mbar_init(&bar.p_full[g][1], 4);
+      for (int w = 0; w < 4; ++w) mbar_init(&bar.turn[g][w], 1);
       mbar_init(&bar.o_full[g], 1);
       mbar_init(&bar.drained[g], 1);
     }
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
   const int rest = n > 0 && t.nk < n * kRows ? t.nk - (n - 1) * kRows : 0;
 
   if (past >= 0) {
-    outside_rows<false>(p, kQ * kRows, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+    outside_rows<false>(p, kQ * kRows, past, [&](int row, int d) {
       if (d == 0) p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
       store_elem(p.out.p, true, row * p.out.token + h * p.out.head + d, 0.f);
     });
@@ -244,6 +251,9 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
     bool ok = true;
     for (int j = 0; j < tiles[g] && ok; ++j) {
       ok = wait(&bar.s_full[g], j);
+      // after the other tile's step before
+      if (C::kTurns && ok && j >= 1 - g && j - 1 + g < tiles[1 - g])
+        ok = wait(&bar.turn[1 - g][warp & 3], j - 1 + g);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after();
@@ -309,6 +319,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[g][half]);
       }
+      if (C::kTurns && lane == 0) mbar_arrive(&bar.turn[g][warp & 3]);
       const float2 both = split(sum);
       l += both.x + both.y;
     }
@@ -391,13 +402,14 @@ bool attn_tc(const Attn& p) {
 }
 
 cudaError_t launch_attn_tc(const Attn& p, cudaStream_t st) {
-  // Two tiles of queries in a CTA where sequences are long and there are enough
-  // of them: one sequence of 16384 (4 heads of 128, causal) 188 us against 205
-  // with one tile, 16 of 1024 (16 heads of 64) 104 against 107; but 32 of 512 (16
-  // heads of 128) 90 against 84, 64 of 100 (12 heads of 64) 25 against 16, one of
-  // 2048 (4 heads of 128) 36 against 30.
+  // Two tiles of queries in a CTA where sequences are long (with a causal mask the
+  // two see different numbers of keys) and there are enough of them: 16 of 1024 (16
+  // heads of 128) 119 us against 126 with one tile, 12 of 1300 (12 heads) 127 against
+  // 136; but 64 of 300 128 against 114.  Causal: 8 of 2000 (8 heads) 69.3 against 69.9;
+  // but 12 of 1300 90 against 81, 32 of 512 75 against 67.  Heads of 64: 99 against 104,
+  // 105 against 109, 104 against 87; 53.5 against 55.4, 69 against 65, 54 against 51.
   const int64_t pairs = most_tiles(p, false, 2 * kRows) * p.Hq;
-  if (p.Tk / p.batch >= 1024 && pairs >= device_sm_count())
+  if (p.Tk / p.batch >= (p.causal ? 1792 : 768) && pairs >= device_sm_count())
     return p.D <= 64 ? launch<64, 2>(p, st) : launch<128, 2>(p, st);
   return p.D <= 64 ? launch<64, 1>(p, st) : launch<128, 1>(p, st);
 }

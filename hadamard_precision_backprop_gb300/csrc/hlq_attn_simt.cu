@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_fwd_simt_kernel(co
   AttnTile t;
   const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {  // rows of no sequence
-    outside_rows<false>(p, BM, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+    outside_rows<false>(p, BM, past, [&](int row, int d) {
       if (d == 0) p.lse[(int64_t)row * p.Hq + h] = -INFINITY;
       store_elem(p.out.p, p.bf16, row * p.out.token + h * p.out.head + d, 0.f);
     });
@@ -384,7 +384,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
   AttnTile t;
   const int past = find_tile<true, BM>(p, (int)tile, t);
   if (past >= 0) {
-    outside_rows<true>(p, BM, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+    outside_rows<true>(p, BM, past, [&](int row, int d) {
       store_elem(p.gk.p, p.g_bf16, row * p.gk.token + hk * p.gk.head + d, 0.f);
       store_elem(p.gv.p, p.g_bf16, row * p.gv.token + hk * p.gv.head + d, 0.f);
     });
@@ -453,7 +453,7 @@ __device__ __forceinline__ void queries_body(const Attn& p, uint32_t block) {
   AttnTile t;
   const int past = find_tile<false, BM>(p, (int)tile, t);
   if (past >= 0) {
-    outside_rows<false>(p, BM, past, threadIdx.x, C::kThreads, [&](int row, int d) {
+    outside_rows<false>(p, BM, past, [&](int row, int d) {
       store_elem(p.gq.p, p.g_bf16, row * p.gq.token + h * p.gq.head + d, 0.f);
     });
     return;
