@@ -22,7 +22,7 @@
 // of the tensor pipe (64 for each 128 x 128 x 16) and, for each of the four
 // schedulers, 512 of exponentials (4 a warp) and about as many of multiplications,
 // maxima, sums and conversions; the reads and writes of TMEM and the waits between
-// them are what is left.  Tensor pipe busy for 46 % (4 sequences of 2048).
+// them are what is left.  Tensor pipe busy for 49 % (4 sequences of 2048).
 // Causal, 32 heads of 128 with 8 of keys, 8 sequences of 2048: 257 us (1.07
 // PFLOP/s of the half that is not masked); 4 heads, one sequence of 16384:
 // 184 us (1.49 PFLOP/s), where the longest tile's 128 steps are the time.

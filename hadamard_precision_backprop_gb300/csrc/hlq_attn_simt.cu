@@ -17,9 +17,12 @@
 // memory without a barrier.  The backward pass goes over the keys' tiles (g_k,
 // g_v) and over the queries' tiles (g_q) in CTAs of their own: two products
 // more than one pass with atomics would take, and equal calls give equal bits.
-// What bounds it is shared memory beside the multiplications (a thread's 4 x 4
-// scores take 8 loads of 16 bytes for 64 of them), and each tile's barriers and
-// first loads: 4 x 1024 tokens, 8 heads, 34 TFLOP/s forward and 28 (of five
+// What bounds it is shared memory: a thread's 4 x 4 scores take 8 loads of 16 bytes
+// for 64 multiplications, so a warp's loads (512 bytes each, whether lanes read
+// the same or not) 32 clocks of the SM at 128 bytes a clock for 64 clocks of one of
+// its four schedulers.  The multiplications fill half of their pipe (8 x 700 tokens, 6
+// heads of 64); 8 x 4 scores need more registers than leaves warps enough (64 rows,
+// 128 threads, D 64 backward: 805 us against 769).  4 x 1024 tokens, 8 heads, 34 TFLOP/s forward and 28 (of five
 // products) backward for heads of 64, 32 and 26 for heads of 128.
 #include <cmath>
 
