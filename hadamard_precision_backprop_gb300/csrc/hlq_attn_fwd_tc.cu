@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
         for (int i = 0; i < 32; ++i) {
           const uint32_t(&r)[32] = s[2 * half + i / 16];
           const int k = 2 * (i % 16);
-          const float2 x = split(fma2(f2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c22, base2));
+          const F2 two = f2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+          const float2 x = split(fma2(two, c22, base2));
           const float a = exp2_fast(x.x), b = exp2_fast(x.y);
           sum = sum + f2(a, b);
           e[i] = bf16x2(a, b);
@@ -356,14 +357,15 @@ cudaError_t launch(const Attn& p, cudaStream_t st) {
   const int64_t grid = most_tiles(p, false, kQ * kRows) * p.Hq;
   if (grid == 0) return cudaSuccess;
   CUtensorMap mq, mk, mv;
-  if (!heads_map(&mq, p.q, p.Tq, p.Hq, p.D, kRows) || !heads_map(&mk, p.k, p.Tk, p.Hk, p.D, kRows) ||
+  if (!heads_map(&mq, p.q, p.Tq, p.Hq, p.D, kRows) ||
+      !heads_map(&mk, p.k, p.Tk, p.Hk, p.D, kRows) ||
       !heads_map(&mv, p.v, p.Tk, p.Hk, p.D, kRows))
     return cudaErrorInvalidValue;
   cudaError_t e = allow_smem<attn_fwd_tc_kernel<DP, kQ>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int wide_out = p.D % 8 == 0 && tma_heads(p.out, p.Tq, p.Hq);
-  return launch_pdl(attn_fwd_tc_kernel<DP, kQ>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, st, p,
-                    mq, mk, mv, wide_out);
+  return launch_pdl(attn_fwd_tc_kernel<DP, kQ>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem,
+                    st, p, mq, mk, mv, wide_out);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode() {

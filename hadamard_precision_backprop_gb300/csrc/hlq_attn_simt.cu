@@ -12,18 +12,20 @@
 // One CTA of 8 x 16 or 16 x 16 threads has a tile of rows (queries; keys in the keys'
 // pass) in shared memory and goes over tiles of the other side.  Thread
 // (ty, tx) has rows ty RM .., columns tx, tx + 16, .. of a tile of scores and
-// columns 4 tx + 64 c .. (2 tx .. of 32) of a row of results, so that a row belongs to half a
-// warp: maxima and sums are shuffles, and the probabilities go through shared
-// memory without a barrier.  The backward pass goes over the keys' tiles (g_k,
-// g_v) and over the queries' tiles (g_q) in CTAs of their own: two products
+// columns 4 tx + 64 c .. (2 tx .. of 32) of a row of results, so that a row belongs
+// to half a warp: maxima and sums are shuffles, and the probabilities go through
+// shared memory without a barrier.  The backward pass goes over the keys' tiles
+// (g_k, g_v) and over the queries' tiles (g_q) in CTAs of their own: two products
 // more than one pass with atomics would take, and equal calls give equal bits.
+//
 // What bounds it is shared memory: a thread's 4 x 4 scores take 8 loads of 16 bytes
 // for 64 multiplications, so a warp's loads (512 bytes each, whether lanes read
 // the same or not) 32 clocks of the SM at 128 bytes a clock for 64 clocks of one of
-// its four schedulers.  The multiplications fill half of their pipe (8 x 700 tokens, 6
-// heads of 64); 8 x 4 scores need more registers than leaves warps enough (64 rows,
-// 128 threads, D 64 backward: 805 us against 769).  4 x 1024 tokens, 8 heads, 34 TFLOP/s forward and 28 (of five
-// products) backward for heads of 64, 32 and 26 for heads of 128.
+// its four schedulers.  The multiplications fill half of their pipe (8 x 700 tokens,
+// 6 heads of 64); 8 x 4 scores need so many registers that too few warps are left
+// (64 rows, 128 threads, D 64 backward: 805 us against 769).  4 x 1024 tokens, 8
+// heads: 34 TFLOP/s forward and 28 (of five products) backward for heads of 64, 32
+// and 26 for heads of 128.
 #include <cmath>
 
 #include "hlq_attn.cuh"
