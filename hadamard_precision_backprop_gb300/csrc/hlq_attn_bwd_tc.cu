@@ -162,8 +162,12 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
         i < (int)kMoreBytes / 16 && i % 16 < 8 ? make_uint4(0x3f803f80u, 0x00003f80u, 0, 0)
                                                : make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (warp == 1) alloc(&bar.tmem, C::kColumns);
-  pdl_trigger();
+  if (warp == 1) {
+    alloc(&bar.tmem, C::kColumns);
+    // One warp's trigger is the CTA's, and not before it holds its TMEM: a CTA of
+    // the next kernel that had taken it instead would wait for this one.
+    pdl_trigger();
+  }
   pdl_wait();
 
   const uint32_t unit = kSplit ? block >> log_split : block, tile = unit / p.by_hk;
@@ -541,8 +545,10 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == 1) alloc(&bar.tmem, C::kColumns);
-  pdl_trigger();
+  if (warp == 1) {
+    alloc(&bar.tmem, C::kColumns);
+    pdl_trigger();  // as in the keys' CTAs
+  }
   pdl_wait();
 
   const uint32_t tile = block / p.by_hq;
