@@ -121,7 +121,10 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
   AttnTile t;
   const int past = find_tile<false, kQ * kRows>(p, (int)tile, t);
   const auto wait = [&](uint64_t* b, uint32_t phase) {
-    return wait_for(b, phase, abort_flag, p.status);
+    return wait_warp(abort_flag, p.status, [&] { return mbar_test(b, phase & 1); });
+  };
+  const auto wait_alone = [&](uint64_t* b, uint32_t phase) {
+    return wait_lane(b, phase, abort_flag, p.status);
   };
   // tiles of keys that the tiles of queries see
   int tiles[2] = {0, 0};
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
         };
         const auto load_k = [&](int j) {
           const int s = j % C::kStages;
-          if (j >= C::kStages && !wait(&bar.k_empty[s], j / C::kStages - 1)) return false;
+          if (j >= C::kStages && !wait_alone(&bar.k_empty[s], j / C::kStages - 1)) return false;
           mbar_expect_tx(&bar.k_full[s], C::kTile);
           load_tile<C::kChunks>(sk + s * C::kTile, &mk, &bar.k_full[s], hk, t.k0 + j * kRows);
           ++k_done;
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
         };
         const auto load_v = [&](int j) {
           const int s = j % C::kStages;
-          if (j >= C::kStages && !wait(&bar.v_empty[s], j / C::kStages - 1)) return false;
+          if (j >= C::kStages && !wait_alone(&bar.v_empty[s], j / C::kStages - 1)) return false;
           uint64_t* full = rest && j == n - 1 ? &bar.v_last : &bar.v_full[s];
           mbar_expect_tx(full, C::kTile);
           load_tile<C::kChunks>(sv + s * C::kTile, &mv, full, hk, t.k0 + j * kRows);
@@ -254,7 +257,6 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
       // after the other tile's step before
       if (C::kTurns && ok && j >= 1 - g && j - 1 + g < tiles[1 - g])
         ok = wait(&bar.turn[1 - g][warp & 3], j - 1 + g);
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after();
       uint32_t s[4][32];
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
       const float2 both = split(sum);
       l += both.x + both.y;
     }
-    if (tiles[g] > 0 && ok) ok = __all_sync(0xffffffffu, wait(&bar.o_full[g], 0));
+    if (tiles[g] > 0 && ok) ok = wait(&bar.o_full[g], 0);
     const bool there = past < 0 && row < t.nq;
     if (ok) {
       fence_after();

@@ -81,20 +81,31 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait, as mbar_wait, for waits that a product or a softmax hangs on: the
 // time and the abort flag are looked at every 64th try only (reading the timer
 // takes long enough to be missed on every wait).
-__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t phase, volatile int* abort_flag,
+__device__ __forceinline__ bool gives_up(uint32_t& t0, volatile int* abort_flag,
                                          unsigned int* status) {
-  const uint32_t parity = phase & 1;
-  unsigned long long t0 = 0;
-  for (int i = 1; !mbar_test(b, parity); ++i) {
-    if (i % 64 != 0) continue;
-    if (*abort_flag) return false;
-    const unsigned long long t = now_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitNs) {
-      if (atomicExch((int*)abort_flag, 1) == 0) atomicOr(status, HLQ_DEV_TIMEOUT);
-      return false;
-    }
-  }
+  if (*abort_flag) return true;
+  const uint32_t t = (uint32_t)(now_ns() >> 16);  // in 32 bits: one register less in each wait
+  if (t0 == 0) t0 = t;
+  if (t - t0 <= (uint32_t)(kWaitNs >> 16)) return false;
+  if (atomicExch((int*)abort_flag, 1) == 0) atomicOr(status, HLQ_DEV_TIMEOUT);
+  return true;
+}
+// By one thread.
+__device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t phase, volatile int* abort_flag,
+                                          unsigned int* status) {
+  uint32_t t0 = 0;
+  for (int i = 1; !mbar_test(b, phase & 1); ++i)
+    if (i % 64 == 0 && gives_up(t0, abort_flag, status)) return false;
+  return true;
+}
+// By a whole warp: one lane may see the phase where another would give up, so the
+// lanes vote on both, and the result is the warp's.
+template <typename F>
+__device__ __forceinline__ bool wait_warp(volatile int* abort_flag, unsigned int* status,
+                                          F&& test) {
+  uint32_t t0 = 0;
+  for (int i = 1; !__all_sync(0xffffffffu, test()); ++i)
+    if (i % 64 == 0 && __any_sync(0xffffffffu, gives_up(t0, abort_flag, status))) return false;
   return true;
 }
 

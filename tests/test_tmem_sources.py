@@ -30,3 +30,25 @@ def test_the_next_kernel_is_let_in_after_tmem_is_held(name):
         between = text[held[-1]:at]
         opened = text[:held[-1]].rstrip().endswith("{")
         assert "__syncthreads();" in between or (opened and "}" not in between), between
+
+
+@pytest.mark.parametrize("name", ["hlq_attn_fwd_tc.cu", "hlq_attn_bwd_tc.cu"])
+def test_a_warp_votes_on_a_wait(name):
+    """A bounded wait may end for one lane and give up for another.  Where a whole warp waits, the
+    lanes vote before the instructions that need all of them (elections, products, TMEM accesses);
+    only the one thread that loads waits alone."""
+    warp = code("hlq_attn_tc.cuh")
+    warp = warp[warp.index("bool wait_warp("):]
+    warp = warp[:warp.index("\n}")]
+    assert "while" not in warp and "!__all_sync(0xffffffffu, test())" in warp
+    assert re.findall(r"return ([^;]*);", warp) == ["false", "true"]
+    assert "__any_sync(0xffffffffu, gives_up(t0, abort_flag, status))) return false;" in warp
+    text = code(name)
+    kernels = len(re.findall(r"AttnTile t;", text))
+    assert text.count("return wait_warp(abort_flag, p.status, [&] { return mbar_test(b, phase & 1); });") == kernels
+    lane = r"const auto wait_alone = \[&\]\(uint64_t\* b, uint32_t phase\) \{\s*return wait_lane\(b, phase, abort_flag, p\.status\);\s*\};"
+    text, n = re.subn(lane, "", text)
+    assert n == kernels
+    text = re.sub(r"const auto load_\w+ = \[&\]\(.*?\n *\};", "", text, flags=re.S)  # one thread's
+    text = text.replace("__all_sync(0xffffffffu, wait_alone(", "")
+    assert "wait_lane(" not in text and "wait_alone(" not in text and "mbar_wait" not in text
