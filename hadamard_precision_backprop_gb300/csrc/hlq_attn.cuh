@@ -183,9 +183,10 @@ __device__ __forceinline__ void outside_rows(const Attn& p, int rows, int chunk,
 }
 
 // Keys that query i of a tile's sequence sees: the last query sees all of
-// them, each one before it one fewer.
+// them, each one before it one fewer.  (The difference first: a sum of two
+// lengths may leave 32 bits.)
 __device__ __forceinline__ int keys_of(const Attn& p, const AttnTile& t, int i) {
-  return p.causal ? max(0, min(t.nk, i + 1 + t.nk - t.nq)) : t.nk;
+  return p.causal ? max(0, min(t.nk, i + 1 + (t.nk - t.nq))) : t.nk;
 }
 
 }  // namespace hlq

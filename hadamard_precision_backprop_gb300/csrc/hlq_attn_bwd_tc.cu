@@ -188,7 +188,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
   // tile's first key
   int first = 0, per_head = 0;
   if (past < 0) {
-    if (p.causal) first = max(0, t.row0 + t.nq - t.nk) / C::kN;
+    if (p.causal) first = max(0, t.row0 + (t.nq - t.nk)) / C::kN;
     per_head = max(0, (t.nq + C::kN - 1) / C::kN - first);
   }
   const int n = per_head * heads;
@@ -382,8 +382,8 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
     const uint32_t ts = tmem + C::kS + lanes + 32 * part, td = tmem + C::kD + lanes + 32 * part;
     const F2 c22 = f2(p.scale * kLog2e);
     // the first query that sees this row's key, and the tile's last key
-    const int from = p.causal ? key + t.nq - t.nk : 0;
-    const int last_from = p.causal ? t.row0 + kRows - 1 + t.nq - t.nk : 0;
+    const int from = p.causal ? key + (t.nq - t.nk) : 0;
+    const int last_from = p.causal ? t.row0 + kRows - 1 + (t.nq - t.nk) : 0;
     bool ok = true;
     for (int it = 0, tile_q = first; it < n; ++it, ++tile_q) {
       if (tile_q == first + per_head) tile_q = first;

@@ -402,7 +402,7 @@ __device__ __forceinline__ void keys_body(const Attn& p, uint32_t block) {
   clear<C, RM>(gk);
   clear<C, RM>(gv);
   // the first query that sees the tile's first key
-  const int first = p.causal ? max(0, t.row0 + t.nq - t.nk) / BN * BN : 0;
+  const int first = p.causal ? max(0, t.row0 + (t.nq - t.nk)) / BN * BN : 0;
   const float c2 = p.scale * kLog2e;
   for (int h = hk * group; h < (hk + 1) * group; ++h)
     for (int i0 = first; i0 < t.nq; i0 += BN) {

@@ -13,6 +13,8 @@ namespace hlq {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+// of attention: a tile (256 rows at most) may reach past a sequence's end in 32 bits
+constexpr int64_t kMaxTokens = kMaxRows - 1024;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int kMaxHeadSize = 256;
 
@@ -38,7 +40,7 @@ Heads heads_of(const hlq_heads& x, int64_t T, int64_t H) {
 hlq_status check_sizes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t batch) {
   if (Tq < 0 || Tk < 0 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || D < 1 || batch < 1)
     return HLQ_ERR_SHAPE;
-  if (D > kMaxHeadSize || Tq >= kMaxRows || Tk >= kMaxRows || Hq >= kMaxRows ||
+  if (D > kMaxHeadSize || Tq > kMaxTokens || Tk > kMaxTokens || Hq >= kMaxRows ||
       Tq * Hq >= kMaxRows || Tk * Hk >= kMaxRows || batch >= kMaxRows ||
       (batch + 1) * Hq >= kMaxRows / 2)
     return HLQ_ERR_UNSUPPORTED;

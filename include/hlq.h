@@ -693,7 +693,8 @@ typedef struct {
  * bytes; the probabilities are then rounded to bf16 for their product with v.
  * Maxima, sums and out are held in fp32 and out is rounded once.
  * Any other alignment or D: products in fp32, slower.
- * D <= 256; Tq Hq, Tk Hk < 2^31; (batch + 1) Hq < 2^30; scale from 2^-64 to 2^64.
+ * D <= 256; Tq, Tk <= 2^31 - 1024; Tq Hq, Tk Hk < 2^31; (batch + 1) Hq < 2^30;
+ * scale from 2^-64 to 2^64.
  * No output may overlap an input.
  */
 hlq_status hlq_attention(const hlq_heads *q, const hlq_heads *k, const hlq_heads *v, int dt,
