@@ -358,7 +358,8 @@ __device__ __forceinline__ void keys_body(const Attn& p, const Maps& maps, uint3
         for (int i = 0; i < C::kN / 32; ++i)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float x = k == 0 ? fminf(3e38f, fmaxf(-3e38f, -v[0][i] * back)) : -v[1][i];
+            float x = k == 0 ? -v[0][i] * back : -v[1][i];
+            if (k == 0) x = x > 3e38f ? 3e38f : x < -3e38f ? -3e38f : x;  // NaN stays NaN
             const float hi = __bfloat162float(__float2bfloat16_rn(x));
             const float mid = __bfloat162float(__float2bfloat16_rn(x - hi));
             *reinterpret_cast<uint2*>(stats + (2 * u + k) * C::kMoreN + more_at(32 * i + lane)) =
