@@ -674,7 +674,7 @@ __device__ __forceinline__ void queries_body(const Attn& p, const Maps& maps, ui
       __syncwarp();
     } else if (warp == 2) {
       if (rest) {
-        if (wait(&bar.k_last, 0)) {
+        if (wait_warp(abort_flag, p.status, [&] { return mbar_test(&bar.k_last, 0); }, n)) {
           clear_rows<C::kChunks, C::kN>(sk + ((n - 1) % C::kStagesK) * C::kOther, rest);
           if (lane == 0) mbar_arrive(&bar.k_clear);
         }

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(FwdCfg<DP, kQ>::kThreads, FwdCfg<DP, kQ>::kCta
     } else if (warp == 2) {
       if (rest) {
         const int s = (n - 1) % C::kStages;
-        if (wait(&bar.v_last, 0)) {
+        if (wait_warp(abort_flag, p.status, [&] { return mbar_test(&bar.v_last, 0); }, n)) {
           clear_rows<C::kChunks>(sv + s * C::kTile, rest);
           if (lane == 0) mbar_arrive(&bar.v_clear);
         }

@@ -82,11 +82,12 @@ __device__ __forceinline__ bool elect_one() {
 // time and the abort flag are looked at every 64th try only (reading the timer
 // takes long enough to be missed on every wait).
 __device__ __forceinline__ bool gives_up(uint32_t& t0, volatile int* abort_flag,
-                                         unsigned int* status) {
+                                         unsigned int* status, int steps = 1) {
   if (*abort_flag) return true;
   const uint32_t t = (uint32_t)(now_ns() >> 16);  // in 32 bits: one register less in each wait
   if (t0 == 0) t0 = t;
-  if (t - t0 <= (uint32_t)(kWaitNs >> 16)) return false;
+  const unsigned long long limit = (kWaitNs >> 16) * steps;
+  if (t - t0 <= (uint32_t)(limit < 1u << 31 ? limit : 1u << 31)) return false;
   if (atomicExch((int*)abort_flag, 1) == 0) atomicOr(status, HLQ_DEV_TIMEOUT);
   return true;
 }
@@ -99,13 +100,15 @@ __device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t phase, volatile 
   return true;
 }
 // By a whole warp: one lane may see the phase where another would give up, so the
-// lanes vote on both, and the result is the warp's.
+// lanes vote on both, and the result is the warp's.  `steps`: what is waited for
+// comes after so many steps of the CTA's, each of which has the limit (where one of
+// them takes longer, the warp that waits for it gives up, and all others with it).
 template <typename F>
 __device__ __forceinline__ bool wait_warp(volatile int* abort_flag, unsigned int* status,
-                                          F&& test) {
+                                          F&& test, int steps = 1) {
   uint32_t t0 = 0;
   for (int i = 1; !__all_sync(0xffffffffu, test()); ++i)
-    if (i % 64 == 0 && __any_sync(0xffffffffu, gives_up(t0, abort_flag, status))) return false;
+    if (i % 64 == 0 && __any_sync(0xffffffffu, gives_up(t0, abort_flag, status, steps))) return false;
   return true;
 }
 

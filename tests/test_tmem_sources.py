@@ -42,7 +42,7 @@ def test_a_warp_votes_on_a_wait(name):
     warp = warp[:warp.index("\n}")]
     assert "while" not in warp and "!__all_sync(0xffffffffu, test())" in warp
     assert re.findall(r"return ([^;]*);", warp) == ["false", "true"]
-    assert "__any_sync(0xffffffffu, gives_up(t0, abort_flag, status))) return false;" in warp
+    assert "__any_sync(0xffffffffu, gives_up(t0, abort_flag, status, steps))) return false;" in warp
     text = code(name)
     kernels = len(re.findall(r"AttnTile t;", text))
     assert text.count("return wait_warp(abort_flag, p.status, [&] { return mbar_test(b, phase & 1); });") == kernels
