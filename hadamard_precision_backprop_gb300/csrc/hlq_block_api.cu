@@ -28,8 +28,13 @@ bool heads_strides_ok(const hlq_heads& x, int64_t T, int64_t H, int64_t D, bool 
   const int64_t t = T > 1 ? x.token_stride : 0, h = H > 1 ? x.head_stride : 0;
   if (t < 0 || h < 0 || t > kMaxStride || h > kMaxStride) return false;
   if (input) return true;
-  const bool by_token = (H <= 1 || h >= D) && (T <= 1 || t >= (H - 1) * h + D);
-  const bool by_head = (T <= 1 || t >= D) && (H <= 1 || h >= (T - 1) * t + D);
+  // n - 1 steps of `inner` and one element row fit a step of `outer` (no product: it
+  // may leave 64 bits)
+  const auto fits = [&](int64_t outer, int64_t n, int64_t inner) {
+    return outer >= D && (n <= 1 || n - 1 <= (outer - D) / inner);
+  };
+  const bool by_token = (H <= 1 || h >= D) && (T <= 1 || fits(t, H, h));
+  const bool by_head = (T <= 1 || t >= D) && (H <= 1 || fits(h, T, t));
   return by_token || by_head;
 }
 

@@ -15,3 +15,22 @@ def test_lengths_whose_tiles_leave_32_bits(L, call):  # noqa: F811
     T = 2 ** 31 - 1024
     assert call(L, Tq=T, Hq=1, Hk=1, D=8, batch=1, scale=0.0) == 1
     assert call(L, Tk=T, Hq=1, Hk=1, D=8, batch=1, scale=0.0) == 1
+
+
+@pytest.mark.parametrize("call,out", [(attention, "out"), (backward, "g_q")])
+def test_output_strides_whose_product_leaves_64_bits(L, call, out):  # noqa: F811
+    """2^24 heads 2^40 apart are 2^64 elements of a token, and not the few (less than none) that the low
+    bits of the product say: with tokens 8 apart they overlap.  Tokens and heads the other way round alike."""
+    for T, H, token, head in ((2, 2 ** 24, 8, 2 ** 40), (2 ** 24, 2, 2 ** 40, 8)):
+        assert call(L, Tq=T, Tk=T, Hq=H, Hk=1, D=64, batch=1, **{out: heads(token=token, head=head)}) == 2
+
+
+@pytest.mark.parametrize("call,out", [(attention, "out"), (backward, "g_q")])
+def test_output_strides_at_their_limits(L, call, out):  # noqa: F811
+    """One step less overlaps; exactly enough is taken (refused here for a later argument)."""
+    for T, H, token, head in ((2, 4, 3 * 70 + 64, 70), (5, 3, 70, 4 * 70 + 64), (2, 1, 64, 0), (1, 2, 0, 64)):
+        late = dict(lse=None)
+        args = dict(Tq=T, Tk=T, Hq=H, Hk=1, D=64, batch=1, **late)
+        assert call(L, **args, **{out: heads(token=token, head=head)}) == 1
+        less = heads(token=token - 1, head=head) if token > head else heads(token=token, head=head - 1)
+        assert call(L, **args, **{out: less}) == 2
