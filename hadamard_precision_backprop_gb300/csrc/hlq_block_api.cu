@@ -159,6 +159,10 @@ hlq_status hlq_attention_backward(const hlq_heads* g_out, int gout_dt, const hlq
                                   void* stream) {
   if (!dtype_ok(dt) || !dtype_ok(gout_dt) || !dtype_ok(g_dt)) return HLQ_ERR_INVALID_ARG;
   HLQ_NEED(check_sizes(Tq, Tk, Hq, Hk, D, batch));
+  // the CTAs of both sides are one grid: tiles of 32 rows at least, and one that may
+  // stay empty for each sequence, and for the rows outside them
+  if ((Tq / 32 + batch + 2) * Hq + (Tk / 32 + batch + 2) * Hk >= kMaxRows)
+    return HLQ_ERR_UNSUPPORTED;
   HLQ_NEED(check_seqs(Tq, Tk, batch, d_seqs, d_seqs_k, scale));
   HLQ_NEED(check_heads(g_out, gout_dt, Tq, Hq, D, true));
   HLQ_NEED(check_heads(q, dt, Tq, Hq, D, true));

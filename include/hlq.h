@@ -718,6 +718,7 @@ hlq_status hlq_attention(const hlq_heads *q, const hlq_heads *k, const hlq_heads
  * (also where the gradients are fp32), and p and ds are unless g_out is fp32 (then
  * they enter as two bf16 numbers each, 16 bits); all sums are fp32.
  * Infinities and NaN in a sequence may reach all its gradients, and no others.
+ * Sizes as above, and (Tq / 32 + batch + 2) Hq + (Tk / 32 + batch + 2) Hk < 2^31.
  * Workspace: hlq_attention_backward_workspace_bytes.
  */
 hlq_status hlq_attention_backward(const hlq_heads *g_out, int gout_dt, const hlq_heads *q,

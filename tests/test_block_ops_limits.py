@@ -2,7 +2,7 @@
 host (no device needed)."""
 import pytest
 
-from tests.test_block_ops import L, attention, backward, heads  # noqa: F401
+from tests.test_block_ops import FAKE, L, attention, backward, heads  # noqa: F401
 
 
 @pytest.mark.parametrize("call", [attention, backward])
@@ -34,3 +34,14 @@ def test_output_strides_at_their_limits(L, call, out):  # noqa: F811
         assert call(L, **args, **{out: heads(token=token, head=head)}) == 1
         less = heads(token=token - 1, head=head) if token > head else heads(token=token, head=head - 1)
         assert call(L, **args, **{out: less}) == 2
+
+
+def test_backward_passes_of_more_ctas_than_a_grid(L):  # noqa: F811
+    """Both sides' CTAs are one grid, of less than 2^31: a size like any other, not a failed launch."""
+    B = 2 ** 29
+    for kw in (dict(batch=B, Hq=1, Hk=1, Tq=64, Tk=64, seqs=FAKE), dict(batch=1, Hq=2 ** 29 - 1, Hk=2 ** 29 - 1, Tq=1, Tk=1, seqs=FAKE),
+               dict(batch=2 ** 30 - 2, Hq=1, Hk=1, Tq=64, Tk=64, seqs=FAKE)):
+        n = (kw["Tq"] // 32 + kw["batch"] + 2) * kw["Hq"] + (kw["Tk"] // 32 + kw["batch"] + 2) * kw["Hk"]
+        late = dict(scale=0.0)                          # is looked at after the sizes
+        assert backward(L, D=8, **kw, **late) == (4 if n >= 2 ** 31 else 1)
+        assert attention(L, D=8, **kw, **late) == 1     # its own grid is half of that
