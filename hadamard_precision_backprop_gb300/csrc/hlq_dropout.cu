@@ -34,6 +34,12 @@ __device__ __forceinline__ uint32_t half_of(const U4& w, int k) {
   return k & 1 ? word >> 16 : word & 0xffffu;
 }
 
+// Without a residual nothing is added: -0 + 0 would be 0.
+template <bool kResidual>
+__device__ __forceinline__ float scaled(float x, float scale, float other) {
+  return kResidual ? fmaf(x, scale, other) : x * scale;
+}
+
 template <int kPlace, bool kX, bool kY, bool kResidual>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p) {
   pdl_trigger();
@@ -68,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float other = kResidual ? r[i].v[k] : 0.f;
-        y.v[k] = half_of(w, k) >= p.drop ? fmaf(x[i].v[k], p.scale, other) : other;
+        y.v[k] = half_of(w, k) >= p.drop ? scaled<kResidual>(x[i].v[k], p.scale, other) : other;
       }
       store8(p.y, kY, row * p.ldy + col, y);
     } else {
@@ -79,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p) {
         const float other = kResidual ? load_elem(p.residual, kY, t * p.ldr + c) : 0.f;
         store_elem(p.y, kY, t * p.ldy + c,
                    half_of(w, k) >= p.drop
-                       ? fmaf(load_elem(p.x, kX, t * p.ldx + c), p.scale, other)
+                       ? scaled<kResidual>(load_elem(p.x, kX, t * p.ldx + c), p.scale, other)
                        : other);
         if (++c == p.C && kPlace != kDense) c = 0, ++t;
       }
