@@ -692,7 +692,7 @@ typedef struct {
  * D <= 128 and q, k and v begin on 16-byte boundaries with strides of whole 16
  * bytes; the probabilities are then rounded to bf16 for their product with v.
  * Maxima, sums and out are held in fp32 and out is rounded once.
- * Any other alignment or D: products in fp32, slower.
+ * Any other alignment or D: products in fp32 on CUDA cores, 20 to 90 times slower.
  * D <= 256; Tq, Tk <= 2^31 - 1024; Tq Hq, Tk Hk < 2^31; (batch + 1) Hq < 2^30;
  * scale from 2^-64 to 2^64.
  * No output may overlap an input.
