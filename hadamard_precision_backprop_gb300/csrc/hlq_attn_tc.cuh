@@ -95,7 +95,7 @@ __device__ __forceinline__ bool gives_up(uint32_t& t0, volatile int* abort_flag,
 __device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t phase, volatile int* abort_flag,
                                           unsigned int* status) {
   uint32_t t0 = 0;
-  for (int i = 1; !mbar_test(b, phase & 1); ++i)
+  for (uint32_t i = 1; !mbar_test(b, phase & 1); ++i)
     if (i % 64 == 0 && gives_up(t0, abort_flag, status)) return false;
   return true;
 }
@@ -107,7 +107,7 @@ template <typename F>
 __device__ __forceinline__ bool wait_warp(volatile int* abort_flag, unsigned int* status,
                                           F&& test, int steps = 1) {
   uint32_t t0 = 0;
-  for (int i = 1; !__all_sync(0xffffffffu, test()); ++i)
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, test()); ++i)
     if (i % 64 == 0 && __any_sync(0xffffffffu, gives_up(t0, abort_flag, status, steps))) return false;
   return true;
 }
